@@ -36,6 +36,10 @@ EP_MAX_EXPERTS = 4096
 # ep_layout_path_t
 LAYOUT_PATHS = {"auto": 0, "multi": 1, "single": 2}
 
+# ep_score_t, ep_act_t
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTS = {"none": 0, "swiglu": 1}
+
 # every entry point declared in include/ep.h
 EXPORTED = ("ep_status_string", "ep_workspace_bytes", "ep_get_dispatch_layout",
             "ep_layout_single_launch_fits", "ep_layout_auto_single_launch",
@@ -48,7 +52,9 @@ EXPORTED = ("ep_status_string", "ep_workspace_bytes", "ep_get_dispatch_layout",
             "ep_layout_dispatch_fused_fits", "ep_layout_dispatch_fused",
             "ep_layout_dispatch_fused_workspace_bytes", "ep_debug_set_fused_stall",
             "ep_shard_workspace_bytes", "ep_shard_layout", "ep_shard_offsets",
-            "ep_shard_recv_tokens_per_expert", "ep_debug_e4m3_range")
+            "ep_shard_recv_tokens_per_expert", "ep_debug_e4m3_range",
+            "ep_route", "ep_route_backward", "ep_combine_backward", "ep_ll_combine_backward",
+            "ep_ll_experts_w4")
 
 # 64-bit words of a combine's scheduling counters (EP_COMBINE_SCHED_WORDS)
 COMBINE_SCHED_WORDS = 2
@@ -116,6 +122,15 @@ def load(path: str | None = None) -> C.CDLL:
     L.ep_shard_layout.argtypes = [P, i64, i32, i32, i32, P, P, P, P, P, P, P, sz, P]
     L.ep_shard_offsets.argtypes = [P, i32, i32, P, P]
     L.ep_shard_recv_tokens_per_expert.argtypes = [P, i32, i32, i32, P]
+    f32 = C.c_float
+    L.ep_route.argtypes = [P, i32, i64, P, i64, i32, i32, i32, i32, i32, i32, f32, P, P, P]
+    L.ep_route_backward.argtypes = [P, P, i32, i64, P, i64, i32, i32, i32, i32, f32, P, P, P]
+    L.ep_combine_backward.argtypes = [P, P, i32, i64, P, P, i64, i32, i32, i32, P, P, P, P, P]
+    L.ep_ll_combine_backward.argtypes = [P, P, i32, i64, P, i64, i32, P, P, P, P, P]
+    L.ep_ll_experts_w4.argtypes = [P, i32, P, i32, P, i32, i64, P, P, P, i32, i32, i32, P, P, P]
+    for name in ("ep_route", "ep_route_backward", "ep_combine_backward",
+                 "ep_ll_combine_backward", "ep_ll_experts_w4"):
+        getattr(L, name).restype = i32
     for name in ("ep_get_dispatch_layout", "ep_get_dispatch_layout_path",
                  "ep_layout_total_rows", "ep_dispatch", "ep_combine",
                  "ep_ll_get_dispatch_layout", "ep_ll_get_dispatch_layout_path",
@@ -670,3 +685,224 @@ def debug_e4m3_range(first: int, out: torch.Tensor) -> None:
     _need(out, "out", torch.uint8)
     _check(lib().ep_debug_e4m3_range(int(first), out.numel(), _ptr(out), _stream(out.device)),
            "ep_debug_e4m3_range")
+
+
+# --------------------------------------------------------------------------
+# the router and its gradient
+# --------------------------------------------------------------------------
+def _need_logits(logits: torch.Tensor) -> int:
+    """Checks router logits (rows may be strided); returns the row stride."""
+    if not logits.is_cuda:
+        raise EPError("logits must be a CUDA tensor")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise EPError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise EPError("logits must be [num_tokens, num_experts]")
+    T, E = logits.shape
+    if E > 1 and logits.stride(1) != 1:
+        raise EPError("logits must be contiguous along the experts")
+    stride = logits.stride(0) if T > 1 else E
+    if stride < E:
+        raise EPError("the rows of logits must not overlap")
+    return stride
+
+
+def _enum(table: dict, value: str, name: str) -> int:
+    if value not in table:
+        raise EPError(f"{name} must be one of {sorted(table)}")
+    return table[value]
+
+
+def route(logits: torch.Tensor, num_topk: int, *, score: str = "softmax",
+          bias: torch.Tensor | None = None, num_groups: int = 1, topk_groups: int = 1,
+          renormalize: bool = True, scale: float = 1.0,
+          out: tuple[torch.Tensor, torch.Tensor] | None = None
+          ) -> tuple[torch.Tensor, torch.Tensor]:
+    """Router: the top-k experts of every token and their weights, (topk_idx
+    [T, K] int64, topk_weights [T, K] float32), from logits [T, E] (float32 or
+    bfloat16).  score: "softmax" or "sigmoid"; bias [E] steers the choice and
+    stays out of the weights; num_groups / topk_groups restrict it to the best
+    groups of consecutive experts.  Ties go to the lowest index; experts at
+    -inf or NaN are never chosen.  Enqueued on the current stream."""
+    stride = _need_logits(logits)
+    T, E = logits.shape
+    K = int(num_topk)
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,))
+    if out is None:
+        out = (torch.empty((T, K), dtype=torch.int64, device=logits.device),
+               torch.empty((T, K), dtype=torch.float32, device=logits.device))
+    else:
+        _need(out[0], "out[0]", torch.int64, (T, K))
+        _need(out[1], "out[1]", torch.float32, (T, K))
+    _check(lib().ep_route(_ptr(logits), int(logits.dtype == torch.bfloat16), stride, _ptr(bias), T,
+                          E, K, _enum(SCORES, score, "score"), int(num_groups), int(topk_groups),
+                          int(renormalize), float(scale), _ptr(out[0]), _ptr(out[1]),
+                          _stream(logits.device)), "ep_route")
+    _debug_check("route", None, logits.device)
+    return out
+
+
+def route_backward(dweights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor, *,
+                   score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                   err: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of route's weights with respect to the logits, [T, E] of the
+    logits' type, at the choice topk_idx.  Enqueued on the current stream."""
+    stride = _need_logits(logits)
+    T, E = logits.shape
+    if topk_idx.dim() != 2:
+        raise EPError("topk_idx must be [num_tokens, num_topk]")
+    K = topk_idx.shape[1]
+    _need(topk_idx, "topk_idx", torch.int64, (T, K))
+    _need(dweights, "dweights", torch.float32, (T, K))
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _need(out, "out", logits.dtype, (T, E))
+    if err is not None:
+        _need(err, "err", torch.int32)
+    _check(lib().ep_route_backward(_ptr(dweights), _ptr(logits),
+                                   int(logits.dtype == torch.bfloat16), stride, _ptr(topk_idx), T,
+                                   E, K, _enum(SCORES, score, "score"), int(renormalize),
+                                   float(scale), _ptr(out), _ptr(err), _stream(logits.device)),
+           "ep_route_backward")
+    _debug_check("route_backward", err, logits.device)
+    return out
+
+
+# --------------------------------------------------------------------------
+# the gradient of the combine
+# --------------------------------------------------------------------------
+def _grad_outputs(dout, y, T, K, out):
+    _need(dout, "dout", torch.bfloat16)
+    _need(y, "y", torch.bfloat16)
+    if dout.dim() != 2 or y.dim() != 2 or y.shape[1] != dout.shape[1]:
+        raise EPError("dout must be [num_tokens, hidden] and y [rows, hidden]")
+    if dout.shape[0] != T:
+        raise EPError(f"dout must have {T} rows, got {dout.shape[0]}")
+    if out is None:  # rows that no slot names get no gradient
+        out = torch.zeros_like(y)
+    _need(out, "out", torch.bfloat16, y.shape)
+    return out, torch.empty((T, K), dtype=torch.float32, device=y.device)
+
+
+def combine_backward(dout: torch.Tensor, y: torch.Tensor, topk_idx: torch.Tensor,
+                     topk_weights: torch.Tensor, layout: Layout, *,
+                     err: torch.Tensor | None = None, out: torch.Tensor | None = None
+                     ) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradient of combine(y, topk_idx, topk_weights, layout) for the gradient
+    dout [T, H] of its output: (dy like y, dweights [T, K] float32).  Rows of
+    dy that no slot names keep what `out` holds (zeros without `out`).
+    Enqueued on the current stream."""
+    if topk_idx.dim() != 2:
+        raise EPError("topk_idx must be [num_tokens, num_topk]")
+    T, K = topk_idx.shape
+    dy, dw = _grad_outputs(dout, y, T, K, out)
+    _need(topk_idx, "topk_idx", torch.int64, (T, K))
+    _need(topk_weights, "topk_weights", torch.float32, (T, K))
+    R, E = layout.num_ranks, layout.num_experts
+    _need(layout.slot, "slot", torch.int32, (T, R))
+    if err is not None:
+        _need(err, "err", torch.int32)
+    _check(lib().ep_combine_backward(_ptr(dout), _ptr(y), y.shape[1], y.shape[0], _ptr(topk_idx),
+                                     _ptr(topk_weights), T, K, E, R, _ptr(layout.slot), _ptr(dy),
+                                     _ptr(dw), _ptr(err), _stream(y.device)),
+           "ep_combine_backward")
+    _debug_check("combine_backward", err, y.device)
+    return dy, dw
+
+
+def ll_combine_backward(dout: torch.Tensor, y: torch.Tensor, topk_weights: torch.Tensor,
+                        layout: LLLayout, *, err: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradient of ll_combine(y, topk_weights, layout): (dy like y, dweights
+    [T, K] float32), as combine_backward.  Enqueued on the current stream."""
+    T, K = layout.ll_slot.shape
+    dy, dw = _grad_outputs(dout, y, T, K, out)
+    _need(layout.ll_slot, "ll_slot", torch.int32, (T, K))
+    _need(topk_weights, "topk_weights", torch.float32, (T, K))
+    if err is not None:
+        _need(err, "err", torch.int32)
+    _check(lib().ep_ll_combine_backward(_ptr(dout), _ptr(y), y.shape[1], y.shape[0],
+                                        _ptr(topk_weights), T, K, _ptr(layout.ll_slot), _ptr(dy),
+                                        _ptr(dw), _ptr(err), _stream(y.device)),
+           "ep_ll_combine_backward")
+    _debug_check("ll_combine_backward", err, y.device)
+    return dy, dw
+
+
+# --------------------------------------------------------------------------
+# the experts' products with 4-bit weights
+# --------------------------------------------------------------------------
+@dataclass
+class W4Weights:
+    """4-bit weights of E experts: W[e][n][i] = (q - zero) * scale, one scale
+    and zero point per group of consecutive input channels."""
+    q: torch.Tensor             # [E, N', I / 2] uint8, channel 2j low half, 2j + 1 high half of byte j
+    scales: torch.Tensor        # [E, N', I / group] bfloat16
+    zeros: torch.Tensor | None = None  # [E, N', I / group] uint8 in [0, 16); None: 8 everywhere
+
+
+def quantize_w4(weight: torch.Tensor, group_size: int = 128, *,
+                zero_points: bool = False) -> W4Weights:
+    """Rounds weights [E, N', I] to W4Weights, on the weights' device (set-up
+    work in torch, once per model).  Without zero points the scale maps a
+    group's largest magnitude to 7; with them, its range to [0, 15]."""
+    if weight.dim() != 3 or weight.shape[2] % group_size or group_size not in (32, 64, 128):
+        raise EPError("weight must be [E, N, I] with I a multiple of group_size (32, 64 or 128)")
+    E, N, I = weight.shape
+    w = weight.float().reshape(E, N, I // group_size, group_size)
+    if zero_points:
+        lo, hi = w.amin(-1).clamp(max=0.0), w.amax(-1).clamp(min=0.0)
+        scales = ((hi - lo) / 15.0).clamp(min=1e-8).to(torch.bfloat16)
+        zero = torch.round(-lo / scales.float()).clamp(0, 15)
+    else:
+        scales = (w.abs().amax(-1) / 7.0).clamp(min=1e-8).to(torch.bfloat16)
+        zero = torch.full_like(scales, 8.0, dtype=torch.float32)
+    q = (torch.round(w / scales.float()[..., None]) + zero[..., None]).clamp(0, 15)
+    q = q.to(torch.uint8).reshape(E, N, I // 2, 2)
+    return W4Weights((q[..., 0] | (q[..., 1] << 4)).contiguous(), scales,
+                     zero.to(torch.uint8) if zero_points else None)
+
+
+def ll_experts_w4(x: torch.Tensor, weights: W4Weights, layout: LLLayout, *,
+                  x_scales: torch.Tensor | None = None, act: str = "none",
+                  err: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """Every expert's product with its rows of the expert-major layout: x
+    [E * cap, I] bfloat16, or E4M3 codes (uint8) with x_scales [E * cap, I /
+    128] as ll_dispatch leaves them; returns [E * cap, N] bfloat16.  act
+    "swiglu": the weights' first N rows are the gate's, the next N the up
+    projection's.  Rows beyond an expert's count keep what `out` holds
+    (nothing defined without `out`).  Enqueued on the current stream."""
+    E, cap = layout.num_experts, layout.expert_capacity
+    fp8 = x_scales is not None
+    a = _enum(ACTS, act, "act")
+    _need(weights.q, "weights.q", torch.uint8)
+    _need(weights.scales, "weights.scales", torch.bfloat16)
+    if weights.q.dim() != 3 or weights.scales.dim() != 3 or weights.q.shape[0] != E:
+        raise EPError(f"weights.q must be [{E}, N, I / 2] and weights.scales [{E}, N, I / group]")
+    rows, I = weights.q.shape[1], 2 * weights.q.shape[2]
+    groups = weights.scales.shape[2]
+    if tuple(weights.scales.shape[:2]) != (E, rows) or groups == 0 or I % groups:
+        raise EPError("weights.scales must have one value per group of input channels")
+    if weights.zeros is not None:
+        _need(weights.zeros, "weights.zeros", torch.uint8, weights.scales.shape)
+    if a and rows % 2:
+        raise EPError("swiglu weights have 2 N rows")
+    N = rows // 2 if a else rows
+    _need(x, "x", torch.uint8 if fp8 else torch.bfloat16, (E * cap, I))
+    if fp8:
+        _need(x_scales, "x_scales", torch.float32, (E * cap, I // 128))
+    _need(layout.ll_count, "ll_count", torch.int32, (E,))
+    if out is None:
+        out = torch.empty((E * cap, N), dtype=torch.bfloat16, device=x.device)
+    _need(out, "out", torch.bfloat16, (E * cap, N))
+    if err is not None:
+        _need(err, "err", torch.int32)
+    _check(lib().ep_ll_experts_w4(_ptr(x), int(fp8), _ptr(x_scales), I, _ptr(layout.ll_count), E,
+                                  cap, _ptr(weights.q), _ptr(weights.scales), _ptr(weights.zeros),
+                                  I // groups, N, a, _ptr(out), _ptr(err), _stream(x.device)),
+           "ep_ll_experts_w4")
+    _debug_check("ll_experts_w4", err, x.device)
+    return out

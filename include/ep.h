@@ -567,6 +567,131 @@ void ep_debug_set_combine_stall(int unit);
  */
 ep_status_t ep_debug_e4m3_range(uint32_t first, int64_t n, uint8_t* out, ep_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The router: from logits to the topk_idx / topk_weights that the layouts,
+ * the dispatch and the combine take, and its gradient.  (The pages start
+ * from a finished topk_idx; these entry points have no counterpart there.)
+ *
+ * For token t with logits l[e], e < E:
+ *   score  softmax: s[e] = exp(l[e] - max l) / sum exp(l - max l)
+ *          sigmoid: s[e] = 1 / (1 + exp(-l[e]))
+ *   key    c[e] = s[e] + bias[e] (bias: a balance term that steers the choice
+ *          and stays out of the weights); without a bias c = s for sigmoid
+ *          scores and c = l for softmax scores (the same order, no rounding)
+ *   groups E/num_groups consecutive experts each; the topk_groups groups with
+ *          the largest group scores are kept.  A group's score is the sum of
+ *          its two largest keys (sigmoid) or its largest key (softmax).
+ *   choice the num_topk largest keys of the kept groups, in descending order
+ *   weight u_k = s[e_k]; renormalize: w_k = scale * u_k / sum_j u_j (0 where
+ *          the sum is 0), else w_k = scale * u_k.  Renormalised softmax
+ *          weights are computed as the softmax over the chosen logits.
+ * Ties, of experts and of groups, go to the lowest index.  An expert whose
+ * logit is -inf or NaN is never chosen and counts nowhere, also not in its
+ * group's score (a group with none left scores -inf); a slot for which no
+ * expert is left gets idx -1 and weight 0, the masked slot of every other
+ * call.  If the largest softmax logit is +inf, the experts at +inf share the
+ * mass equally.  All arithmetic is float32.
+ * ------------------------------------------------------------------------ */
+typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score_t;
+
+/*
+ * In (device): logits [T, E], float32 or (logits_bf16 != 0) bfloat16, rows
+ *   row_stride elements apart (>= E), any alignment of the element type; bias
+ *   [E] float32 (nullable).
+ * score: an ep_score_t.  1 <= num_topk <= min(E, EP_MAX_TOPK); num_groups
+ *   divides E, 1 <= topk_groups <= num_groups; 1 and 1: no groups.
+ * Out (device), every element written: topk_idx [T, K] int64, topk_weights
+ *   [T, K] float32.
+ */
+ep_status_t ep_route(const void* logits, int logits_bf16, int64_t row_stride, const float* bias,
+                     int64_t num_tokens, int num_experts, int num_topk, int score, int num_groups,
+                     int topk_groups, int renormalize, float scale, int64_t* topk_idx,
+                     float* topk_weights, ep_stream_t stream);
+
+/*
+ * The gradient of the weights w of ep_route with respect to the logits, at a
+ * fixed choice topk_idx (a choice has no gradient, so neither has the bias).
+ * With du_k = scale * (dw_k - sum_j dw_j u_j / S) / S, S = sum_j u_j
+ * (renormalize; 0 where S is 0) or du_k = scale * dw_k:
+ *   sigmoid: dl[e] = sum_{k: e_k = e} du_k * u_k (1 - u_k), 0 elsewhere
+ *   softmax: dl[e] = s[e] * (sum_{k: e_k = e} du_k - sum_j u_j du_j); with
+ *            renormalised weights this is w'_k (scale dw_k - sum_j w'_j scale
+ *            dw_j) on the chosen experts, w' = softmax over the chosen
+ *            logits, and 0 elsewhere.
+ * In (device): dweights [T, K] float32, logits as in ep_route, topk_idx
+ *   [T, K] int64 (-1: masked; an id outside [-1, E) is taken as masked and
+ *   sets EP_ERRBIT_BAD_EXPERT; an expert named twice sums its slots, k
+ *   ascending).  A chosen expert whose logit is -inf or NaN gets 0.
+ * Out (device): dlogits [T, E] contiguous, of the logits' type, every element
+ *   written (rounded once from float32).  dlogits and logits must not overlap.
+ */
+ep_status_t ep_route_backward(const float* dweights, const void* logits, int logits_bf16,
+                              int64_t row_stride, const int64_t* topk_idx, int64_t num_tokens,
+                              int num_experts, int num_topk, int score, int renormalize,
+                              float scale, void* dlogits, int32_t* err_word, ep_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The gradient of the combine.  (That of the dispatch is the combine itself:
+ * the unweighted rank sum for the rank-major layout, ep_ll_combine with NULL
+ * weights for the expert-major one.)
+ * For every row that token t's slots name:
+ *   dy[row]          = bf16_rne( W * float(dout[t]) ), W = the sum, k
+ *                      ascending, of the weights w[t][k] of the slots that
+ *                      name the row (one slot in the expert-major layout,
+ *                      every slot of that rank in the rank-major one)
+ *   dweights[t][k]   = sum_h float(dout[t][h]) * float(y[row][h])   (float32;
+ *                      0 for a masked slot)
+ * In (device): dout [T, H] bf16; y [num_rows, H] bf16, topk_idx, topk_weights
+ *   (required here) and slot as in ep_combine / ep_ll_combine.
+ * Out (device): dy [num_rows, H] bf16: rows that no slot names are not
+ *   touched; dweights [T, K] float32, every element written.  Either may be
+ *   NULL (skipped; y may be NULL when dweights is).  dy must overlap neither
+ *   y nor dout.
+ * A row >= num_rows is skipped (its dweights are 0) and sets
+ * EP_ERRBIT_CAPACITY; an id outside [-1, E) sets EP_ERRBIT_BAD_EXPERT.
+ * ------------------------------------------------------------------------ */
+ep_status_t ep_combine_backward(const void* dout, const void* y, int hidden, int64_t num_rows,
+                                const int64_t* topk_idx, const float* topk_weights,
+                                int64_t num_tokens, int num_topk, int num_experts, int num_ranks,
+                                const int32_t* slot, void* dy, float* dweights, int32_t* err_word,
+                                ep_stream_t stream);
+ep_status_t ep_ll_combine_backward(const void* dout, const void* y, int hidden, int64_t num_rows,
+                                   const float* topk_weights, int64_t num_tokens, int num_topk,
+                                   const int32_t* ll_slot, void* dy, float* dweights,
+                                   int32_t* err_word, ep_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' products with 4-bit weights, on the rows of the expert-major
+ * layout (serving: quantised weights have no gradient).
+ *
+ * Expert e's rows are x[e*cap .. e*cap + n_e), n_e = min(ll_count[e], cap).
+ * Its weights are W_e [N', I] with N' = N (act EP_ACT_NONE) or 2N
+ * (EP_ACT_SWIGLU: rows [0, N) are the gate's, rows [N, 2N) the up
+ * projection's), held as 4-bit codes q in [0, 16) with one scale and one
+ * zero point per group of group_size consecutive input channels:
+ *   W_e[n][i] = (q[e][n][i] - zero[e][n][i / group_size]) * scale[e][n][i / group_size]
+ *   p[n]      = sum_i W_e[n][i] * x[row][i]                       (float32)
+ *   none:   y[row][n] = bf16_rne(p[n])
+ *   swiglu: y[row][n] = bf16_rne(p[n] / (1 + exp(-p[n])) * p[N + n])
+ * In (device): x [E*cap, I] bf16, or (x_fp8 != 0) E4M3 codes with x_scales
+ *   [E*cap, I/128] float32, as ep_ll_dispatch leaves them; ll_count [E] int32;
+ *   q [E, N', I/2] bytes, channel i in the low (i even) or high (i odd) half of
+ *   byte i/2; scales [E, N', I/group_size] bf16; zeros of the same shape, one
+ *   byte each in [0, 16) (nullable: every zero point is 8).
+ * group_size 32, 64 or 128, dividing I; x_fp8: I % 128 == 0; N % 8 == 0.
+ * Out (device): y [E*cap, N] bf16; rows at or beyond n_e are not touched.
+ * Rounding: E4M3 codes, and 4-bit codes less their zero point, are exact in
+ * bf16.  Scales that do not span a whole matrix step are multiplied into the
+ * weight and rounded to bf16 once; the sums are float32 throughout.
+ * ------------------------------------------------------------------------ */
+typedef enum { EP_ACT_NONE = 0, EP_ACT_SWIGLU = 1 } ep_act_t;
+
+ep_status_t ep_ll_experts_w4(const void* x, int x_fp8, const float* x_scales, int in_channels,
+                             const int32_t* ll_count, int num_experts, int64_t expert_capacity,
+                             const uint8_t* q, const void* scales, const uint8_t* zeros,
+                             int group_size, int out_channels, int act, void* y,
+                             int32_t* err_word, ep_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
