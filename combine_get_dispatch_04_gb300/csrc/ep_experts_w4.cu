@@ -10,11 +10,10 @@
 // each, and unpacks them in registers.  Nothing passes through shared memory
 // but the final sum.  A step of the product is 128 channels, which the warps
 // of a block divide among themselves.
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "ep_common.cuh"
+#include "ep_experts_w4.cuh"
 
 namespace ep {
 namespace {
@@ -23,23 +22,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMT = 2;  // 16-row weight tiles per warp (swiglu: one of the gate, one of up)
 constexpr unsigned kFull = 0xFFFFFFFFu;
-
-struct Args {
-  const uint8_t* x;  // bf16 or E4M3 rows
-  const float* x_scales;
-  int I;  // input channels
-  const int32_t* count;
-  int E;
-  int64_t cap;
-  const uint8_t* q;
-  const __nv_bfloat16* scales;
-  const uint8_t* zeros;
-  int N;         // output channels
-  int rows;      // weight rows per expert (N or 2 N)
-  int tiles;     // tiles of output channels per expert
-  int ksplit;    // warps that share one tile (a power of two)
-  __nv_bfloat16* y;
-};
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -122,7 +104,7 @@ __device__ __forceinline__ void load_row(const uint8_t* p, bool live, uint32_t (
 // kGroup: 128 (a scale spans a step: it multiplies the float32 sum of the
 // step), else 64 or 32 (it multiplies the weights, rounded to bf16 once).
 template <int NT, bool kFP8, bool kSwiglu, int kGroup>
-__global__ void __launch_bounds__(kThreads) experts_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads) experts_kernel(ExpertsArgs a, int ks) {
   pdl_wait_then_release();
   extern __shared__ float red[];  // [warp][16 * kMT][kPitch], then the live experts
   __shared__ int warp_total[kWarps];
@@ -138,7 +120,8 @@ __global__ void __launch_bounds__(kThreads) experts_kernel(Args a) {
   __syncthreads();
   for (int e0 = 0; e0 < a.E; e0 += kThreads) {
     const int e = e0 + tid;
-    const bool busy = e < a.E && a.count[e] > 0;
+    const int64_t n = e < a.E ? min((int64_t)a.count[e], a.cap) : 0;
+    const bool busy = n > 0 && n <= kFewRows;
     const unsigned bal = __ballot_sync(kFull, busy);
     if (lane == 0) warp_total[warp] = __popc(bal);
     __syncthreads();
@@ -150,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) experts_kernel(Args a) {
     __syncthreads();
   }
   const int64_t items = (int64_t)live_total * a.tiles;
-  const int ks = a.ksplit, kw = warp % ks, mw = warp / ks;
+  const int kw = warp % ks, mw = warp / ks;
   const int steps = (a.I + 127) / 128;
   const int mrows = kSwiglu ? 16 : 16 * kMT;  // output channels per warp
   constexpr int kBytes = kFP8 ? 1 : 2;
@@ -287,31 +270,31 @@ __global__ void __launch_bounds__(kThreads) experts_kernel(Args a) {
 }
 
 template <int NT, bool kFP8, bool kSwiglu, int kGroup>
-ep_status_t launch_small(Args a, cudaStream_t st) {
+ep_status_t launch_small(ExpertsArgs a, cudaStream_t st) {
   DeviceProps props;
   if (!device_props(&props)) return EP_ERR_CUDA;
   const int steps = (a.I + 127) / 128;
-  a.ksplit = kWarps;
-  while (a.ksplit > 1 && a.ksplit > steps) a.ksplit /= 2;
-  const int outs = (kWarps / a.ksplit) * (kSwiglu ? 16 : 16 * kMT);
+  int ks = kWarps;  // warps that share one tile
+  while (ks > 1 && ks > steps) ks /= 2;
+  const int outs = (kWarps / ks) * (kSwiglu ? 16 : 16 * kMT);
   a.tiles = (a.N + outs - 1) / outs;
   const size_t smem = (size_t)kWarps * 16 * kMT * (8 * NT + 1) * 4 + (size_t)a.E * 2;
   static_assert(kWarps * 16 * kMT * 33 * 4 + EP_MAX_EXPERTS * 2 <= 48 * 1024, "shared memory");
   const int64_t most = (int64_t)a.E * a.tiles;
   const unsigned grid = (unsigned)(most < 2 * props.sm_count ? most : 2 * props.sm_count);
-  launch_pdl(experts_kernel<NT, kFP8, kSwiglu, kGroup>, grid, kThreads, smem, st, a);
+  launch_pdl(experts_kernel<NT, kFP8, kSwiglu, kGroup>, grid, kThreads, smem, st, a, ks);
   return launch_status();
 }
 
 template <bool kFP8, bool kSwiglu, int kGroup>
-ep_status_t launch_rows(const Args& a, cudaStream_t st) {
+ep_status_t launch_rows(const ExpertsArgs& a, cudaStream_t st) {
   if (a.cap <= 8) return launch_small<1, kFP8, kSwiglu, kGroup>(a, st);
   if (a.cap <= 16) return launch_small<2, kFP8, kSwiglu, kGroup>(a, st);
   return launch_small<4, kFP8, kSwiglu, kGroup>(a, st);
 }
 
 template <bool kFP8, bool kSwiglu>
-ep_status_t launch_group(const Args& a, int group, cudaStream_t st) {
+ep_status_t launch_group(const ExpertsArgs& a, int group, cudaStream_t st) {
   if (group == 32) return launch_rows<kFP8, kSwiglu, 32>(a, st);
   if (group == 64) return launch_rows<kFP8, kSwiglu, 64>(a, st);
   return launch_rows<kFP8, kSwiglu, 128>(a, st);
@@ -328,7 +311,6 @@ extern "C" ep_status_t ep_ll_experts_w4(const void* x, int x_fp8, const float* x
                                         const void* scales, const uint8_t* zeros, int group_size,
                                         int out_channels, int act, void* y, int32_t* err_word,
                                         ep_stream_t stream) {
-  (void)err_word;
   if (num_experts < 1 || num_experts > EP_MAX_EXPERTS || expert_capacity < 0 ||
       expert_capacity * (int64_t)num_experts >= (int64_t(1) << 31))
     return EP_ERR_INVALID_ARG;
@@ -337,12 +319,15 @@ extern "C" ep_status_t ep_ll_experts_w4(const void* x, int x_fp8, const float* x
     return EP_ERR_INVALID_ARG;
   if (out_channels < 8 || out_channels % 8 || out_channels > (1 << 28)) return EP_ERR_INVALID_ARG;
   if (act != EP_ACT_NONE && act != EP_ACT_SWIGLU) return EP_ERR_INVALID_ARG;
+  const bool swiglu = act == EP_ACT_SWIGLU;
+  if ((int64_t)num_experts * out_channels * (swiglu ? 2 : 1) >= (int64_t(1) << 31))
+    return EP_ERR_INVALID_ARG;
   if (expert_capacity == 0) return EP_OK;
   if (!x || !ll_count || !q || !scales || !y || (x_fp8 && !x_scales)) return EP_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(x_scales) || !aligned16(q) || !aligned16(scales) ||
       !aligned16(zeros) || !aligned16(y) || !aligned16(ll_count))
     return EP_ERR_INVALID_ARG;
-  Args a = {};
+  ExpertsArgs a = {};
   a.x = static_cast<const uint8_t*>(x);
   a.x_scales = x_scales;
   a.I = in_channels;
@@ -353,13 +338,16 @@ extern "C" ep_status_t ep_ll_experts_w4(const void* x, int x_fp8, const float* x
   a.scales = static_cast<const __nv_bfloat16*>(scales);
   a.zeros = zeros;
   a.N = out_channels;
-  a.rows = act == EP_ACT_SWIGLU ? 2 * out_channels : out_channels;
+  a.rows = swiglu ? 2 * out_channels : out_channels;
   a.y = static_cast<__nv_bfloat16*>(y);
+  a.err = err_word;
   cudaStream_t st = to_cuda(stream);
-  const bool swiglu = act == EP_ACT_SWIGLU;
+  ep_status_t s;
   if (x_fp8)
-    return swiglu ? launch_group<true, true>(a, group_size, st)
-                  : launch_group<true, false>(a, group_size, st);
-  return swiglu ? launch_group<false, true>(a, group_size, st)
-                : launch_group<false, false>(a, group_size, st);
+    s = swiglu ? launch_group<true, true>(a, group_size, st)
+               : launch_group<true, false>(a, group_size, st);
+  else
+    s = swiglu ? launch_group<false, true>(a, group_size, st)
+               : launch_group<false, false>(a, group_size, st);
+  return s == EP_OK ? launch_experts_many(a, x_fp8 != 0, swiglu, group_size, st) : s;
 }

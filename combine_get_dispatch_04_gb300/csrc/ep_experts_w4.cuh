@@ -1,0 +1,40 @@
+// ep_experts_w4.cuh -- what the two kernels of the experts' products with
+// 4-bit weights share: the arguments and the split between them.
+//
+// An expert with at most kFewRows rows is bound by reading its weights and
+// goes to the register kernel (ep_experts_w4.cu); one with more goes to the
+// tcgen05 kernel (ep_experts_w4_tc.cu).  The counts are on the device, so
+// each kernel skips the other's experts.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "ep_common.cuh"
+
+namespace ep {
+
+constexpr int kFewRows = 32;
+
+struct ExpertsArgs {
+  const uint8_t* x;  // bf16 or E4M3 rows
+  const float* x_scales;
+  int I;  // input channels
+  const int32_t* count;
+  int E;
+  int64_t cap;
+  const uint8_t* q;
+  const __nv_bfloat16* scales;
+  const uint8_t* zeros;
+  int N;      // output channels
+  int rows;   // weight rows per expert (N, or 2 N for swiglu)
+  int tiles;  // tiles of output channels per expert
+  __nv_bfloat16* y;
+  int32_t* err;
+};
+
+// Experts with more than kFewRows rows (nothing is launched if the capacity
+// rules them out).
+ep_status_t launch_experts_many(const ExpertsArgs& a, bool fp8, bool swiglu, int group,
+                                cudaStream_t st);
+
+}  // namespace ep
