@@ -10,14 +10,18 @@
 // rows are multiplied as they are, at the 8-bit rate.
 //
 // A block takes 128 weight rows (swiglu: 64 of the gate and the same 64 of
-// the up projection) times up to 256 rows of x, as two halves of up to 128
-// rows, so that one half's sums are read while the other's are computed:
-//   warp 0      TMA of the x tiles (128 channels x the rows, swizzled 128 B)
-//   warp 1      tensor memory, and the tcgen05.mma of both halves
-//   warp 2      TMA of the weight codes (128 rows x 64 bytes)
-//   warp 3      the scales of E4M3 rows, into shared memory
-//   warps 4-7   codes -> integers -> operand A in tensor memory
-//   warps 8-15  sums of a half -> scaled -> registers; the epilogue
+// the up projection) times up to 192 (E4M3: 160) rows of x, with two buffers of sums in
+// tensor memory (2 x 192 columns; the last 128 columns hold A), so that one
+// group's sums are read while the next group is multiplied:
+//   warp 0       TMA of the x tiles (128 channels x the rows, swizzled 128 B)
+//   warp 1       tensor memory, and the tcgen05.mma
+//   warp 2       TMA of the weight codes (128 rows x 64 bytes)
+//   warp 3       group scales, zero points and scales of E4M3 rows, by
+//                4-byte asynchronous copies into shared memory
+//   warps 4-11   codes -> integers -> operand A; each four of them take
+//                every other step of 128 channels
+//   warps 12-19  sums -> scaled -> registers, each four of them for half of
+//                the rows; the epilogue
 // Every wait is bounded; a block whose wait runs out reports
 // EP_ERRBIT_TIMEOUT and leaves.
 #include <cuda.h>
@@ -27,61 +31,78 @@
 namespace ep {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kRows = 256;      // rows of x per block, two halves
-constexpr int kHalf = 128;
-constexpr int kBoxRows = 32;    // rows per TMA box of x
-constexpr int kSlotsA = 4;      // operand A slots of 128 channels in tensor memory
-constexpr int kSlotsS = 8;      // slots of row scales
+constexpr int kTeams = 2;  // teams of four warps that unpack codes, a step each in turn
+constexpr int kParts = 2;  // teams of four warps that add up sums, a part of the rows each
+constexpr int kThreads = 128 * (1 + kTeams + kParts);
+constexpr int kLaunchRegs = 96;  // per thread: what the register split draws on
+constexpr int kBoxes = 6;  // x is loaded in boxes of 32, 64, ... 192 rows
 constexpr int kWBytes = 8192;   // 128 weight rows x 64 bytes
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
-template <bool kFP8>
+// A step is 128 channels: one stage of x, one of codes, one slot of A, and
+// one slot of scales.
+template <bool kFP8, int kGroup>
 struct Cfg {
-  static constexpr int kXBytes = kRows * (kFP8 ? 128 : 256);  // a stage of 128 channels
-  static constexpr int kStagesX = kFP8 ? 4 : 3;
-  static constexpr int kStagesW = kFP8 ? 10 : 3;
+  // rows of x per block: what the accumulators of two teams hold in registers
+  // without moves (E4M3 rows need registers for their scales as well)
+  static constexpr int kRows = kFP8 ? 160 : 192;
+  static constexpr int kPart = kRows / kParts;
+  static constexpr int kXBytes = kRows * (kFP8 ? 128 : 256);
+  static constexpr int kStagesX = kFP8 ? 5 : 3;
+  static constexpr int kStagesW = kFP8 ? 8 : 6;
   static constexpr int kColsA = kFP8 ? 32 : 64;  // tensor-memory columns per slot of A
+  static constexpr int kSlotsA = 128 / kColsA;
+  static constexpr int kPerStep = 128 / kGroup;  // groups in a step
+  static constexpr int kSlotsS = kGroup == 128 ? 8 : 4;
+  // words of a slot of scales: per group 128 scale words and 128 zero-point
+  // words, then the rows' scales
+  static constexpr int kSWords = kPerStep * 256 + (kFP8 ? kRows : 0);
   static constexpr int kSmem =
-      1024 + kStagesX * kXBytes + kStagesW * kWBytes + (kFP8 ? kSlotsS * kRows * 4 : 0);
+      1024 + kStagesX * kXBytes + kStagesW * kWBytes + kSlotsS * kSWords * 4;
+};
+
+// One tensor map per height of a box, so that a step of x is one copy (two
+// for bf16) whatever the number of rows.
+struct XMaps {
+  CUtensorMap rows[kBoxes];  // [i]: 32 * (i + 1) rows
 };
 
 struct Barriers {
-  uint64_t xfull[4], xempty[4], wfull[10], wempty[10], afull[kSlotsA], aempty[kSlotsA], pfull[2],
-      pempty[2], sfull[kSlotsS], sempty[kSlotsS];
+  // full: a step's x and A are in place; done: its products are finished
+  uint64_t full[5], done[5], wfull[9], wempty[9], sfull[8], sempty[8], pfull[2], pempty[2];
 };
 
 // --- the items of a block ----------------------------------------------------
 struct Item {
-  int e, tile, r0, rows, nh;  // nh: rows of a half, a multiple of 16
+  int e, tile, r0, rows, np;  // np: rows of a part, a multiple of 16
 };
 
 // Walks the experts with more than kFewRows rows; item numbers run over the
 // experts, their chunks of rows, and the tiles of channels, tiles innermost.
+// 32 bits hold them: an item is at least 64 channels of 2-byte results for
+// more than kFewRows rows, so 2^31 of them would not fit the GPU's memory.
 struct Walk {
-  const int32_t* count;
-  int64_t cap;
-  int E, tiles;
-  int e = -1, n = 0, chunks = 0;
-  int64_t base = 0, items = 0;
+  int e = -1, n = 0, chunks = 0, base = 0, items = 0;
 
-  __device__ Walk(const ExpertsArgs& a) : count(a.count), cap(a.cap), E(a.E), tiles(a.tiles) {}
-
-  __device__ bool at(int64_t item, Item* it) {
+  template <int kRows>
+  __device__ bool at(const ExpertsArgs& a, int item, Item* it) {
     while (item >= base + items) {
       base += items;
-      if (++e >= E) return false;
-      n = (int)min((int64_t)__ldg(count + e), cap);
+      if (++e >= a.E) {
+        --e;
+        items = 0;
+        return false;
+      }
+      n = min(__ldg(a.count + e), (int)a.cap);
       chunks = n > kFewRows ? (n + kRows - 1) / kRows : 0;
-      items = (int64_t)chunks * tiles;
+      items = chunks * a.tiles;
     }
-    const int local = (int)(item - base);
-    const int chunk = local / tiles, size = (n + chunks - 1) / chunks;
+    const int local = item - base, chunk = local / a.tiles, size = (n + chunks - 1) / chunks;
     it->e = e;
-    it->tile = local - chunk * tiles;
+    it->tile = local - chunk * a.tiles;
     it->r0 = chunk * size;
     it->rows = min(size, n - it->r0);
-    it->nh = max(16, ((it->rows + 1) / 2 + 15) / 16 * 16);
+    it->np = (it->rows + 31) / 32 * (32 / kParts);
     return true;
   }
 };
@@ -96,6 +117,13 @@ __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x,
       : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -134,50 +162,191 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+// The load and its wait in one statement, so that no use moves between them.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[14]), "=r"(r[15])
       : "r"(addr)
       : "memory");
 }
 
-// two float32 at once
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+// Waits for the phase of the barrier at `bar` (a shared address) with the
+// given parity; false if it has not completed after kTries tries.  A try
+// takes some tens of cycles, and the hardware may suspend it for up to a
+// microsecond: the limit is between a tenth of a second and a few seconds.
+// (Four instructions a try: the warps that wait share their schedulers with
+// those that work.)
+constexpr uint32_t kTries = 1u << 22;
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+  uint32_t left;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "mov.u32 %0, %3;\n"
+      "TRY:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %4;\n\t"
+      "@P bra DONE;\n\t"
+      "sub.u32 %0, %0, 1;\n\t"
+      "setp.ne.u32 P, %0, 0;\n\t"
+      "@P bra TRY;\n"
+      "DONE:\n\t}"
+      : "=&r"(left)
+      : "r"(bar), "r"(parity), "r"(kTries), "r"(1000u)
+      : "memory");
+  return left != 0;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+  return wait(smem_addr(bar), parity);
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
+__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t& a, uint64_t& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// 4-byte asynchronous copy; the barrier counts one arrival per thread when
+// its copies so far have landed.
+__device__ __forceinline__ void copy_word(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+// The word that holds the element at p.
+__device__ __forceinline__ const void* word_of(const void* p) {
+  return reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
+}
+
+// A ring of slots: the slot and the parity of its current round.
+template <int kSlots>
+struct Ring {
+  int slot = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kSlots) {
+      slot = 0;
+      round ^= 1;
+    }
+  }
+};
+
+// --- sums -> accumulators ---------------------------------------------------------
+// acc += v * scale, and acc += (v * x) * scale, for two rows at a time: half
+// the instructions of fmaf.  Volatile, so that they stay behind the loads.
+__device__ __forceinline__ void add2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t scale) {
+  asm volatile(
+      "{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(v0), "r"(v1), "l"(scale));
+}
+__device__ __forceinline__ void add2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t x,
+                                     uint64_t scale) {
+  asm volatile(
+      "{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tmul.rn.f32x2 t, t, %3;\n\t"
+      "fma.rn.f32x2 %0, t, %4, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(v0), "r"(v1), "l"(x), "l"(scale));
+}
+
 __device__ __forceinline__ float2 unpack2(uint64_t v) {
   float2 f;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
   return f;
 }
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t v;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-  return v;
+
+// What the loop over the groups of an item needs.
+struct SumArgs {
+  uint32_t sfull, sempty, pfull, pempty;  // barriers (shared addresses)
+  uint32_t scale, xs;                     // this lane's scale words, this part's row scales
+  uint32_t src;                           // this part's columns of sums
+  uint32_t odd;                           // whether the lane's first group is a word's high half
+  int groups;
+};
+
+// Adds up all groups of an item for 16 * kChunks rows; n and p count steps
+// and groups over the items.  One instance per number of chunks: a branch in
+// the inner loop costs as much as a chunk (measured 87 against 40 cycles for
+// a chunk of bf16 rows).
+template <bool kFP8, int kGroup, int kChunks>
+__device__ __forceinline__ bool add_groups(const SumArgs& s, int lane, uint32_t& n, uint32_t& p,
+                                           uint64_t (&acc)[Cfg<kFP8, kGroup>::kPart / 2]) {
+  using C = Cfg<kFP8, kGroup>;
+#pragma unroll 1
+  for (int g = 0; g < s.groups; ++g) {
+    const uint32_t slot = n % C::kSlotsS, buf = p & 1;
+    const uint32_t in = C::kPerStep == 1 ? 0 : g % C::kPerStep;
+    bool fine = true;
+    if (in == 0) fine = wait(s.sfull + slot * 8, n / C::kSlotsS & 1);
+    fine &= wait(s.pfull + buf * 8, p >> 1 & 1);
+    if (__any_sync(kFull, !fine)) return false;
+    fence_after();
+    // bf16 -> float32 is a shift; the word holds groups 2i and 2i + 1
+    const uint32_t word = lds32(s.scale + slot * C::kSWords * 4 + in * 1024);
+    const uint32_t sv = (s.odd + g) & 1 ? word & 0xFFFF0000u : word << 16;
+    uint64_t scale;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(scale) : "r"(sv));
+    const uint32_t src = s.src + buf * C::kRows, xs = s.xs + slot * C::kSWords * 4;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      uint32_t v[16];
+      tmem_ld16(src + c * 16, v);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        if (kFP8) {
+          uint64_t x0, x1;
+          lds_pairs(xs + c * 64 + i * 4, x0, x1);
+          add2(acc[c * 8 + i / 2], v[i], v[i + 1], x0, scale);
+          add2(acc[c * 8 + i / 2 + 1], v[i + 2], v[i + 3], x1, scale);
+        } else {
+          add2(acc[c * 8 + i / 2], v[i], v[i + 1], scale);
+          add2(acc[c * 8 + i / 2 + 1], v[i + 2], v[i + 3], scale);
+        }
+      }
+    }
+    fence_before();
+    __syncwarp();
+    ++p;
+    const bool last = C::kPerStep == 1 || in == C::kPerStep - 1 || g == s.groups - 1;
+    if (lane == 0) {
+      arrive(s.pempty + buf * 8);
+      if (last) arrive(s.sempty + slot * 8);
+    }
+    if (last) ++n;
+  }
+  return true;
 }
 
 // --- codes -> operand A ---------------------------------------------------------
@@ -193,14 +362,20 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t zp, uint32_t* ou
   }
 }
 
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+
 // Eight codes as E4M3 bytes, looked up in the 16 bytes of (q - zero).
 __device__ __forceinline__ void codes_e4m3(uint32_t w, const uint4& t, uint32_t* out) {
   const uint32_t idx = w & 0x77777777u, high = (w >> 3) & 0x11111111u;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t i = h ? idx >> 16 : idx, m = h ? high >> 16 : high;
-    const uint32_t lo = __byte_perm(t.x, t.y, i), hi = __byte_perm(t.z, t.w, i);
-    const uint32_t mask = __byte_perm(0x0000FF00u, 0, m);
+    const uint32_t lo = prmt(t.x, t.y, i), hi = prmt(t.z, t.w, i);
+    const uint32_t mask = prmt(0x0000FF00u, 0, m);
     out[h] = (lo & ~mask) | (hi & mask);
   }
 }
@@ -213,12 +388,28 @@ __device__ __forceinline__ uint32_t e4m3_of_int(int v) {
   return (uint32_t)((v < 0 ? 0x80 : 0) | (7 + p) << 3 | ((m << 3 >> p) & 7));
 }
 
+// Lane r of tensor memory (0..127) holds the weight row of this channel of the
+// tile; with swiglu, lanes 16..31 of each 32 hold the up projection's.
+template <bool kSwiglu>
+__device__ __forceinline__ int lane_channel(int r) {
+  return kSwiglu ? (r >> 5) * 16 + (r & 15) : r;
+}
+template <bool kSwiglu>
+__device__ __forceinline__ bool lane_is_up(int r) {
+  return kSwiglu && (r & 16);
+}
+template <bool kSwiglu>
+__device__ __forceinline__ int64_t lane_row(const ExpertsArgs& a, const Item& it, int r) {
+  const int c = min(it.tile * (kSwiglu ? 64 : 128) + lane_channel<kSwiglu>(r), a.N - 1);
+  return (int64_t)it.e * a.rows + c + (lane_is_up<kSwiglu>(r) ? a.N : 0);
+}
+
 template <bool kFP8, bool kSwiglu, int kGroup>
 __global__ void __launch_bounds__(kThreads, 1)
-    experts_tc_kernel(ExpertsArgs a, const __grid_constant__ CUtensorMap xmap,
+    experts_tc_kernel(ExpertsArgs a, const __grid_constant__ XMaps xmaps,
                       const __grid_constant__ CUtensorMap wmap) {
-  using C = Cfg<kFP8>;
-  constexpr int kPerBlock = 128 / kGroup;  // groups in a step of 128 channels
+  using C = Cfg<kFP8, kGroup>;
+  constexpr int kPerStep = C::kPerStep;
   constexpr int kMmaPerGroup = kGroup / (kFP8 ? 32 : 16);
   extern __shared__ uint8_t raw[];
   __shared__ Barriers bar;
@@ -230,14 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sx = base;
   uint8_t* sw = sx + C::kStagesX * C::kXBytes;
-  float* ss = reinterpret_cast<float*>(sw + C::kStagesW * kWBytes);
+  uint32_t* ss = reinterpret_cast<uint32_t*>(sw + C::kStagesW * kWBytes);
 
   if (tid == 0) {
-    for (int i = 0; i < C::kStagesX; ++i) mbar_init(&bar.xfull[i], 1), mbar_init(&bar.xempty[i], 1);
+    for (int i = 0; i < C::kStagesX; ++i) mbar_init(&bar.full[i], 5), mbar_init(&bar.done[i], 1);
     for (int i = 0; i < C::kStagesW; ++i) mbar_init(&bar.wfull[i], 1), mbar_init(&bar.wempty[i], 4);
-    for (int i = 0; i < kSlotsA; ++i) mbar_init(&bar.afull[i], 4), mbar_init(&bar.aempty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&bar.pfull[i], 1), mbar_init(&bar.pempty[i], 4);
-    for (int i = 0; i < kSlotsS; ++i) mbar_init(&bar.sfull[i], 1), mbar_init(&bar.sempty[i], 8);
+    for (int i = 0; i < C::kSlotsS; ++i) mbar_init(&bar.sfull[i], 32), mbar_init(&bar.sempty[i], 4 * kParts + 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.pfull[i], 1), mbar_init(&bar.pempty[i], 4 * kParts);
     fence_barrier_init();
     abort_flag = 0;
   }
@@ -259,286 +449,272 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_base;
-  const uint32_t tmem_a = tmem + 2 * kHalf;
-  volatile int* abort = &abort_flag;
+  const uint32_t tmem_a = tmem + 384;
+  const volatile int* abort = &abort_flag;
 
   pdl_wait_then_release();
 
-  const int blocks = (a.I + 127) / 128;  // steps of 128 channels
+  const int steps = (a.I + 127) / 128;
   const int groups = a.I / kGroup;
   const auto give_up = [&]() {
     abort_flag = 1;
     if (a.err) atomicOr(a.err, EP_ERRBIT_TIMEOUT);
   };
+  Walk walk;
+  Item it;
+  bool ok = true;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    Walk walk(a);
-    Item it;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {  // x tiles
-      uint32_t n = 0;
-      for (int64_t item = blockIdx.x; walk.at(item, &it) && !*abort; item += gridDim.x) {
-        const int row = (int)(it.e * a.cap) + it.r0, boxes = 2 * it.nh / kBoxRows;
-        const uint32_t bytes = (uint32_t)(2 * it.nh) * (kFP8 ? 128 : 256);
-        for (int b = 0; b < blocks; ++b, ++n) {
-          const int s = n % C::kStagesX;
-          if (!mbar_wait_bounded(&bar.xempty[s], (n / C::kStagesX & 1) ^ 1, abort)) {
-            give_up();
-            break;
-          }
-          mbar_arrive_expect_tx(&bar.xfull[s], bytes);
-          uint8_t* dst = sx + s * C::kXBytes;
-          for (int i = 0; i < boxes; ++i) {
-            if (kFP8) {
-              tma_2d(dst + i * kBoxRows * 128, &xmap, b * 128, row + i * kBoxRows, &bar.xfull[s]);
-            } else {
-              tma_2d(dst + i * kBoxRows * 128, &xmap, b * 128, row + i * kBoxRows, &bar.xfull[s]);
-              tma_2d(dst + kRows * 128 + i * kBoxRows * 128, &xmap, b * 128 + 64,
-                     row + i * kBoxRows, &bar.xfull[s]);
-            }
-          }
+      Ring<C::kStagesX> rx;
+      for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
+        const int row = (int)(it.e * a.cap) + it.r0;
+        const CUtensorMap* map = &xmaps.rows[it.np / (32 / kParts) - 1];
+        const uint32_t bytes = (uint32_t)(kParts * it.np) * (kFP8 ? 128 : 256);
+        for (int b = 0; b < steps; ++b) {
+          ok = wait(&bar.done[rx.slot], rx.round ^ 1);
+          if (!ok) break;
+          uint8_t* dst = sx + rx.slot * C::kXBytes;
+          mbar_arrive_expect_tx(&bar.full[rx.slot], bytes);
+          tma_2d(dst, map, b * 128, row, &bar.full[rx.slot]);
+          if (!kFP8) tma_2d(dst + C::kRows * 128, map, b * 128 + 64, row, &bar.full[rx.slot]);
+          rx.next();
         }
       }
-    } else if (warp == 1 && lane == 0) {  // products
+      if (!ok) give_up();
+    } else if (warp == 1) {  // products: the whole warp waits, one lane issues
       const uint32_t idesc0 = 1u << 4 | (kFP8 ? 0u : (1u << 7 | 1u << 10)) | (128u >> 4) << 24;
-      uint32_t n = 0, p = 0;  // steps, groups
-      bool ok = true;
-      for (int64_t item = blockIdx.x; ok && walk.at(item, &it) && !*abort; item += gridDim.x) {
-        const uint32_t idesc = idesc0 | (uint32_t)(it.nh >> 3) << 17;
-        for (int b = 0; ok && b < blocks; ++b, ++n) {
-          const int s = n % C::kStagesX, sa = n % kSlotsA;
-          ok = mbar_wait_bounded(&bar.xfull[s], n / C::kStagesX & 1, abort) &&
-               mbar_wait_bounded(&bar.afull[sa], n / kSlotsA & 1, abort);
-          const int here = min(kPerBlock, groups - b * kPerBlock);
-          for (int g = 0; ok && g < here; ++g, ++p) {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              ok = ok && mbar_wait_bounded(&bar.pempty[h], (p & 1) ^ 1, abort);
-              if (!ok) break;
-              fence_after();
+      const uint64_t desc0 = smem_desc(0);
+      Ring<C::kStagesX> rx;
+      Ring<C::kSlotsA> ra;
+      Ring<2> rp;
+      bool any = false;
+      for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
+        const uint32_t idesc = idesc0 | (uint32_t)(kParts * it.np >> 3) << 17;
+        for (int b = 0; ok && b < steps; ++b) {
+          ok = wait(&bar.full[rx.slot], rx.round);
+          const uint32_t x0 = smem_addr(sx + rx.slot * C::kXBytes);
+          const uint32_t a0 = tmem_a + ra.slot * C::kColsA;
+          const int here = kPerStep == 1 ? 1 : min(kPerStep, groups - b * kPerStep);
+          for (int g = 0; g < here; ++g) {
+            ok = ok && wait(&bar.pempty[rp.slot], rp.round ^ 1);
+            if (!__all_sync(kFull, ok)) {
+              ok = false;
+              break;
+            }
+            fence_after();
+            if (elect_one()) {
 #pragma unroll
               for (int j = 0; j < kMmaPerGroup; ++j) {
-                const int k = g * kMmaPerGroup + j;  // matrix step within the block
-                const uint32_t xa = smem_addr(sx + s * C::kXBytes) + (uint32_t)(h * it.nh) * 128 +
-                                    (kFP8 ? k * 32 : (k >> 2) * kRows * 128 + (k & 3) * 32);
-                mma<kFP8>(tmem + h * kHalf, tmem_a + sa * C::kColsA + k * 8, smem_desc(xa), idesc,
-                          j > 0);
+                const int k = g * kMmaPerGroup + j;  // matrix step within the step
+                const uint32_t off = kFP8 ? k * 32 : (k >> 2) * C::kRows * 128 + (k & 3) * 32;
+                mma<kFP8>(tmem + rp.slot * C::kRows, a0 + k * 8, desc0 | (uint64_t)((x0 + off) >> 4),
+                          idesc, j > 0);
               }
-              commit(&bar.pfull[h]);
+              commit(&bar.pfull[rp.slot]);
+              if (g == here - 1) commit(&bar.done[rx.slot]);
             }
+            __syncwarp();
+            rp.next();
           }
-          if (!ok) break;
-          commit(&bar.xempty[s]);
-          commit(&bar.aempty[sa]);
+          any = ok;
+          rx.next();
+          ra.next();
         }
       }
       // the last arrivals land before the block may leave
-      if (ok && n > 0)
-        ok = mbar_wait_bounded(&bar.aempty[(n - 1) % kSlotsA], (n - 1) / kSlotsA & 1, abort);
+      if (ok && any) {
+        const int last = (rx.slot + C::kStagesX - 1) % C::kStagesX;
+        ok = wait(&bar.done[last], rx.slot == 0 ? rx.round ^ 1 : rx.round);
+      }
       if (!ok) give_up();
     } else if (warp == 2 && lane == 0) {  // weight codes
-      uint32_t n = 0;
-      bool ok = true;
-      for (int64_t item = blockIdx.x; ok && walk.at(item, &it) && !*abort; item += gridDim.x) {
+      Ring<C::kStagesW> rw;
+      for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
         const int row0 = it.e * a.rows + it.tile * (kSwiglu ? 64 : 128);
-        const int row1 = row0 + (kSwiglu ? a.N : 64);
-        for (int b = 0; b < blocks; ++b, ++n) {
-          const int s = n % C::kStagesW;
-          ok = mbar_wait_bounded(&bar.wempty[s], (n / C::kStagesW & 1) ^ 1, abort);
+        for (int b = 0; b < steps; ++b) {
+          ok = wait(&bar.wempty[rw.slot], rw.round ^ 1);
           if (!ok) break;
-          mbar_arrive_expect_tx(&bar.wfull[s], kWBytes);
-          tma_2d(sw + s * kWBytes, &wmap, b * 64, row0, &bar.wfull[s]);
-          tma_2d(sw + s * kWBytes + 4096, &wmap, b * 64, row1, &bar.wfull[s]);
+          uint8_t* dst = sw + rw.slot * kWBytes;
+          mbar_arrive_expect_tx(&bar.wfull[rw.slot], kWBytes);
+          tma_2d(dst, &wmap, b * 64, row0, &bar.wfull[rw.slot]);
+          tma_2d(dst + 4096, &wmap, b * 64, row0 + (kSwiglu ? a.N : 64), &bar.wfull[rw.slot]);
+          rw.next();
         }
       }
       if (!ok) give_up();
-    } else if (kFP8 && warp == 3) {  // row scales
-      uint32_t n = 0;
-      bool ok = true;
-      for (int64_t item = blockIdx.x; ok && walk.at(item, &it) && !*abort; item += gridDim.x) {
-        const float* src = a.x_scales + ((int64_t)it.e * a.cap + it.r0) * blocks;
-        int off[8];
-        float now[8], next[8];
+    } else if (warp == 3) {  // scales and zero points
+      Ring<C::kSlotsS> rs;
+      for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
+        const float* xs = kFP8 ? a.x_scales + ((int64_t)it.e * a.cap + it.r0) * steps : nullptr;
+        int64_t at[4];  // this lane's four weight rows: their first group
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          off[i] = min(lane + 32 * i, it.rows - 1) * blocks;
-          now[i] = __ldg(src + off[i]);
-          next[i] = __ldg(src + off[i] + min(1, blocks - 1));
-        }
-        for (int b = 0; b < blocks; ++b, ++n) {
-          const int s = n % kSlotsS;
-          float later[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) later[i] = __ldg(src + off[i] + min(b + 2, blocks - 1));
-          ok = mbar_wait_bounded(&bar.sempty[s], (n / kSlotsS & 1) ^ 1, abort);
+        for (int i = 0; i < 4; ++i) at[i] = lane_row<kSwiglu>(a, it, lane + 32 * i) * groups;
+        for (int b = 0; b < steps; ++b) {
+          ok = wait(&bar.sempty[rs.slot], rs.round ^ 1);
           if (!__all_sync(kFull, ok)) {
             ok = false;
             break;
           }
+          uint32_t* dst = ss + rs.slot * C::kSWords;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            ss[s * kRows + lane + 32 * i] = now[i];
-            now[i] = next[i];
-            next[i] = later[i];
+          for (int g = 0; g < kPerStep; ++g) {
+            const int gi = kPerStep == 1 ? b : min(b * kPerStep + g, groups - 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              copy_word(dst + g * 256 + lane + 32 * i, word_of(a.scales + at[i] + gi));
+              if (a.zeros)
+                copy_word(dst + g * 256 + 128 + lane + 32 * i, word_of(a.zeros + at[i] + gi));
+            }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.sfull[s]);
+          if (kFP8) {
+#pragma unroll
+            for (int i = 0; i < C::kRows / 32; ++i) {
+              const int r = lane + 32 * i;
+              if (r < kParts * it.np)
+                copy_word(dst + kPerStep * 256 + r, xs + min(r, it.rows - 1) * steps + b);
+            }
+          }
+          copies_arrive(&bar.sfull[rs.slot]);
+          rs.next();
         }
       }
       if (!ok) give_up();
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
-  } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    // codes -> operand A; this thread's weight row is tensor-memory lane
-    // 32 * (warp % 4) + lane
-    const int quad = warp & 3;
-    const int ch = kSwiglu ? quad * 16 + (lane & 15) : quad * 32 + lane;
-    const int srow = kSwiglu ? ch + (lane >= 16 ? 64 : 0) : ch;
-    const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
-    Walk walk(a);
-    Item it;
-    uint32_t n = 0;
-    bool ok = true;
-    for (int64_t item = blockIdx.x; ok && walk.at(item, &it) && !*abort; item += gridDim.x) {
-      const int c = min(it.tile * (kSwiglu ? 64 : 128) + ch, a.N - 1);
-      const int64_t wrow = (int64_t)it.e * a.rows + c + (kSwiglu && lane >= 16 ? a.N : 0);
-      const uint8_t* zrow = a.zeros ? a.zeros + wrow * groups : nullptr;
-      for (int b = 0; b < blocks; ++b, ++n) {
-        uint32_t z[kPerBlock];
-#pragma unroll
-        for (int g = 0; g < kPerBlock; ++g)
-          z[g] = zrow ? (uint32_t)__ldg(zrow + min(b * kPerBlock + g, groups - 1)) : 8u;
-        const int s = n % C::kStagesW, sa = n % kSlotsA;
-        ok = mbar_wait_bounded(&bar.wfull[s], n / C::kStagesW & 1, abort);
-        ok = ok && mbar_wait_bounded(&bar.aempty[sa], (n / kSlotsA & 1) ^ 1, abort);
-        if (!__all_sync(kFull, ok)) {
-          ok = false;
-          break;
-        }
-        fence_after();
-        const uint4* src = reinterpret_cast<const uint4*>(sw + s * kWBytes + srow * 64);
-        const int swz = (srow >> 1) & 3;
-        if (kFP8) {
-          uint32_t r[32];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 w = src[i ^ swz];
-            const uint4 t = tables[z[i * kPerBlock / 4] & 15];
-            codes_e4m3(w.x, t, r + 8 * i);
-            codes_e4m3(w.y, t, r + 8 * i + 2);
-            codes_e4m3(w.z, t, r + 8 * i + 4);
-            codes_e4m3(w.w, t, r + 8 * i + 6);
+  } else if (warp < 4 + 4 * kTeams) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // codes -> operand A: this thread's weight row is lane 32 * quad + lane of
+    // tensor memory
+    const int team = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const int srow = lane_channel<kSwiglu>(r) + (lane_is_up<kSwiglu>(r) ? 64 : 0);
+    const uint32_t swz = (uint32_t)((srow >> 1) & 3) << 4;
+    const uint32_t row_addr = smem_addr(sw) + srow * 64;
+    const uint32_t zero_addr = smem_addr(ss) + (128 + r) * 4;
+    const uint32_t table_addr = smem_addr(tables);
+    const uint32_t a_addr = tmem_a + ((uint32_t)(quad * 32) << 16);
+    Ring<C::kStagesX> rx;  // the stage of this step, and of the one that used its slot of A
+    Ring<C::kStagesX> rd;
+    Ring<C::kStagesW> rw;
+    uint32_t n = 0;  // steps
+    for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
+      const int at4 = (int)(lane_row<kSwiglu>(a, it, r) * groups & 3);
+      for (int b = 0; b < steps; ++b, ++n) {
+        if (n % kTeams == (uint32_t)team) {
+          const uint32_t ss_slot = n % C::kSlotsS;
+          bool fine = wait(&bar.wfull[rw.slot], rw.round);
+          fine &= wait(&bar.sfull[ss_slot], n / C::kSlotsS & 1);
+          if (n >= C::kSlotsA) fine &= wait(&bar.done[rd.slot], rd.round);
+          if (__any_sync(kFull, !fine)) {
+            ok = false;
+            break;
           }
-          tmem_st32(tmem_a + sa * C::kColsA + lane_addr, r);
-        } else {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t r[32];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int chunk = half * 2 + i;
-              const uint4 w = src[chunk ^ swz];
-              const uint32_t zp = 0x43004300u | z[chunk * kPerBlock / 4] * 0x00010001u;
-              codes_bf16(w.x, zp, r + 16 * i);
-              codes_bf16(w.y, zp, r + 16 * i + 4);
-              codes_bf16(w.z, zp, r + 16 * i + 8);
-              codes_bf16(w.w, zp, r + 16 * i + 12);
+          fence_after();
+          const uint32_t src = row_addr + rw.slot * kWBytes;
+          const uint32_t dst = a_addr + n % C::kSlotsA * C::kColsA;
+          uint32_t zero = 8;
+#pragma unroll(kFP8 ? 4 : 2)
+          for (int i = 0; i < 4; ++i) {  // 32 channels
+            const uint4 w = lds128(src + (i << 4 ^ swz));
+            if (i % (4 / kPerStep) == 0 && a.zeros) {  // the next group's zero point
+              const int g = i * kPerStep / 4;
+              const int gi = at4 + min(b * kPerStep + g, groups - 1);
+              zero = lds32(zero_addr + ss_slot * C::kSWords * 4 + g * 1024) >> (8 * (gi & 3)) & 15;
             }
-            tmem_st32(tmem_a + sa * C::kColsA + half * 32 + lane_addr, r);
+            if (kFP8) {
+              const uint4 t = lds128(table_addr + zero * 16);
+              uint32_t v[8];
+              codes_e4m3(w.x, t, v);
+              codes_e4m3(w.y, t, v + 2);
+              codes_e4m3(w.z, t, v + 4);
+              codes_e4m3(w.w, t, v + 6);
+              tmem_st8(dst + i * 8, v);
+            } else {
+              const uint32_t zp = 0x43004300u | zero * 0x00010001u;
+              uint32_t v[16];
+              codes_bf16(w.x, zp, v);
+              codes_bf16(w.y, zp, v + 4);
+              codes_bf16(w.z, zp, v + 8);
+              codes_bf16(w.w, zp, v + 12);
+              tmem_st16(dst + i * 16, v);
+            }
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bar.full[rx.slot]);
+            mbar_arrive(&bar.wempty[rw.slot]);
+            mbar_arrive(&bar.sempty[ss_slot]);
           }
         }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar.wempty[s]);
-          mbar_arrive(&bar.afull[sa]);
-        }
+        rx.next();
+        rw.next();
+        if (n >= C::kSlotsA) rd.next();
       }
     }
     if (!ok) give_up();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    const int h = (warp - 8) >> 2, quad = warp & 3;
-    const int ch = kSwiglu ? quad * 16 + (lane & 15) : quad * 32 + lane;
-    const uint32_t part = tmem + h * kHalf + ((uint32_t)(quad * 32) << 16);
-    Walk walk(a);
-    Item it;
-    uint32_t n = 0, p = 0;
-    bool ok = true;
-    for (int64_t item = blockIdx.x; ok && walk.at(item, &it) && !*abort; item += gridDim.x) {
-      const int n0 = it.tile * (kSwiglu ? 64 : 128) + ch;
-      const int64_t wrow =
-          (int64_t)it.e * a.rows + min(n0, a.N - 1) + (kSwiglu && lane >= 16 ? a.N : 0);
-      const __nv_bfloat16* srow = a.scales + wrow * groups;
-      uint64_t acc[kHalf / 2];
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    const int h = (warp - 4 - 4 * kTeams) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    SumArgs sum;
+    sum.sfull = smem_addr(bar.sfull);
+    sum.sempty = smem_addr(bar.sempty);
+    sum.pfull = smem_addr(bar.pfull);
+    sum.pempty = smem_addr(bar.pempty);
+    sum.scale = smem_addr(ss) + r * 4;
+    sum.groups = groups;
+    uint32_t n = 0, p = 0;  // steps and groups
+    for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
+      sum.odd = (uint32_t)(lane_row<kSwiglu>(a, it, r) * groups & 1);
+      sum.src = tmem + ((uint32_t)(quad * 32) << 16) + h * it.np;
+      sum.xs = smem_addr(ss) + (kPerStep * 256 + h * it.np) * 4;
+      uint64_t acc[C::kPart / 2];
 #pragma unroll
-      for (int i = 0; i < kHalf / 2; ++i) acc[i] = 0;
-      __nv_bfloat16 s0 = srow[0], s1 = srow[min(1, groups - 1)];
-      for (int g = 0; g < groups; ++g, ++p) {
-        const __nv_bfloat16 s2 = srow[min(g + 2, groups - 1)];
-        const uint32_t sv = __float_as_uint(__bfloat162float(s0));
-        const uint64_t scale = pack2(sv, sv);
-        const int slot = n % kSlotsS;
-        ok = mbar_wait_bounded(&bar.pfull[h], p & 1, abort);
-        if (kFP8 && g % kPerBlock == 0)
-          ok = ok && mbar_wait_bounded(&bar.sfull[slot], n / kSlotsS & 1, abort);
-        if (!__all_sync(kFull, ok)) {
-          ok = false;
-          break;
-        }
-        fence_after();
-        const float* xs = ss + slot * kRows + h * it.nh;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c * 32 < it.nh) {
-            uint32_t r[32];
-            tmem_ld32(part + c * 32, r);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              uint64_t v = pack2(r[2 * i], r[2 * i + 1]);
-              if (kFP8) v = mul2(v, *reinterpret_cast<const uint64_t*>(xs + c * 32 + 2 * i));
-              fma2(acc[c * 16 + i], v, scale);
-            }
-          }
-        }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.pempty[h]);
-        if (g % kPerBlock == kPerBlock - 1 || g == groups - 1) {
-          if (kFP8 && lane == 0) mbar_arrive(&bar.sempty[slot]);
-          ++n;
-        }
-        s0 = s1;
-        s1 = s2;
+      for (int i = 0; i < C::kPart / 2; ++i) acc[i] = 0;
+      switch (it.np / 16) {
+        case 1: ok = add_groups<kFP8, kGroup, 1>(sum, lane, n, p, acc); break;
+        case 2: ok = add_groups<kFP8, kGroup, 2>(sum, lane, n, p, acc); break;
+        case 3: ok = add_groups<kFP8, kGroup, 3>(sum, lane, n, p, acc); break;
+        case 4: ok = add_groups<kFP8, kGroup, 4>(sum, lane, n, p, acc); break;
+        case 5: ok = add_groups<kFP8, kGroup, 5>(sum, lane, n, p, acc); break;
+        default: ok = add_groups<kFP8, kGroup, C::kPart / 16>(sum, lane, n, p, acc); break;
       }
       if (!ok) break;
-      const int left = it.rows - h * it.nh;  // live rows of this half
-      __nv_bfloat16* y = a.y + ((int64_t)it.e * a.cap + it.r0 + h * it.nh) * a.N + n0;
-      if (kSwiglu) {
+      const int n0 = it.tile * (kSwiglu ? 64 : 128) + lane_channel<kSwiglu>(r);
+      const int left = min(it.rows - h * it.np, it.np);  // live rows of this part
+      __nv_bfloat16* dst =
+          a.y + ((int64_t)it.e * a.cap + it.r0 + h * it.np + (kSwiglu ? lane >> 4 : 0)) * a.N + n0;
+      if (n0 >= a.N) {
+        // a channel beyond the last tile's end
+      } else if (kSwiglu) {
         // lanes 0-15 hold the gate, 16-31 the up projection of the same
         // channels: the lower lanes finish the first row of each pair, the
         // upper ones the second
+        const unsigned in = __activemask();
 #pragma unroll
-        for (int i = 0; i < kHalf / 2; ++i) {
+        for (int i = 0; i < C::kPart / 2; ++i) {
+          if (2 * i >= left) break;
           const float2 v = unpack2(acc[i]);
-          const float other = __shfl_xor_sync(kFull, lane < 16 ? v.y : v.x, 16);
+          const float other = __shfl_xor_sync(in, lane < 16 ? v.y : v.x, 16);
           const float gate = lane < 16 ? v.x : other, up = lane < 16 ? other : v.y;
-          const int r = 2 * i + (lane >> 4);
-          if (r < left && r < it.nh && n0 < a.N)
-            y[(int64_t)r * a.N] = __float2bfloat16_rn(gate / (1.0f + expf(-gate)) * up);
+          // a few units in the last place of float32, rounded to bf16 next
+          const float out = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+          if (2 * i + (lane >> 4) < left) *dst = __float2bfloat16_rn(out);
+          dst += 2 * a.N;
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < kHalf / 2; ++i) {
+        for (int i = 0; i < C::kPart / 2; ++i) {
+          if (2 * i >= left) break;
           const float2 v = unpack2(acc[i]);
-          if (n0 < a.N) {
-            if (2 * i < left && 2 * i < it.nh) y[(int64_t)(2 * i) * a.N] = __float2bfloat16_rn(v.x);
-            if (2 * i + 1 < left && 2 * i + 1 < it.nh)
-              y[(int64_t)(2 * i + 1) * a.N] = __float2bfloat16_rn(v.y);
-          }
+          dst[0] = __float2bfloat16_rn(v.x);
+          if (2 * i + 1 < left) dst[a.N] = __float2bfloat16_rn(v.y);
+          dst += 2 * a.N;
         }
       }
+      __syncwarp();
     }
     if (!ok) give_up();
   }
@@ -589,7 +765,7 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, uint
 
 template <bool kFP8, bool kSwiglu, int kGroup>
 ep_status_t launch(ExpertsArgs a, cudaStream_t st) {
-  using C = Cfg<kFP8>;
+  using C = Cfg<kFP8, kGroup>;
   const auto kernel = experts_tc_kernel<kFP8, kSwiglu, kGroup>;
   DeviceProps props;
   if (!device_props(&props)) return EP_ERR_CUDA;
@@ -602,23 +778,27 @@ ep_status_t launch(ExpertsArgs a, cudaStream_t st) {
     if (!ready[dev]) {
       // the register split draws on what the block was launched with
       cudaFuncAttributes fa;
-      if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs * kThreads < 65536 ||
+      if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs < kLaunchRegs ||
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
               cudaSuccess)
         return EP_ERR_CUDA;
       ready[dev] = true;
     }
   }
-  CUtensorMap xmap, wmap;
-  if (!encode_2d(&xmap, kFP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                 a.x, a.I, (uint64_t)a.E * a.cap, (uint64_t)a.I * (kFP8 ? 1 : 2), kFP8 ? 128 : 64,
-                 kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q, a.I / 2, (uint64_t)a.E * a.rows,
+  XMaps xmaps;
+  CUtensorMap wmap;
+  for (int i = 0; i < kBoxes; ++i)
+    if (!encode_2d(&xmaps.rows[i],
+                   kFP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x,
+                   a.I, (uint64_t)a.E * a.cap, (uint64_t)a.I * (kFP8 ? 1 : 2), kFP8 ? 128 : 64,
+                   32 * (i + 1), CU_TENSOR_MAP_SWIZZLE_128B))
+      return EP_ERR_CUDA;
+  if (!encode_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q, a.I / 2, (uint64_t)a.E * a.rows,
                  a.I / 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B))
     return EP_ERR_CUDA;
   const int width = kSwiglu ? 64 : 128;
   a.tiles = (a.N + width - 1) / width;
-  launch_pdl(kernel, props.sm_count, kThreads, C::kSmem, st, a, xmap, wmap);
+  launch_pdl(kernel, props.sm_count, kThreads, C::kSmem, st, a, xmaps, wmap);
   return launch_status();
 }
 
