@@ -1,17 +1,34 @@
 // ep_experts_w4.cu -- the experts' products with 4-bit weights on the rows of
 // the expert-major layout, for few rows per expert.
 //
-// A warp multiplies 16-row tiles of the weights by up to 8 * NT of the
-// expert's rows with mma.sync m16n8k16 (weights as A, rows as B, float32
-// accumulators).  The dot product may run over the channels in any order, as
-// long as both operands use the same one, and that order is chosen so that
-// the stored weights are the A fragment: of 128 channels, thread t of a quad
-// takes channels [32 t, 32 t + 32) of its two weight rows, one 16-byte load
-// each, and unpacks them in registers.  Nothing passes through shared memory
-// but the final sum.  A step of the product is 128 channels, which the warps
-// of a block divide among themselves.
+// A warp multiplies a tile of 64 weight rows (swiglu: 32 of the gate and the
+// same 32 of the up projection) by up to 16 of the expert's rows, or 32 by up
+// to 32, with mma.sync m16n8k16 (weights as A, rows as B, float32
+// accumulators): at a few rows the tensor rate is not what counts, and A can
+// come from registers.  The dot product may run over the channels in any
+// order, as long as both operands use the same one.  A step is 128 channels;
+// thread t of a quad takes the t-th quarter of every 64 channels (32 where those
+// have a scale of their own), so that one matrix step never mixes groups, and
+// unpacks the codes of its bytes without moving them to another thread.  The
+// sums of a group are scaled in float32; no weight is rounded.
+//
+// bf16 rows: the codes become 128 + q (the bits of q are the low mantissa
+// bits of 128) and the sum over the group less (128 + zero) * sum(x), which
+// the tensor cores add up with a tile of ones: 7 instructions for 8 codes
+// instead of 11.  E4M3 rows: both sides as f16, where codes less their zero
+// point and E4M3 values are exact.
+//
+// What bounds it is the stream of the codes, and close behind it the integer
+// pipe, which takes two cycles an instruction: so every warp keeps two or
+// more steps on their way with asynchronous copies, across the ends of its
+// tiles, pointers advance instead of being computed, and lanes without a row
+// of x read the last one instead of zeros (their columns are not stored).
+// The warps of a block share a tile by its channels when there are too few
+// tiles for all warps.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "ep_experts_w4.cuh"
 
@@ -20,100 +37,308 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMT = 2;  // 16-row weight tiles per warp (swiglu: one of the gate, one of up)
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
+// NTMAX: most rows of x per expert, in eights.  Experts with at most 8 rows
+// have a kernel of their own: with their accumulators two blocks fit an SM.
+template <int NTMAX>
+struct Cfg {
+  static constexpr int kMT = NTMAX == 1 ? 4 : 2;   // 16-row weight tiles per warp
+  static constexpr int kStages = NTMAX == 1 ? 3 : 4;
+  static constexpr int kStage = kMT * 16 * 64;     // bytes of codes of a step
+  // a tile's partial sums, where warps share it, go to the stage just used;
+  // 32 rows of x do not fit there
+  static constexpr int kRed = NTMAX == 1 ? 0 : kMT * 16 * 8 * NTMAX * 4;
+  static constexpr int kSmem = kWarps * (kStages * kStage + kRed);
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// (a & b) | c in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 
-// Codes i and i + 4 of the 8 in `w`, as bf16 (128 + q): the bits of q are the
-// low mantissa bits of 128.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
-  return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-}
-
-// E4M3 codes c0, c1 (the low halves of `two`) as bf16x2, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  const float2 f = __half22float2(__half2(h));
-  const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// B fragments of 32 channels of one row, in the order of the weights' codes:
-// word w of 8 channels gives the pairs (0,4) (1,5) (2,6) (3,7).
-template <bool kFP8>
-__device__ __forceinline__ void load_row(const uint8_t* p, bool live, uint32_t (&b)[16]) {
-  uint32_t x[16];
-  if (kFP8) {
-    int4 v[2] = {};
-    if (live) {
-      v[0] = __ldg(reinterpret_cast<const int4*>(p));
-      v[1] = __ldg(reinterpret_cast<const int4*>(p) + 1);
-    }
-    const uint32_t c[8] = {(uint32_t)v[0].x, (uint32_t)v[0].y, (uint32_t)v[0].z, (uint32_t)v[0].w,
-                           (uint32_t)v[1].x, (uint32_t)v[1].y, (uint32_t)v[1].z, (uint32_t)v[1].w};
+// Codes i and i + 4 of the 8 in w (i = 0..3), less nothing (bf16: 128 + q) ...
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t (&o)[4]) {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      // bytes 0..3 of both words: pair (j, j + 4)
+  for (int i = 0; i < 4; ++i) o[i] = and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u);
+}
+// ... or less their zero point (f16): 0x6400 | q is 1024 + q, and with q in
+// the next four bits 1024 + 16 q, so two of four need no shift.
+// low = -(1024 + zero), high = -(64 + zero), as f16 pairs.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t low, uint32_t high,
+                                          uint32_t (&o)[4]) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        b[4 * w + j] = e4m3x2_to_bf16x2(
-            __byte_perm(c[2 * w], c[2 * w + 1], (uint32_t)(j | ((4 + j) << 4))) & 0xFFFFu);
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t v = i ? w >> 8 : w;
+    const uint32_t a = and_or(v, 0x000F000Fu, 0x64006400u), b = and_or(v, 0x00F000F0u, 0x64006400u);
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * i]) : "r"(a), "r"(low));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[2 * i + 1]) : "r"(b), "r"(0x2C002C00u), "r"(high));
+  }
+}
+
+// The B fragments of 8 channels: the pairs (0,4) (1,5) (2,6) (3,7).
+__device__ __forceinline__ void pairs_bf16(const uint4& x, uint32_t (&b)[4]) {
+  b[0] = __byte_perm(x.x, x.z, 0x5410);
+  b[1] = __byte_perm(x.x, x.z, 0x7632);
+  b[2] = __byte_perm(x.y, x.w, 0x5410);
+  b[3] = __byte_perm(x.y, x.w, 0x7632);
+}
+__device__ __forceinline__ void pairs_e4m3(const uint2& x, uint32_t (&b)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t two = __byte_perm(x.x, x.y, (uint32_t)(j | (4 + j) << 4));
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFF), __NV_E4M3);
+    b[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// First channel, within a step, of word j (8 channels) of thread t of a quad:
+// the t-th quarter of every 64 channels, or of every 32 where those have
+// scales of their own.
+template <int kGroup>
+__device__ __forceinline__ int word_channel(int t, int j) {
+  return kGroup == 32 ? j * 32 + t * 8 : (j >> 1) * 64 + t * 16 + (j & 1) * 8;
+}
+
+// The 16-byte chunks of a staged weight row are permuted by its place among
+// eight rows, so that the loads of fragments meet no bank twice.
+__device__ __forceinline__ int chunk_swizzle(int g) { return (g & 2) | (g >> 2 & 1); }
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+// Row i * 8 + g of a tile of MT * 16 weight rows, relative to the tile's
+// first: rows beyond the last channel read the last one (32-bit indices and
+// one multiply-add an address, instead of a pointer for each row).
+template <int MT, bool kSwiglu>
+__device__ __forceinline__ uint32_t tile_row(int i, int g, int last, int N) {
+  if (!kSwiglu) return (uint32_t)min(g + 8 * i, last);
+  return i < MT ? (uint32_t)min(g + 8 * i, last) : (uint32_t)(min(g + 8 * (i - MT), last) + N);
+}
+
+// What a warp reads with its own lanes for the products of a tile: pointers
+// to this step's first byte, advanced from step to step.
+template <int NT>
+struct Sources {
+  const uint8_t* x[NT];         // rows of x: this lane's channels
+  const float* xs;              // scales of the expert's E4M3 rows, and which
+  uint32_t xrow[NT][2];
+  const __nv_bfloat16* scale;   // scales and zero points of the tile's first row
+  const uint8_t* zero;
+  int last;                     // last row of the tile that is a channel
+};
+
+// The scales (pairs of bf16) and zero points (bytes) of the kPer groups of a
+// step, g0 the first one.  Where whole steps make up a row they are aligned
+// to be read at once; else one by one, groups beyond the row's end as any.
+template <int kPer>
+__device__ __forceinline__ void load_scales(const __nv_bfloat16* p, int g0, bool ragged,
+                                            uint32_t groups, uint32_t (&v)[(kPer + 1) / 2]) {
+  const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
+  if (kPer == 1) {
+    v[0] = __ldg(u);
+  } else if (!ragged && groups % kPer == 0) {
+    if (kPer == 2) {
+      v[0] = __ldg(reinterpret_cast<const uint32_t*>(u));
+    } else {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(u));
+      v[0] = w.x;
+      v[(kPer + 1) / 2 - 1] = w.y;
     }
   } else {
-    int4 v[4] = {};
-    if (live) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const int4*>(p) + i);
+    for (int q = 0; q < kPer; q += 2) {
+      const uint32_t lo = __ldg(u + (g0 + q < (int)groups ? q : 0));
+      const uint32_t hi = __ldg(u + (g0 + q + 1 < (int)groups ? q + 1 : 0));
+      v[q / 2] = lo | hi << 16;
     }
+  }
+}
+template <int kPer>
+__device__ __forceinline__ uint32_t load_zeros(const uint8_t* p, int g0, bool ragged,
+                                               uint32_t groups) {
+  if (kPer == 1) return __ldg(p);
+  if (!ragged && groups % kPer == 0)
+    return kPer == 2 ? __ldg(reinterpret_cast<const uint16_t*>(p))
+                     : __ldg(reinterpret_cast<const uint32_t*>(p));
+  uint32_t v = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[4 * i] = (uint32_t)v[i].x;
-      x[4 * i + 1] = (uint32_t)v[i].y;
-      x[4 * i + 2] = (uint32_t)v[i].z;
-      x[4 * i + 3] = (uint32_t)v[i].w;
+  for (int q = 0; q < kPer; ++q)
+    v |= (uint32_t)__ldg(p + (g0 + q < (int)groups ? q : 0)) << (8 * q);
+  return v;
+}
+
+// The products of step s of a tile.  ragged: channels end within the step.
+template <int MT, int NT, int kStages, bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
+__device__ __forceinline__ void step_products(const ExpertsArgs& a, const Sources<NT>& src,
+                                              int s, bool ragged, uint32_t stage, int lane,
+                                              float (&acc)[MT][NT][4]) {
+  constexpr int kPer = 128 / kGroup;
+  constexpr int MP = NT >= 2 ? 2 : MT;  // weight tiles at a time: what the registers hold
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t groups = (uint32_t)a.I / kGroup;
+  // everything that comes from global memory goes out before the wait for
+  // the codes
+  uint4 xv[NT][kFP8 ? 2 : 4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // word_channel less this thread's own offset, which the pointer holds
+      const int k = word_channel<kGroup>(0, j);
+      if (kFP8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src.x[nt] + k));
+        (&xv[nt][j >> 1].x)[(j & 1) * 2] = v.x;
+        (&xv[nt][j >> 1].x)[(j & 1) * 2 + 1] = v.y;
+      } else if (!ragged) {
+        xv[nt][j] = __ldg(reinterpret_cast<const uint4*>(src.x[nt] + 2 * k));
+      } else {
+        xv[nt][j] = make_uint4(0, 0, 0, 0);
+        if (s * 128 + word_channel<kGroup>(t, j) < a.I)
+          xv[nt][j] = __ldg(reinterpret_cast<const uint4*>(src.x[nt] + 2 * k));
+      }
     }
+  float xs[NT][2];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      b[4 * w] = __byte_perm(x[4 * w], x[4 * w + 2], 0x5410);
-      b[4 * w + 1] = __byte_perm(x[4 * w], x[4 * w + 2], 0x7632);
-      b[4 * w + 2] = __byte_perm(x[4 * w + 1], x[4 * w + 3], 0x5410);
-      b[4 * w + 3] = __byte_perm(x[4 * w + 1], x[4 * w + 3], 0x7632);
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) xs[nt][i] = kFP8 ? __ldg(src.xs + src.xrow[nt][i]) : 1.0f;
+  // a row's scales and zero points of this step, in one load each
+  uint32_t sv[MT][2][(kPer + 1) / 2], zv[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint64_t at = (uint64_t)tile_row<MT, kSwiglu>(mt * 2 + h, g, src.last, a.N) * groups;
+      load_scales<kPer>(src.scale + at, s * kPer, ragged, groups, sv[mt][h]);
+      zv[mt][h] = 0x08080808u;
+      if (kZeros) zv[mt][h] = load_zeros<kPer>(src.zero + at, s * kPer, ragged, groups);
+    }
+  asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+  __syncwarp();
+
+  float ones[NT][kPer][4] = {};
+#pragma unroll
+  for (int m0 = 0; m0 < MT; m0 += MP) {
+    float part[MP][NT][4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int q = j / (4 / kPer);  // the word's group
+      uint32_t b[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (kFP8) {
+          const uint4 v = xv[nt][j >> 1];
+          pairs_e4m3(j & 1 ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y), b[nt]);
+        } else {
+          constexpr uint32_t k1 = 0x3F803F80u;  // ones
+          pairs_bf16(xv[nt][kFP8 ? 0 : j], b[nt]);
+          if (m0 == 0) {
+            mma_bf16(ones[nt][q], k1, k1, k1, k1, b[nt][0], b[nt][1]);
+            mma_bf16(ones[nt][q], k1, k1, k1, k1, b[nt][2], b[nt][3]);
+          }
+        }
+      }
+      // the words of both rows of the weight tiles; two at a time where a
+      // thread has two next to one another
+      const int byte = word_channel<kGroup>(t, j) / 2;
+      const uint32_t at = stage + ((byte >> 4 ^ chunk_swizzle(g)) << 4) + (byte & 15) + g * 64;
+#pragma unroll
+      for (int m = 0; m < MP; ++m) {
+        const int mt = m0 + m;
+        const uint32_t w0 = lds32(at + mt * 1024), w1 = lds32(at + mt * 1024 + 512);
+        const uint32_t z0 = zv[mt][0] >> (8 * q) & 0xFF, z1 = zv[mt][1] >> (8 * q) & 0xFF;
+        uint32_t lo[4], hi[4];
+        if (kFP8) {
+          // -(1024 + z) and -(64 + z) as f16: 0xE400 | z, 0xD400 | z << 4
+          codes_f16(w0, 0xE400E400u | z0 * 0x00010001u, 0xD400D400u | z0 * 0x00100010u, lo);
+          codes_f16(w1, 0xE400E400u | z1 * 0x00010001u, 0xD400D400u | z1 * 0x00100010u, hi);
+        } else {
+          codes_bf16(w0, lo);
+          codes_bf16(w1, hi);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (kFP8) {
+            mma_f16(part[m][nt], lo[0], hi[0], lo[1], hi[1], b[nt][0], b[nt][1]);
+            mma_f16(part[m][nt], lo[2], hi[2], lo[3], hi[3], b[nt][2], b[nt][3]);
+          } else {
+            mma_bf16(part[m][nt], lo[0], hi[0], lo[1], hi[1], b[nt][0], b[nt][1]);
+            mma_bf16(part[m][nt], lo[2], hi[2], lo[3], hi[3], b[nt][2], b[nt][3]);
+          }
+        }
+      }
+      if ((j + 1) % (4 / kPer) == 0) {  // the end of a group
+#pragma unroll
+        for (int m = 0; m < MP; ++m) {
+          const int mt = m0 + m;
+          const uint32_t z0 = zv[mt][0] >> (8 * q) & 0xFF, z1 = zv[mt][1] >> (8 * q) & 0xFF;
+          const uint32_t w0 = sv[mt][0][q / 2], w1 = sv[mt][1][q / 2];
+          const float s0 = __uint_as_float(q & 1 ? w0 & 0xFFFF0000u : w0 << 16);
+          const float s1 = __uint_as_float(q & 1 ? w1 & 0xFFFF0000u : w1 << 16);
+          // -(128 + z): z << 16 is z in units of 128's last mantissa places
+          const float f0 = __uint_as_float(0xC3000000u | z0 << 16);
+          const float f1 = __uint_as_float(0xC3000000u | z1 << 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float v = kFP8 ? part[m][nt][i] * xs[nt][i & 1]
+                                   : fmaf(i < 2 ? f0 : f1, ones[nt][q][i], part[m][nt][i]);
+              acc[mt][nt][i] = fmaf(v, i < 2 ? s0 : s1, acc[mt][nt][i]);
+              part[m][nt][i] = 0.0f;
+            }
+        }
+      }
     }
   }
 }
 
-// kGroup: 128 (a scale spans a step: it multiplies the float32 sum of the
-// step), else 64 or 32 (it multiplies the weights, rounded to bf16 once).
-template <int NT, bool kFP8, bool kSwiglu, int kGroup>
-__global__ void __launch_bounds__(kThreads) experts_kernel(ExpertsArgs a, int ks) {
+// A warp's place in its sequence of tiles and steps; one for the copies and,
+// some steps behind, one for the products.
+struct Cursor {
+  int item, s, e, n0;  // tile and step; the tile's expert and first output channel
+};
+
+template <int NTMAX, bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
+__global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 2 : 1) experts_kernel(ExpertsArgs a) {
+  using C = Cfg<NTMAX>;
+  constexpr int MT = C::kMT, kRows = MT * 16;
+  constexpr int kChannels = kSwiglu ? kRows / 2 : kRows;  // output channels of a tile
   pdl_wait_then_release();
-  extern __shared__ float red[];  // [warp][16 * kMT][kPitch], then the live experts
+  extern __shared__ __align__(16) uint8_t smem[];  // stages, sums, then the live experts
   __shared__ int warp_total[kWarps];
   __shared__ int live_total;
-  constexpr int kPitch = 8 * NT + 1;
-  uint16_t* live = reinterpret_cast<uint16_t*>(red + kWarps * 16 * kMT * kPitch);
+  __shared__ int used_slot[kWarps];  // the stage of a warp's last step
+  uint16_t* live = reinterpret_cast<uint16_t*>(smem + C::kSmem);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t4 = lane & 3;
+  const int g = lane >> 2, t = lane & 3;
 
   // the experts that have rows, in order
   if (tid == 0) live_total = 0;
@@ -121,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) experts_kernel(ExpertsArgs a, int ks
   for (int e0 = 0; e0 < a.E; e0 += kThreads) {
     const int e = e0 + tid;
     const int64_t n = e < a.E ? min((int64_t)a.count[e], a.cap) : 0;
-    const bool busy = n > 0 && n <= kFewRows;
+    const bool busy = NTMAX == 1 ? n > 0 && n <= 8 : n > 8 && n <= kFewRows;
     const unsigned bal = __ballot_sync(kFull, busy);
     if (lane == 0) warp_total[warp] = __popc(bal);
     __syncthreads();
@@ -132,165 +357,204 @@ __global__ void __launch_bounds__(kThreads) experts_kernel(ExpertsArgs a, int ks
     if (tid == kThreads - 1) live_total = before + __popc(bal);
     __syncthreads();
   }
-  const int64_t items = (int64_t)live_total * a.tiles;
-  const int kw = warp % ks, mw = warp / ks;
-  const int steps = (a.I + 127) / 128;
-  const int mrows = kSwiglu ? 16 : 16 * kMT;  // output channels per warp
-  constexpr int kBytes = kFP8 ? 1 : 2;
-
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int e = live[item / a.tiles];
-    const int tile = (int)(item % a.tiles);
-    const int n0 = (tile * (kWarps / ks) + mw) * mrows;
-    const int have = (int)min((int64_t)a.count[e], a.cap);
-
-    for (int r0 = 0; r0 < have; r0 += 8 * NT) {
-      const int nrows = min(have - r0, 8 * NT);
-      float acc[kMT][NT][4] = {};
-      const uint8_t* xrow[NT];
-      const float* xsc[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int64_t r = (int64_t)e * a.cap + r0 + min(nt * 8 + g, nrows - 1);
-        xrow[nt] = a.x + r * a.I * kBytes;
-        if (kFP8) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            xsc[nt][c] = a.x_scales + ((int64_t)e * a.cap + r0 + min(nt * 8 + 2 * t4 + c, nrows - 1)) *
-                                          (a.I / 128);
-        }
+  const int steps = (a.I + 127) / 128, groups = a.I / kGroup;
+  const int items = live_total * a.tiles;
+  // warps per tile: what leaves the busiest warp the fewest steps
+  int ks = 1;
+  {
+    const int warps = (int)gridDim.x * kWarps;
+    int64_t best = (int64_t)((items + warps - 1) / warps) * steps;
+    for (int k = 2; k <= kWarps && k <= steps; k *= 2) {
+      const int64_t most = (int64_t)((items * (int64_t)k + warps - 1) / warps) * ((steps + k - 1) / k);
+      if (most < best) {
+        best = most;
+        ks = k;
       }
-      for (int s = kw; s < steps; s += ks) {
-        const int k0 = s * 128 + t4 * 32;  // this thread's 32 channels
-        const bool kin = k0 < a.I;
-        uint4 wv[kMT][2];
-        float ws[kMT][2];
-        uint32_t zp[kMT][2];
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            int n = n0 + (kSwiglu ? 0 : mt * 16) + h * 8 + g;
-            n = min(n, a.N - 1) + (kSwiglu && mt ? a.N : 0);
-            const int64_t wrow = (int64_t)e * a.rows + n;
-            wv[mt][h] = make_uint4(0, 0, 0, 0);
-            ws[mt][h] = 0.0f;
-            zp[mt][h] = 0x43084308u;
-            if (kin) {
-              wv[mt][h] = *reinterpret_cast<const uint4*>(a.q + wrow * (a.I / 2) + k0 / 2);
-              const int64_t gi = wrow * (a.I / kGroup) + k0 / kGroup;
-              ws[mt][h] = __bfloat162float(a.scales[gi]);
-              if (a.zeros) zp[mt][h] = 0x43004300u | (uint32_t)a.zeros[gi] * 0x00010001u;
-            }
-          }
-        }
-        uint32_t b[NT][16];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          if (nt == 0 || nt * 8 < nrows)
-            load_row<kFP8>(xrow[nt] + (int64_t)k0 * kBytes, kin && nt * 8 + g < nrows, b[nt]);
-        float part[kMT][NT][4] = {};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) {
-            const uint32_t w0 = (&wv[mt][0].x)[j], w1 = (&wv[mt][1].x)[j];
-            uint32_t lo[4], hi[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              lo[i] = bf16x2_sub(code_pair(w0, i), zp[mt][0]);
-              hi[i] = bf16x2_sub(code_pair(w1, i), zp[mt][1]);
-              if (kGroup != 128) {
-                const __nv_bfloat162 s0 = __float2bfloat162_rn(ws[mt][0]);
-                const __nv_bfloat162 s1 = __float2bfloat162_rn(ws[mt][1]);
-                lo[i] = bf16x2_mul(lo[i], *reinterpret_cast<const uint32_t*>(&s0));
-                hi[i] = bf16x2_mul(hi[i], *reinterpret_cast<const uint32_t*>(&s1));
-              }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (nt == 0 || nt * 8 < nrows) {
-                const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
-                const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-                mma_bf16(part[mt][nt], a0, b[nt][4 * j], b[nt][4 * j + 1]);
-                mma_bf16(part[mt][nt], a1, b[nt][4 * j + 2], b[nt][4 * j + 3]);
-              }
-            }
-          }
-        }
-        // the step's sums, scaled in float32: per weight row (a group of 128
-        // channels is the step) and per row of x (FP8)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float x0 = 1.0f, x1 = 1.0f;
-          if (kFP8) {
-            x0 = __ldg(xsc[nt][0] + s);
-            x1 = __ldg(xsc[nt][1] + s);
-          }
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) {
-            const float s0 = kGroup == 128 ? __shfl_sync(kFull, ws[mt][0], lane & ~3) : 1.0f;
-            const float s1 = kGroup == 128 ? __shfl_sync(kFull, ws[mt][1], lane & ~3) : 1.0f;
-            acc[mt][nt][0] = fmaf(part[mt][nt][0], s0 * x0, acc[mt][nt][0]);
-            acc[mt][nt][1] = fmaf(part[mt][nt][1], s0 * x1, acc[mt][nt][1]);
-            acc[mt][nt][2] = fmaf(part[mt][nt][2], s1 * x0, acc[mt][nt][2]);
-            acc[mt][nt][3] = fmaf(part[mt][nt][3], s1 * x1, acc[mt][nt][3]);
-          }
-        }
-      }
-
-      // sum over the warps that share the tile, then the epilogue
-#pragma unroll
-      for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            red[(warp * 16 * kMT + mt * 16 + (c >> 1) * 8 + g) * kPitch + nt * 8 + 2 * t4 + (c & 1)] =
-                acc[mt][nt][c];
-      __syncthreads();
-      const int outs = (kWarps / ks) * mrows;  // output channels of the block
-      for (int i = tid; i < outs * nrows; i += kThreads) {
-        const int ch = i % outs, r = i / outs;
-        const int m = ch / mrows, c = ch % mrows;
-        const int n = tile * outs + ch;
-        float v0 = 0.0f, v1 = 0.0f;
-        for (int k = 0; k < ks; ++k) {
-          const float* p = red + (m * ks + k) * 16 * kMT * kPitch;
-          v0 += p[c * kPitch + r];
-          if (kSwiglu) v1 += p[(16 + c) * kPitch + r];
-        }
-        if (kSwiglu) v0 = v0 / (1.0f + expf(-v0)) * v1;
-        if (n < a.N)
-          a.y[((int64_t)e * a.cap + r0 + r) * a.N + n] = __float2bfloat16_rn(v0);
-      }
-      __syncthreads();
     }
   }
+  const int kw = warp % ks, team = warp / ks, teams = kWarps / ks;
+  const int first = blockIdx.x * teams + team, stride = gridDim.x * teams;
+  const uint32_t stage0 = smem_addr(smem) + warp * C::kStages * C::kStage;
+
+  const auto enter = [&](Cursor& c) {
+    if (c.item < items) {
+      c.e = live[c.item / a.tiles];
+      c.n0 = c.item % a.tiles * kChannels;
+    }
+    c.s = kw;
+  };
+  Cursor load, use;
+  load.item = use.item = first;
+  enter(load);
+  enter(use);
+  const uint8_t* codes;  // this lane's chunk of the tile's first row at load.s
+  int last = 0;
+  const auto point = [&]() {
+    codes = a.q + ((int64_t)load.e * a.rows + load.n0) * (a.I / 2) + load.s * 64 + t * 16;
+    last = min(kChannels, a.N - load.n0) - 1;
+  };
+  if (load.item < items) point();
+  const uint32_t chunk = (uint32_t)(g * 64 + ((t ^ chunk_swizzle(g)) << 4));
+  const auto issue = [&](uint32_t stage) {
+    if (load.item < items) {
+      // beyond the last channel: any bytes of the row, x is zero there
+      const uint8_t* p = load.s * 128 + t * 32 < a.I ? codes : codes - load.s * 64 - t * 16;
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i)
+        copy16(stage + chunk + i * 512,
+               p + (uint64_t)tile_row<MT, kSwiglu>(i, g, last, a.N) * (uint32_t)(a.I / 2));
+      codes += ks * 64;
+      load.s += ks;
+      if (load.s >= steps) {
+        load.item += stride;
+        enter(load);
+        if (load.item < items) point();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) issue(stage0 + i * C::kStage);
+  int slot = 0;
+
+  // one tile times the rows of its expert
+  const auto tile = [&](auto nt_tag, int nrows) {
+    constexpr int NT = decltype(nt_tag)::value;
+    Sources<NT> src;
+    {
+      const int64_t row = (int64_t)use.e * a.cap;
+      const int64_t at = ((int64_t)use.e * a.rows + use.n0) * groups + use.s * (128 / kGroup);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        src.x[nt] = a.x + ((row + min(nt * 8 + g, nrows - 1)) * a.I + use.s * 128 +
+                           word_channel<kGroup>(t, 0)) * (kFP8 ? 1 : 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) src.xrow[nt][i] = (uint32_t)(min(nt * 8 + 2 * t + i, nrows - 1) * steps);
+      }
+      src.xs = kFP8 ? a.x_scales + row * steps + use.s : nullptr;
+      src.scale = a.scales + at;
+      src.zero = a.zeros + at;
+      src.last = min(kChannels, a.N - use.n0) - 1;
+    }
+    float acc[MT][NT][4] = {};
+    for (; use.s < steps; use.s += ks) {
+      const uint32_t stage = stage0 + slot * C::kStage;
+      step_products<MT, NT, C::kStages, kFP8, kSwiglu, kGroup, kZeros>(
+          a, src, use.s, !kFP8 && use.s * 128 + 128 > a.I, stage, lane, acc);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) src.x[nt] += ks * 128 * (kFP8 ? 1 : 2);
+      src.xs += ks;
+      src.scale += ks * (128 / kGroup);
+      src.zero += ks * (128 / kGroup);
+      __syncwarp();
+      issue(stage0 + (slot == 0 ? C::kStages - 1 : slot - 1) * C::kStage);
+      slot = slot == C::kStages - 1 ? 0 : slot + 1;
+    }
+    __nv_bfloat16* y = a.y + (int64_t)use.e * a.cap * a.N;
+    if (ks > 1) {
+      // the team's sums meet in shared memory: each warp's in the stage that
+      // its last step used (the next copy into it is a step away)
+      if (lane == 0) used_slot[warp] = slot == 0 ? C::kStages - 1 : slot - 1;
+      __syncwarp();
+      constexpr int kCols = 8 * NT;
+      const auto sums = [&](int w) {
+        return reinterpret_cast<float*>(
+            C::kRed ? smem + kWarps * C::kStages * C::kStage + w * C::kRed
+                    : smem + (w * C::kStages + used_slot[w]) * C::kStage);
+      };
+      float* mine = sums(warp);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2*>(mine + (mt * 16 + h * 8 + g) * kCols + nt * 8 + 2 * t) =
+                make_float2(acc[mt][nt][2 * h], acc[mt][nt][2 * h + 1]);
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(ks * 32) : "memory");
+      for (int i = kw * 32 + lane; i < kChannels * nrows; i += ks * 32) {
+        const int ch = i % kChannels, r = i / kChannels;
+        float v0 = 0.0f, v1 = 0.0f;
+        for (int k = 0; k < ks; ++k) {
+          const float* p = sums(team * ks + k);
+          v0 += p[ch * kCols + r];
+          if (kSwiglu) v1 += p[(kChannels + ch) * kCols + r];
+        }
+        if (kSwiglu) v0 = v0 / (1.0f + expf(-v0)) * v1;
+        if (use.n0 + ch < a.N) y[(int64_t)r * a.N + use.n0 + ch] = __float2bfloat16_rn(v0);
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(ks * 32) : "memory");
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = nt * 8 + 2 * t + (i & 1), ch = use.n0 + (i >> 1) * 8 + g;
+          if (r >= nrows) continue;
+#pragma unroll
+          for (int mt = 0; mt < (kSwiglu ? MT / 2 : MT); ++mt) {
+            float v = acc[mt][nt][i];
+            if (kSwiglu) v = v / (1.0f + expf(-v)) * acc[mt + MT / 2][nt][i];
+            if (ch + mt * 16 < a.N) y[(int64_t)r * a.N + ch + mt * 16] = __float2bfloat16_rn(v);
+          }
+        }
+    }
+  };
+  while (use.item < items) {
+    const int nrows = (int)min((int64_t)a.count[use.e], a.cap);
+    if (NTMAX == 1)
+      tile(std::integral_constant<int, 1>{}, nrows);
+    else if (nrows <= 16)
+      tile(std::integral_constant<int, NTMAX == 1 ? 1 : 2>{}, nrows);
+    else
+      tile(std::integral_constant<int, NTMAX>{}, nrows);
+    use.item += stride;
+    enter(use);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int NT, bool kFP8, bool kSwiglu, int kGroup>
+template <int NTMAX, bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
 ep_status_t launch_small(ExpertsArgs a, cudaStream_t st) {
+  using C = Cfg<NTMAX>;
+  const auto kernel = experts_kernel<NTMAX, kFP8, kSwiglu, kGroup, kZeros>;
   DeviceProps props;
   if (!device_props(&props)) return EP_ERR_CUDA;
-  const int steps = (a.I + 127) / 128;
-  int ks = kWarps;  // warps that share one tile
-  while (ks > 1 && ks > steps) ks /= 2;
-  const int outs = (kWarps / ks) * (kSwiglu ? 16 : 16 * kMT);
-  a.tiles = (a.N + outs - 1) / outs;
-  const size_t smem = (size_t)kWarps * 16 * kMT * (8 * NT + 1) * 4 + (size_t)a.E * 2;
-  static_assert(kWarps * 16 * kMT * 33 * 4 + EP_MAX_EXPERTS * 2 <= 48 * 1024, "shared memory");
-  const int64_t most = (int64_t)a.E * a.tiles;
-  const unsigned grid = (unsigned)(most < 2 * props.sm_count ? most : 2 * props.sm_count);
-  launch_pdl(experts_kernel<NT, kFP8, kSwiglu, kGroup>, grid, kThreads, smem, st, a, ks);
+  static std::mutex mu;
+  static int resident[64] = {};  // blocks per SM, at a few hundred experts
+  int dev = -1, blocks = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EP_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (resident[dev] == 0) {
+      int n = 0;
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               C::kSmem + EP_MAX_EXPERTS * 2) != cudaSuccess ||
+          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, C::kSmem + 1024) !=
+              cudaSuccess ||
+          n < 1)
+        return EP_ERR_CUDA;
+      resident[dev] = n;
+    }
+    blocks = resident[dev];
+  }
+  constexpr int kChannels = C::kMT * (kSwiglu ? 8 : 16);
+  a.tiles = (a.N + kChannels - 1) / kChannels;
+  launch_pdl(kernel, (unsigned)(blocks * props.sm_count), kThreads, C::kSmem + (size_t)a.E * 2, st, a);
   return launch_status();
+}
+
+template <bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
+ep_status_t launch_zeros(const ExpertsArgs& a, cudaStream_t st) {
+  const ep_status_t s = launch_small<1, kFP8, kSwiglu, kGroup, kZeros>(a, st);
+  if (s != EP_OK || a.cap <= 8) return s;
+  return launch_small<4, kFP8, kSwiglu, kGroup, kZeros>(a, st);
 }
 
 template <bool kFP8, bool kSwiglu, int kGroup>
 ep_status_t launch_rows(const ExpertsArgs& a, cudaStream_t st) {
-  if (a.cap <= 8) return launch_small<1, kFP8, kSwiglu, kGroup>(a, st);
-  if (a.cap <= 16) return launch_small<2, kFP8, kSwiglu, kGroup>(a, st);
-  return launch_small<4, kFP8, kSwiglu, kGroup>(a, st);
+  return a.zeros ? launch_zeros<kFP8, kSwiglu, kGroup, true>(a, st)
+                 : launch_zeros<kFP8, kSwiglu, kGroup, false>(a, st);
 }
 
 template <bool kFP8, bool kSwiglu>

@@ -357,7 +357,8 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t zp, uint32_t* ou
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t two = __byte_perm(w, odd, (uint32_t)(j | j << 4 | (4 + j) << 8 | (4 + j) << 12));
-    const uint32_t v = (two & 0x000F000Fu) | 0x43004300u;
+    uint32_t v;  // (two & 0x000F000F) | 0x43004300
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(two), "r"(0x000F000Fu), "r"(0x43004300u));
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(out[j]) : "r"(v), "r"(zp));
   }
 }
