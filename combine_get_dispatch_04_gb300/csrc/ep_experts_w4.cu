@@ -2,10 +2,9 @@
 // the expert-major layout, for few rows per expert.
 //
 // A warp multiplies a tile of 64 weight rows (swiglu: 32 of the gate and the
-// same 32 of the up projection) by up to 16 of the expert's rows, or 32 by up
-// to 32, with mma.sync m16n8k16 (weights as A, rows as B, float32
-// accumulators): at a few rows the tensor rate is not what counts, and A can
-// come from registers.  The dot product may run over the channels in any
+// same 32 of the up projection) by up to 8 rows of x with mma.sync m16n8k16
+// (weights as A, rows as B, float32 accumulators): at a few rows the tensor
+// rate is not what counts, and A can come from registers.  The dot product may run over the channels in any
 // order, as long as both operands use the same one.  A step is 128 channels;
 // thread t of a quad takes the t-th quarter of every 64 channels (32 where those
 // have a scale of their own), so that one matrix step never mixes groups, and
@@ -19,16 +18,14 @@
 // point and E4M3 values are exact.
 //
 // What bounds it is the stream of the codes, and close behind it the integer
-// pipe, which takes two cycles an instruction: so every warp keeps two or
-// more steps on their way with asynchronous copies, across the ends of its
+// pipe, which takes two cycles an instruction: so every warp keeps two
+// steps on their way with asynchronous copies, across the ends of its
 // tiles, pointers advance instead of being computed, and lanes without a row
 // of x read the last one instead of zeros (their columns are not stored).
 // The warps of a block share a tile by its channels when there are too few
 // tiles for all warps.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
-
-#include <type_traits>
 
 #include "ep_experts_w4.cuh"
 
@@ -39,18 +36,11 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
-// NTMAX: most rows of x per expert, in eights.  Experts with at most 8 rows
-// have a kernel of their own: with their accumulators two blocks fit an SM.
-template <int NTMAX>
-struct Cfg {
-  static constexpr int kMT = NTMAX == 1 ? 4 : 2;   // 16-row weight tiles per warp
-  static constexpr int kStages = NTMAX == 1 ? 3 : 4;
-  static constexpr int kStage = kMT * 16 * 64;     // bytes of codes of a step
-  // a tile's partial sums, where warps share it, go to the stage just used;
-  // 32 rows of x do not fit there
-  static constexpr int kRed = NTMAX == 1 ? 0 : kMT * 16 * 8 * NTMAX * 4;
-  static constexpr int kSmem = kWarps * (kStages * kStage + kRed);
-};
+constexpr int kMT = 4;                     // 16-row weight tiles per warp
+constexpr int kTileRows = kMT * 16;
+constexpr int kStages = 3;                 // of a warp's codes
+constexpr int kStage = kTileRows * 64;     // bytes of codes of a step
+constexpr int kSmem = kWarps * kStages * kStage;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -132,22 +122,21 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
-// Row i * 8 + g of a tile of MT * 16 weight rows, relative to the tile's
+// Row i * 8 + g of a tile of weight rows, relative to the tile's
 // first: rows beyond the last channel read the last one (32-bit indices and
 // one multiply-add an address, instead of a pointer for each row).
-template <int MT, bool kSwiglu>
+template <bool kSwiglu>
 __device__ __forceinline__ uint32_t tile_row(int i, int g, int last, int N) {
   if (!kSwiglu) return (uint32_t)min(g + 8 * i, last);
-  return i < MT ? (uint32_t)min(g + 8 * i, last) : (uint32_t)(min(g + 8 * (i - MT), last) + N);
+  return i < kMT ? (uint32_t)min(g + 8 * i, last) : (uint32_t)(min(g + 8 * (i - kMT), last) + N);
 }
 
 // What a warp reads with its own lanes for the products of a tile: pointers
 // to this step's first byte, advanced from step to step.
-template <int NT>
 struct Sources {
-  const uint8_t* x[NT];         // rows of x: this lane's channels
-  const float* xs;              // scales of the expert's E4M3 rows, and which
-  uint32_t xrow[NT][2];
+  const uint8_t* x;             // the row of x: this lane's channels
+  const float* xs;              // scales of the expert's E4M3 rows, and which two
+  uint32_t xrow[2];
   const __nv_bfloat16* scale;   // scales and zero points of the tile's first row
   const uint8_t* zero;
   int last;                     // last row of the tile that is a channel
@@ -194,47 +183,45 @@ __device__ __forceinline__ uint32_t load_zeros(const uint8_t* p, int g0, bool ra
 }
 
 // The products of step s of a tile.  ragged: channels end within the step.
-template <int MT, int NT, int kStages, bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
-__device__ __forceinline__ void step_products(const ExpertsArgs& a, const Sources<NT>& src,
+template <bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
+__device__ __forceinline__ void step_products(const ExpertsArgs& a, const Sources& src,
                                               int s, bool ragged, uint32_t stage, int lane,
-                                              float (&acc)[MT][NT][4]) {
+                                              float (&acc)[kMT][4]) {
   constexpr int kPer = 128 / kGroup;
-  constexpr int MP = NT >= 2 ? 2 : MT;  // weight tiles at a time: what the registers hold
   const int g = lane >> 2, t = lane & 3;
   const uint32_t groups = (uint32_t)a.I / kGroup;
   // everything that comes from global memory goes out before the wait for
   // the codes
-  uint4 xv[NT][kFP8 ? 2 : 4];
+  uint4 xv[kFP8 ? 2 : 4];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // word_channel less this thread's own offset, which the pointer holds
-      const int k = word_channel<kGroup>(0, j);
-      if (kFP8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src.x[nt] + k));
-        (&xv[nt][j >> 1].x)[(j & 1) * 2] = v.x;
-        (&xv[nt][j >> 1].x)[(j & 1) * 2 + 1] = v.y;
-      } else if (!ragged) {
-        xv[nt][j] = __ldg(reinterpret_cast<const uint4*>(src.x[nt] + 2 * k));
-      } else {
-        xv[nt][j] = make_uint4(0, 0, 0, 0);
-        if (s * 128 + word_channel<kGroup>(t, j) < a.I)
-          xv[nt][j] = __ldg(reinterpret_cast<const uint4*>(src.x[nt] + 2 * k));
-      }
+  for (int j = 0; j < 4; ++j) {
+    // word_channel less this thread's own offset, which the pointer holds
+    const int k = word_channel<kGroup>(0, j);
+    if (kFP8) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(src.x + k));
+      (&xv[j >> 1].x)[(j & 1) * 2] = v.x;
+      (&xv[j >> 1].x)[(j & 1) * 2 + 1] = v.y;
+    } else if (!ragged) {
+      xv[kFP8 ? 0 : j] = __ldg(reinterpret_cast<const uint4*>(src.x + 2 * k));
+    } else {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (s * 128 + word_channel<kGroup>(t, j) < a.I)
+        v = __ldg(reinterpret_cast<const uint4*>(src.x + 2 * k));
+      xv[kFP8 ? 0 : j] = v;
     }
-  float xs[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) xs[nt][i] = kFP8 ? __ldg(src.xs + src.xrow[nt][i]) : 1.0f;
+  }
+  float xs[2] = {1.0f, 1.0f};
+  if (kFP8) {
+    xs[0] = __ldg(src.xs + src.xrow[0]);
+    xs[1] = __ldg(src.xs + src.xrow[1]);
+  }
   // a row's scales and zero points of this step, in one load each
-  uint32_t sv[MT][2][(kPer + 1) / 2], zv[MT][2];
+  uint32_t sv[kMT][2][(kPer + 1) / 2], zv[kMT][2];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint64_t at = (uint64_t)tile_row<MT, kSwiglu>(mt * 2 + h, g, src.last, a.N) * groups;
+      const uint64_t at = (uint64_t)tile_row<kSwiglu>(mt * 2 + h, g, src.last, a.N) * groups;
       load_scales<kPer>(src.scale + at, s * kPer, ragged, groups, sv[mt][h]);
       zv[mt][h] = 0x08080808u;
       if (kZeros) zv[mt][h] = load_zeros<kPer>(src.zero + at, s * kPer, ragged, groups);
@@ -242,79 +229,59 @@ __device__ __forceinline__ void step_products(const ExpertsArgs& a, const Source
   asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
   __syncwarp();
 
-  float ones[NT][kPer][4] = {};
+  float ones[4] = {}, part[kMT][4] = {};
 #pragma unroll
-  for (int m0 = 0; m0 < MT; m0 += MP) {
-    float part[MP][NT][4] = {};
+  for (int j = 0; j < 4; ++j) {
+    const int q = j / (4 / kPer);  // the word's group
+    uint32_t b[4];
+    if (kFP8) {
+      const uint4 v = xv[j >> 1];
+      pairs_e4m3(j & 1 ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y), b);
+    } else {
+      constexpr uint32_t k1 = 0x3F803F80u;  // ones
+      pairs_bf16(xv[kFP8 ? 0 : j], b);
+      mma_bf16(ones, k1, k1, k1, k1, b[0], b[1]);
+      mma_bf16(ones, k1, k1, k1, k1, b[2], b[3]);
+    }
+    const int byte = word_channel<kGroup>(t, j) / 2;
+    const uint32_t at = stage + ((byte >> 4 ^ chunk_swizzle(g)) << 4) + (byte & 15) + g * 64;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int q = j / (4 / kPer);  // the word's group
-      uint32_t b[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (kFP8) {
-          const uint4 v = xv[nt][j >> 1];
-          pairs_e4m3(j & 1 ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y), b[nt]);
-        } else {
-          constexpr uint32_t k1 = 0x3F803F80u;  // ones
-          pairs_bf16(xv[nt][kFP8 ? 0 : j], b[nt]);
-          if (m0 == 0) {
-            mma_bf16(ones[nt][q], k1, k1, k1, k1, b[nt][0], b[nt][1]);
-            mma_bf16(ones[nt][q], k1, k1, k1, k1, b[nt][2], b[nt][3]);
-          }
-        }
+    for (int mt = 0; mt < kMT; ++mt) {
+      const uint32_t w0 = lds32(at + mt * 1024), w1 = lds32(at + mt * 1024 + 512);
+      const uint32_t z0 = zv[mt][0] >> (8 * q) & 0xFF, z1 = zv[mt][1] >> (8 * q) & 0xFF;
+      uint32_t lo[4], hi[4];
+      if (kFP8) {
+        // -(1024 + z) and -(64 + z) as f16: 0xE400 | z, 0xD400 | z << 4
+        codes_f16(w0, 0xE400E400u | z0 * 0x00010001u, 0xD400D400u | z0 * 0x00100010u, lo);
+        codes_f16(w1, 0xE400E400u | z1 * 0x00010001u, 0xD400D400u | z1 * 0x00100010u, hi);
+        mma_f16(part[mt], lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
+        mma_f16(part[mt], lo[2], hi[2], lo[3], hi[3], b[2], b[3]);
+      } else {
+        codes_bf16(w0, lo);
+        codes_bf16(w1, hi);
+        mma_bf16(part[mt], lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
+        mma_bf16(part[mt], lo[2], hi[2], lo[3], hi[3], b[2], b[3]);
       }
-      // the words of both rows of the weight tiles; two at a time where a
-      // thread has two next to one another
-      const int byte = word_channel<kGroup>(t, j) / 2;
-      const uint32_t at = stage + ((byte >> 4 ^ chunk_swizzle(g)) << 4) + (byte & 15) + g * 64;
+    }
+    if ((j + 1) % (4 / kPer) == 0) {  // the end of a group
 #pragma unroll
-      for (int m = 0; m < MP; ++m) {
-        const int mt = m0 + m;
-        const uint32_t w0 = lds32(at + mt * 1024), w1 = lds32(at + mt * 1024 + 512);
+      for (int mt = 0; mt < kMT; ++mt) {
         const uint32_t z0 = zv[mt][0] >> (8 * q) & 0xFF, z1 = zv[mt][1] >> (8 * q) & 0xFF;
-        uint32_t lo[4], hi[4];
-        if (kFP8) {
-          // -(1024 + z) and -(64 + z) as f16: 0xE400 | z, 0xD400 | z << 4
-          codes_f16(w0, 0xE400E400u | z0 * 0x00010001u, 0xD400D400u | z0 * 0x00100010u, lo);
-          codes_f16(w1, 0xE400E400u | z1 * 0x00010001u, 0xD400D400u | z1 * 0x00100010u, hi);
-        } else {
-          codes_bf16(w0, lo);
-          codes_bf16(w1, hi);
-        }
+        const uint32_t w0 = sv[mt][0][q / 2], w1 = sv[mt][1][q / 2];
+        const float s0 = __uint_as_float(q & 1 ? w0 & 0xFFFF0000u : w0 << 16);
+        const float s1 = __uint_as_float(q & 1 ? w1 & 0xFFFF0000u : w1 << 16);
+        // -(128 + z): z << 16 is z in units of 128's last mantissa places
+        const float f0 = __uint_as_float(0xC3000000u | z0 << 16);
+        const float f1 = __uint_as_float(0xC3000000u | z1 << 16);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (kFP8) {
-            mma_f16(part[m][nt], lo[0], hi[0], lo[1], hi[1], b[nt][0], b[nt][1]);
-            mma_f16(part[m][nt], lo[2], hi[2], lo[3], hi[3], b[nt][2], b[nt][3]);
-          } else {
-            mma_bf16(part[m][nt], lo[0], hi[0], lo[1], hi[1], b[nt][0], b[nt][1]);
-            mma_bf16(part[m][nt], lo[2], hi[2], lo[3], hi[3], b[nt][2], b[nt][3]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float v = kFP8 ? part[mt][i] * xs[i & 1] : fmaf(i < 2 ? f0 : f1, ones[i], part[mt][i]);
+          acc[mt][i] = fmaf(v, i < 2 ? s0 : s1, acc[mt][i]);
+          part[mt][i] = 0.0f;
         }
       }
-      if ((j + 1) % (4 / kPer) == 0) {  // the end of a group
 #pragma unroll
-        for (int m = 0; m < MP; ++m) {
-          const int mt = m0 + m;
-          const uint32_t z0 = zv[mt][0] >> (8 * q) & 0xFF, z1 = zv[mt][1] >> (8 * q) & 0xFF;
-          const uint32_t w0 = sv[mt][0][q / 2], w1 = sv[mt][1][q / 2];
-          const float s0 = __uint_as_float(q & 1 ? w0 & 0xFFFF0000u : w0 << 16);
-          const float s1 = __uint_as_float(q & 1 ? w1 & 0xFFFF0000u : w1 << 16);
-          // -(128 + z): z << 16 is z in units of 128's last mantissa places
-          const float f0 = __uint_as_float(0xC3000000u | z0 << 16);
-          const float f1 = __uint_as_float(0xC3000000u | z1 << 16);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float v = kFP8 ? part[m][nt][i] * xs[nt][i & 1]
-                                   : fmaf(i < 2 ? f0 : f1, ones[nt][q][i], part[m][nt][i]);
-              acc[mt][nt][i] = fmaf(v, i < 2 ? s0 : s1, acc[mt][nt][i]);
-              part[m][nt][i] = 0.0f;
-            }
-        }
-      }
+      for (int i = 0; i < 4; ++i) ones[i] = 0.0f;
     }
   }
 }
@@ -325,17 +292,15 @@ struct Cursor {
   int item, s, e, n0;  // tile and step; the tile's expert and first output channel
 };
 
-template <int NTMAX, bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
-__global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 2 : 1) experts_kernel(ExpertsArgs a) {
-  using C = Cfg<NTMAX>;
-  constexpr int MT = C::kMT, kRows = MT * 16;
-  constexpr int kChannels = kSwiglu ? kRows / 2 : kRows;  // output channels of a tile
+template <bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
+__global__ void __launch_bounds__(kThreads, 2) experts_kernel(ExpertsArgs a) {
+  constexpr int kChannels = kSwiglu ? kTileRows / 2 : kTileRows;  // output channels of a tile
   pdl_wait_then_release();
-  extern __shared__ __align__(16) uint8_t smem[];  // stages, sums, then the live experts
+  extern __shared__ __align__(16) uint8_t smem[];  // stages, then the live experts
   __shared__ int warp_total[kWarps];
   __shared__ int live_total;
   __shared__ int used_slot[kWarps];  // the stage of a warp's last step
-  uint16_t* live = reinterpret_cast<uint16_t*>(smem + C::kSmem);
+  uint16_t* live = reinterpret_cast<uint16_t*>(smem + kSmem);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -346,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 2 : 1) experts_kernel(E
   for (int e0 = 0; e0 < a.E; e0 += kThreads) {
     const int e = e0 + tid;
     const int64_t n = e < a.E ? min((int64_t)a.count[e], a.cap) : 0;
-    const bool busy = NTMAX == 1 ? n > 0 && n <= 8 : n > 8 && n <= kFewRows;
+    const bool busy = n > 0 && n <= kFewRows;
     const unsigned bal = __ballot_sync(kFull, busy);
     if (lane == 0) warp_total[warp] = __popc(bal);
     __syncthreads();
@@ -374,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 2 : 1) experts_kernel(E
   }
   const int kw = warp % ks, team = warp / ks, teams = kWarps / ks;
   const int first = blockIdx.x * teams + team, stride = gridDim.x * teams;
-  const uint32_t stage0 = smem_addr(smem) + warp * C::kStages * C::kStage;
+  const uint32_t stage0 = smem_addr(smem) + warp * kStages * kStage;
 
   const auto enter = [&](Cursor& c) {
     if (c.item < items) {
@@ -400,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 2 : 1) experts_kernel(E
       // beyond the last channel: any bytes of the row, x is zero there
       const uint8_t* p = load.s * 128 + t * 32 < a.I ? codes : codes - load.s * 64 - t * 16;
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i)
+      for (int i = 0; i < 2 * kMT; ++i)
         copy16(stage + chunk + i * 512,
-               p + (uint64_t)tile_row<MT, kSwiglu>(i, g, last, a.N) * (uint32_t)(a.I / 2));
+               p + (uint64_t)tile_row<kSwiglu>(i, g, last, a.N) * (uint32_t)(a.I / 2));
       codes += ks * 64;
       load.s += ks;
       if (load.s >= steps) {
@@ -414,71 +379,60 @@ __global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 2 : 1) experts_kernel(E
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) issue(stage0 + i * C::kStage);
+  for (int i = 0; i < kStages - 1; ++i) issue(stage0 + i * kStage);
   int slot = 0;
 
-  // one tile times the rows of its expert
-  const auto tile = [&](auto nt_tag, int nrows) {
-    constexpr int NT = decltype(nt_tag)::value;
-    Sources<NT> src;
+  while (use.item < items) {
+    const int nrows = (int)min((int64_t)a.count[use.e], a.cap);
+    Sources src;
     {
       const int64_t row = (int64_t)use.e * a.cap;
       const int64_t at = ((int64_t)use.e * a.rows + use.n0) * groups + use.s * (128 / kGroup);
+      src.x = a.x + ((row + min(g, nrows - 1)) * a.I + use.s * 128 + word_channel<kGroup>(t, 0)) *
+                        (kFP8 ? 1 : 2);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        src.x[nt] = a.x + ((row + min(nt * 8 + g, nrows - 1)) * a.I + use.s * 128 +
-                           word_channel<kGroup>(t, 0)) * (kFP8 ? 1 : 2);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) src.xrow[nt][i] = (uint32_t)(min(nt * 8 + 2 * t + i, nrows - 1) * steps);
-      }
+      for (int i = 0; i < 2; ++i) src.xrow[i] = (uint32_t)(min(2 * t + i, nrows - 1) * steps);
       src.xs = kFP8 ? a.x_scales + row * steps + use.s : nullptr;
       src.scale = a.scales + at;
       src.zero = a.zeros + at;
       src.last = min(kChannels, a.N - use.n0) - 1;
     }
-    float acc[MT][NT][4] = {};
+    float acc[kMT][4] = {};
     for (; use.s < steps; use.s += ks) {
-      const uint32_t stage = stage0 + slot * C::kStage;
-      step_products<MT, NT, C::kStages, kFP8, kSwiglu, kGroup, kZeros>(
-          a, src, use.s, !kFP8 && use.s * 128 + 128 > a.I, stage, lane, acc);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) src.x[nt] += ks * 128 * (kFP8 ? 1 : 2);
+      step_products<kFP8, kSwiglu, kGroup, kZeros>(a, src, use.s, !kFP8 && use.s * 128 + 128 > a.I,
+                                                   stage0 + slot * kStage, lane, acc);
+      src.x += ks * 128 * (kFP8 ? 1 : 2);
       src.xs += ks;
       src.scale += ks * (128 / kGroup);
       src.zero += ks * (128 / kGroup);
       __syncwarp();
-      issue(stage0 + (slot == 0 ? C::kStages - 1 : slot - 1) * C::kStage);
-      slot = slot == C::kStages - 1 ? 0 : slot + 1;
+      issue(stage0 + (slot == 0 ? kStages - 1 : slot - 1) * kStage);
+      slot = slot == kStages - 1 ? 0 : slot + 1;
     }
     __nv_bfloat16* y = a.y + (int64_t)use.e * a.cap * a.N;
     if (ks > 1) {
       // the team's sums meet in shared memory: each warp's in the stage that
       // its last step used (the next copy into it is a step away)
-      if (lane == 0) used_slot[warp] = slot == 0 ? C::kStages - 1 : slot - 1;
+      if (lane == 0) used_slot[warp] = slot == 0 ? kStages - 1 : slot - 1;
       __syncwarp();
-      constexpr int kCols = 8 * NT;
       const auto sums = [&](int w) {
-        return reinterpret_cast<float*>(
-            C::kRed ? smem + kWarps * C::kStages * C::kStage + w * C::kRed
-                    : smem + (w * C::kStages + used_slot[w]) * C::kStage);
+        return reinterpret_cast<float*>(smem + (w * kStages + used_slot[w]) * kStage);
       };
       float* mine = sums(warp);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float2*>(mine + (mt * 16 + h * 8 + g) * kCols + nt * 8 + 2 * t) =
-                make_float2(acc[mt][nt][2 * h], acc[mt][nt][2 * h + 1]);
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(mine + (mt * 16 + h * 8 + g) * 8 + 2 * t) =
+              make_float2(acc[mt][2 * h], acc[mt][2 * h + 1]);
       asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(ks * 32) : "memory");
       for (int i = kw * 32 + lane; i < kChannels * nrows; i += ks * 32) {
         const int ch = i % kChannels, r = i / kChannels;
         float v0 = 0.0f, v1 = 0.0f;
         for (int k = 0; k < ks; ++k) {
           const float* p = sums(team * ks + k);
-          v0 += p[ch * kCols + r];
-          if (kSwiglu) v1 += p[(kChannels + ch) * kCols + r];
+          v0 += p[ch * 8 + r];
+          if (kSwiglu) v1 += p[(kChannels + ch) * 8 + r];
         }
         if (kSwiglu) v0 = v0 / (1.0f + expf(-v0)) * v1;
         if (use.n0 + ch < a.N) y[(int64_t)r * a.N + use.n0 + ch] = __float2bfloat16_rn(v0);
@@ -486,38 +440,26 @@ __global__ void __launch_bounds__(kThreads, NTMAX == 1 ? 2 : 1) experts_kernel(E
       asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(ks * 32) : "memory");
     } else {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * t + (i & 1), ch = use.n0 + (i >> 1) * 8 + g;
+        if (r >= nrows) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = nt * 8 + 2 * t + (i & 1), ch = use.n0 + (i >> 1) * 8 + g;
-          if (r >= nrows) continue;
-#pragma unroll
-          for (int mt = 0; mt < (kSwiglu ? MT / 2 : MT); ++mt) {
-            float v = acc[mt][nt][i];
-            if (kSwiglu) v = v / (1.0f + expf(-v)) * acc[mt + MT / 2][nt][i];
-            if (ch + mt * 16 < a.N) y[(int64_t)r * a.N + ch + mt * 16] = __float2bfloat16_rn(v);
-          }
+        for (int mt = 0; mt < (kSwiglu ? kMT / 2 : kMT); ++mt) {
+          float v = acc[mt][i];
+          if (kSwiglu) v = v / (1.0f + expf(-v)) * acc[mt + kMT / 2][i];
+          if (ch + mt * 16 < a.N) y[(int64_t)r * a.N + ch + mt * 16] = __float2bfloat16_rn(v);
         }
+      }
     }
-  };
-  while (use.item < items) {
-    const int nrows = (int)min((int64_t)a.count[use.e], a.cap);
-    if (NTMAX == 1)
-      tile(std::integral_constant<int, 1>{}, nrows);
-    else if (nrows <= 16)
-      tile(std::integral_constant<int, NTMAX == 1 ? 1 : 2>{}, nrows);
-    else
-      tile(std::integral_constant<int, NTMAX>{}, nrows);
     use.item += stride;
     enter(use);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int NTMAX, bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
+template <bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
 ep_status_t launch_small(ExpertsArgs a, cudaStream_t st) {
-  using C = Cfg<NTMAX>;
-  const auto kernel = experts_kernel<NTMAX, kFP8, kSwiglu, kGroup, kZeros>;
+  const auto kernel = experts_kernel<kFP8, kSwiglu, kGroup, kZeros>;
   DeviceProps props;
   if (!device_props(&props)) return EP_ERR_CUDA;
   static std::mutex mu;
@@ -529,8 +471,8 @@ ep_status_t launch_small(ExpertsArgs a, cudaStream_t st) {
     if (resident[dev] == 0) {
       int n = 0;
       if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               C::kSmem + EP_MAX_EXPERTS * 2) != cudaSuccess ||
-          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, C::kSmem + 1024) !=
+                               kSmem + EP_MAX_EXPERTS * 2) != cudaSuccess ||
+          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, kSmem + 1024) !=
               cudaSuccess ||
           n < 1)
         return EP_ERR_CUDA;
@@ -538,30 +480,23 @@ ep_status_t launch_small(ExpertsArgs a, cudaStream_t st) {
     }
     blocks = resident[dev];
   }
-  constexpr int kChannels = C::kMT * (kSwiglu ? 8 : 16);
+  constexpr int kChannels = kTileRows / (kSwiglu ? 2 : 1);
   a.tiles = (a.N + kChannels - 1) / kChannels;
-  launch_pdl(kernel, (unsigned)(blocks * props.sm_count), kThreads, C::kSmem + (size_t)a.E * 2, st, a);
+  launch_pdl(kernel, (unsigned)(blocks * props.sm_count), kThreads, kSmem + (size_t)a.E * 2, st, a);
   return launch_status();
 }
 
-template <bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
-ep_status_t launch_zeros(const ExpertsArgs& a, cudaStream_t st) {
-  const ep_status_t s = launch_small<1, kFP8, kSwiglu, kGroup, kZeros>(a, st);
-  if (s != EP_OK || a.cap <= 8) return s;
-  return launch_small<4, kFP8, kSwiglu, kGroup, kZeros>(a, st);
-}
-
 template <bool kFP8, bool kSwiglu, int kGroup>
-ep_status_t launch_rows(const ExpertsArgs& a, cudaStream_t st) {
-  return a.zeros ? launch_zeros<kFP8, kSwiglu, kGroup, true>(a, st)
-                 : launch_zeros<kFP8, kSwiglu, kGroup, false>(a, st);
+ep_status_t launch_zeros(const ExpertsArgs& a, cudaStream_t st) {
+  return a.zeros ? launch_small<kFP8, kSwiglu, kGroup, true>(a, st)
+                 : launch_small<kFP8, kSwiglu, kGroup, false>(a, st);
 }
 
 template <bool kFP8, bool kSwiglu>
 ep_status_t launch_group(const ExpertsArgs& a, int group, cudaStream_t st) {
-  if (group == 32) return launch_rows<kFP8, kSwiglu, 32>(a, st);
-  if (group == 64) return launch_rows<kFP8, kSwiglu, 64>(a, st);
-  return launch_rows<kFP8, kSwiglu, 128>(a, st);
+  if (group == 32) return launch_zeros<kFP8, kSwiglu, 32>(a, st);
+  if (group == 64) return launch_zeros<kFP8, kSwiglu, 64>(a, st);
+  return launch_zeros<kFP8, kSwiglu, 128>(a, st);
 }
 
 }  // namespace

@@ -18,9 +18,9 @@
 //   warp 2       TMA of the weight codes (128 rows x 64 bytes)
 //   warp 3       group scales, zero points and scales of E4M3 rows, by
 //                4-byte asynchronous copies into shared memory
-//   warps 4-11   codes -> integers -> operand A; each four of them take
-//                every other step of 128 channels
-//   warps 12-19  sums -> scaled -> registers, each four of them for half of
+//   then         four warps (E4M3: two times four, a step each in turn): codes
+//                -> integers -> operand A
+//   and eight    sums -> scaled -> registers, each four of them for half of
 //                the rows; the epilogue
 // Every wait is bounded; a block whose wait runs out reports
 // EP_ERRBIT_TIMEOUT and leaves.
@@ -31,10 +31,7 @@
 namespace ep {
 namespace {
 
-constexpr int kTeams = 2;  // teams of four warps that unpack codes, a step each in turn
 constexpr int kParts = 2;  // teams of four warps that add up sums, a part of the rows each
-constexpr int kThreads = 128 * (1 + kTeams + kParts);
-constexpr int kLaunchRegs = 96;  // per thread: what the register split draws on
 constexpr int kBoxes = 6;  // x is loaded in boxes of 32, 64, ... 192 rows
 constexpr int kWBytes = 8192;   // 128 weight rows x 64 bytes
 constexpr unsigned kFull = 0xFFFFFFFFu;
@@ -43,13 +40,24 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 // one slot of scales.
 template <bool kFP8, int kGroup>
 struct Cfg {
+  // teams of four warps that unpack codes, a step each in turn: E4M3 codes
+  // take 13 integer instructions for 8, bf16 9
+  static constexpr int kTeams = kFP8 ? 2 : 1;
+  static constexpr int kThreads = 128 * (1 + kTeams + kParts);
+  // registers per thread: at launch, then for the copying, unpacking and
+  // summing warps; the split draws on what the launch gave
+  static constexpr int kLaunchRegs = kTeams == 2 ? 96 : 128;
+  static constexpr int kRegsCopy = 56, kRegsUnpack = kTeams == 2 ? 56 : 104;
+  static constexpr int kRegsSum = kTeams == 2 ? 152 : 176;
+  static_assert(128 * (kRegsCopy + kTeams * kRegsUnpack + kParts * kRegsSum) <=
+                    kThreads * kLaunchRegs, "the split would wait for ever");
   // rows of x per block: what the accumulators of two teams hold in registers
   // without moves (E4M3 rows need registers for their scales as well)
   static constexpr int kRows = kFP8 ? 160 : 192;
   static constexpr int kPart = kRows / kParts;
   static constexpr int kXBytes = kRows * (kFP8 ? 128 : 256);
-  static constexpr int kStagesX = kFP8 ? 5 : 3;
-  static constexpr int kStagesW = kFP8 ? 8 : 6;
+  static constexpr int kStagesX = kFP8 ? 4 : 3;  // at least kSlotsA
+  static constexpr int kStagesW = 8;
   static constexpr int kColsA = kFP8 ? 32 : 64;  // tensor-memory columns per slot of A
   static constexpr int kSlotsA = 128 / kColsA;
   static constexpr int kPerStep = 128 / kGroup;  // groups in a step
@@ -176,16 +184,20 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
       : "memory");
 }
 
-// The load and its wait in one statement, so that no use moves between them.
+// The registers are written when tmem_wait returns; what uses them is volatile
+// too, and so stays behind it.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      "%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(addr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 // Waits for the phase of the barrier at `bar` (a shared address) with the
@@ -195,22 +207,31 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
 // (Four instructions a try: the warps that wait share their schedulers with
 // those that work.)
 constexpr uint32_t kTries = 1u << 22;
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
-  uint32_t left;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "mov.u32 %0, %3;\n"
-      "TRY:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %4;\n\t"
-      "@P bra DONE;\n\t"
-      "sub.u32 %0, %0, 1;\n\t"
-      "setp.ne.u32 P, %0, 0;\n\t"
-      "@P bra TRY;\n"
-      "DONE:\n\t}"
-      : "=&r"(left)
-      : "r"(bar), "r"(parity), "r"(kTries), "r"(1000u)
-      : "memory");
+#define EP_WAIT(kPause)                                                       \
+  uint32_t left;                                                              \
+  asm volatile(                                                               \
+      "{\n\t.reg .pred P;\n\t"                                                \
+      "mov.u32 %0, %3;\n"                                                     \
+      "TRY:\n\t"                                                              \
+      "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %4;\n\t"         \
+      "@P bra DONE;\n\t" kPause                                               \
+      "sub.u32 %0, %0, 1;\n\t"                                                \
+      "setp.ne.u32 P, %0, 0;\n\t"                                             \
+      "@P bra TRY;\n"                                                         \
+      "DONE:\n\t}"                                                            \
+      : "=&r"(left)                                                           \
+      : "r"(bar), "r"(parity), "r"(kTries), "r"(1000u)                        \
+      : "memory");                                                            \
   return left != 0;
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) { EP_WAIT("") }
+// For warps that run ahead of the others: their tries leave the schedulers to
+// those that are waited for.
+__device__ __forceinline__ bool wait_idle(uint32_t bar, uint32_t parity) {
+  EP_WAIT("nanosleep.u32 64;\n\t")
+}
+#undef EP_WAIT
+__device__ __forceinline__ bool wait_idle(uint64_t* bar, uint32_t parity) {
+  return wait_idle(smem_addr(bar), parity);
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   return wait(smem_addr(bar), parity);
@@ -289,7 +310,7 @@ __device__ __forceinline__ float2 unpack2(uint64_t v) {
 
 // What the loop over the groups of an item needs.
 struct SumArgs {
-  uint32_t sfull, sempty, pfull, pempty;  // barriers (shared addresses)
+  uint32_t sempty, pfull, pempty;  // barriers (shared addresses)
   uint32_t scale, xs;                     // this lane's scale words, this part's row scales
   uint32_t src;                           // this part's columns of sums
   uint32_t odd;                           // whether the lane's first group is a word's high half
@@ -308,9 +329,9 @@ __device__ __forceinline__ bool add_groups(const SumArgs& s, int lane, uint32_t&
   for (int g = 0; g < s.groups; ++g) {
     const uint32_t slot = n % C::kSlotsS, buf = p & 1;
     const uint32_t in = C::kPerStep == 1 ? 0 : g % C::kPerStep;
-    bool fine = true;
-    if (in == 0) fine = wait(s.sfull + slot * 8, n / C::kSlotsS & 1);
-    fine &= wait(s.pfull + buf * 8, p >> 1 & 1);
+    // (the scales are there too: the warp that arrives here has waited for the
+    // unpacked codes, whose warps have waited for the scales)
+    const bool fine = wait(s.pfull + buf * 8, p >> 1 & 1);
     if (__any_sync(kFull, !fine)) return false;
     fence_after();
     // bf16 -> float32 is a shift; the word holds groups 2i and 2i + 1
@@ -319,22 +340,26 @@ __device__ __forceinline__ bool add_groups(const SumArgs& s, int lane, uint32_t&
     uint64_t scale;
     asm("mov.b64 %0, {%1, %1};" : "=l"(scale) : "r"(sv));
     const uint32_t src = s.src + buf * C::kRows, xs = s.xs + slot * C::kSWords * 4;
+    uint32_t v[2][16];
+    tmem_ld16(src, v[0]);
+    tmem_wait_ld();
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      uint32_t v[16];
-      tmem_ld16(src + c * 16, v);
+      const uint32_t(&u)[16] = v[c & 1];
+      if (c + 1 < kChunks) tmem_ld16(src + (c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         if (kFP8) {
           uint64_t x0, x1;
           lds_pairs(xs + c * 64 + i * 4, x0, x1);
-          add2(acc[c * 8 + i / 2], v[i], v[i + 1], x0, scale);
-          add2(acc[c * 8 + i / 2 + 1], v[i + 2], v[i + 3], x1, scale);
+          add2(acc[c * 8 + i / 2], u[i], u[i + 1], x0, scale);
+          add2(acc[c * 8 + i / 2 + 1], u[i + 2], u[i + 3], x1, scale);
         } else {
-          add2(acc[c * 8 + i / 2], v[i], v[i + 1], scale);
-          add2(acc[c * 8 + i / 2 + 1], v[i + 2], v[i + 3], scale);
+          add2(acc[c * 8 + i / 2], u[i], u[i + 1], scale);
+          add2(acc[c * 8 + i / 2 + 1], u[i + 2], u[i + 3], scale);
         }
       }
+      if (c + 1 < kChunks) tmem_wait_ld();
     }
     fence_before();
     __syncwarp();
@@ -406,7 +431,7 @@ __device__ __forceinline__ int64_t lane_row(const ExpertsArgs& a, const Item& it
 }
 
 template <bool kFP8, bool kSwiglu, int kGroup>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
     experts_tc_kernel(ExpertsArgs a, const __grid_constant__ XMaps xmaps,
                       const __grid_constant__ CUtensorMap wmap) {
   using C = Cfg<kFP8, kGroup>;
@@ -428,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::kStagesX; ++i) mbar_init(&bar.full[i], 5), mbar_init(&bar.done[i], 1);
     for (int i = 0; i < C::kStagesW; ++i) mbar_init(&bar.wfull[i], 1), mbar_init(&bar.wempty[i], 4);
     for (int i = 0; i < C::kSlotsS; ++i) mbar_init(&bar.sfull[i], 32), mbar_init(&bar.sempty[i], 4 * kParts + 4);
-    for (int i = 0; i < 2; ++i) mbar_init(&bar.pfull[i], 1), mbar_init(&bar.pempty[i], 4 * kParts);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.pfull[i], 2), mbar_init(&bar.pempty[i], 4 * kParts);
     fence_barrier_init();
     abort_flag = 0;
   }
@@ -466,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsCopy));
     if (warp == 0 && lane == 0) {  // x tiles
       Ring<C::kStagesX> rx;
       for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
@@ -474,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap* map = &xmaps.rows[it.np / (32 / kParts) - 1];
         const uint32_t bytes = (uint32_t)(kParts * it.np) * (kFP8 ? 128 : 256);
         for (int b = 0; b < steps; ++b) {
-          ok = wait(&bar.done[rx.slot], rx.round ^ 1);
+          ok = wait_idle(&bar.done[rx.slot], rx.round ^ 1);
           if (!ok) break;
           uint8_t* dst = sx + rx.slot * C::kXBytes;
           mbar_arrive_expect_tx(&bar.full[rx.slot], bytes);
@@ -514,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           idesc, j > 0);
               }
               commit(&bar.pfull[rp.slot]);
+              mbar_arrive(&bar.pfull[rp.slot]);  // releases what this warp has waited for
               if (g == here - 1) commit(&bar.done[rx.slot]);
             }
             __syncwarp();
@@ -535,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
         const int row0 = it.e * a.rows + it.tile * (kSwiglu ? 64 : 128);
         for (int b = 0; b < steps; ++b) {
-          ok = wait(&bar.wempty[rw.slot], rw.round ^ 1);
+          ok = wait_idle(&bar.wempty[rw.slot], rw.round ^ 1);
           if (!ok) break;
           uint8_t* dst = sw + rw.slot * kWBytes;
           mbar_arrive_expect_tx(&bar.wfull[rw.slot], kWBytes);
@@ -553,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) at[i] = lane_row<kSwiglu>(a, it, lane + 32 * i) * groups;
         for (int b = 0; b < steps; ++b) {
-          ok = wait(&bar.sempty[rs.slot], rs.round ^ 1);
+          ok = wait_idle(&bar.sempty[rs.slot], rs.round ^ 1);
           if (!__all_sync(kFull, ok)) {
             ok = false;
             break;
@@ -584,8 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) give_up();
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
-  } else if (warp < 4 + 4 * kTeams) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  } else if (warp < 4 + 4 * C::kTeams) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsUnpack));
     // codes -> operand A: this thread's weight row is lane 32 * quad + lane of
     // tensor memory
     const int team = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
@@ -595,72 +621,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t zero_addr = smem_addr(ss) + (128 + r) * 4;
     const uint32_t table_addr = smem_addr(tables);
     const uint32_t a_addr = tmem_a + ((uint32_t)(quad * 32) << 16);
-    Ring<C::kStagesX> rx;  // the stage of this step, and of the one that used its slot of A
-    Ring<C::kStagesX> rd;
-    Ring<C::kStagesW> rw;
-    uint32_t n = 0;  // steps
+    const uint32_t wfull0 = smem_addr(bar.wfull), sfull0 = smem_addr(bar.sfull);
+    const uint32_t done0 = smem_addr(bar.done);
+    uint32_t base = 0;  // steps of the items before
     for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
       const int at4 = (int)(lane_row<kSwiglu>(a, it, r) * groups & 3);
-      for (int b = 0; b < steps; ++b, ++n) {
-        if (n % kTeams == (uint32_t)team) {
-          const uint32_t ss_slot = n % C::kSlotsS;
-          bool fine = wait(&bar.wfull[rw.slot], rw.round);
-          fine &= wait(&bar.sfull[ss_slot], n / C::kSlotsS & 1);
-          if (n >= C::kSlotsA) fine &= wait(&bar.done[rd.slot], rd.round);
-          if (__any_sync(kFull, !fine)) {
-            ok = false;
-            break;
-          }
-          fence_after();
-          const uint32_t src = row_addr + rw.slot * kWBytes;
-          const uint32_t dst = a_addr + n % C::kSlotsA * C::kColsA;
-          uint32_t zero = 8;
-#pragma unroll(kFP8 ? 4 : 2)
-          for (int i = 0; i < 4; ++i) {  // 32 channels
-            const uint4 w = lds128(src + (i << 4 ^ swz));
-            if (i % (4 / kPerStep) == 0 && a.zeros) {  // the next group's zero point
+      for (int b = (int)((team + base) % C::kTeams); b < steps; b += C::kTeams) {
+        const uint32_t n = base + b, was = n - C::kSlotsA;  // the step that had the slot of A
+        const uint32_t w_slot = n % C::kStagesW, s_slot = n % C::kSlotsS;
+        bool fine = wait_idle(wfull0 + w_slot * 8, n / C::kStagesW & 1);
+        fine &= wait_idle(sfull0 + s_slot * 8, n / C::kSlotsS & 1);
+        if (n >= C::kSlotsA)
+          fine &= wait_idle(done0 + was % C::kStagesX * 8, was / C::kStagesX & 1);
+        if (__any_sync(kFull, !fine)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint32_t src = row_addr + w_slot * kWBytes;
+        const uint32_t dst = a_addr + n % C::kSlotsA * C::kColsA;
+        uint32_t zero = 8;
+        uint4 t = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 32 channels
+          const uint4 w = lds128(src + (i << 4 ^ swz));
+          if (i % (4 / kPerStep) == 0) {  // the next group's zero point
+            if (a.zeros) {
               const int g = i * kPerStep / 4;
               const int gi = at4 + min(b * kPerStep + g, groups - 1);
-              zero = lds32(zero_addr + ss_slot * C::kSWords * 4 + g * 1024) >> (8 * (gi & 3)) & 15;
+              zero = lds32(zero_addr + s_slot * C::kSWords * 4 + g * 1024) >> (8 * (gi & 3)) & 15;
             }
-            if (kFP8) {
-              const uint4 t = lds128(table_addr + zero * 16);
-              uint32_t v[8];
-              codes_e4m3(w.x, t, v);
-              codes_e4m3(w.y, t, v + 2);
-              codes_e4m3(w.z, t, v + 4);
-              codes_e4m3(w.w, t, v + 6);
-              tmem_st8(dst + i * 8, v);
-            } else {
-              const uint32_t zp = 0x43004300u | zero * 0x00010001u;
-              uint32_t v[16];
-              codes_bf16(w.x, zp, v);
-              codes_bf16(w.y, zp, v + 4);
-              codes_bf16(w.z, zp, v + 8);
-              codes_bf16(w.w, zp, v + 12);
-              tmem_st16(dst + i * 16, v);
-            }
+            if (kFP8) t = lds128(table_addr + zero * 16);
           }
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-          fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bar.full[rx.slot]);
-            mbar_arrive(&bar.wempty[rw.slot]);
-            mbar_arrive(&bar.sempty[ss_slot]);
+          if (kFP8) {
+            uint32_t v[8];
+            codes_e4m3(w.x, t, v);
+            codes_e4m3(w.y, t, v + 2);
+            codes_e4m3(w.z, t, v + 4);
+            codes_e4m3(w.w, t, v + 6);
+            tmem_st8(dst + i * 8, v);
+          } else {
+            const uint32_t zp = 0x43004300u | zero * 0x00010001u;
+            uint32_t v[16];
+            codes_bf16(w.x, zp, v);
+            codes_bf16(w.y, zp, v + 4);
+            codes_bf16(w.z, zp, v + 8);
+            codes_bf16(w.w, zp, v + 12);
+            tmem_st16(dst + i * 16, v);
           }
         }
-        rx.next();
-        rw.next();
-        if (n >= C::kSlotsA) rd.next();
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar.full[n % C::kStagesX]);
+          mbar_arrive(&bar.wempty[w_slot]);
+          mbar_arrive(&bar.sempty[s_slot]);
+        }
       }
+      base += steps;
     }
     if (!ok) give_up();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    const int h = (warp - 4 - 4 * kTeams) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSum));
+    const int h = (warp - 4 - 4 * C::kTeams) >> 2, quad = warp & 3, r = quad * 32 + lane;
     SumArgs sum;
-    sum.sfull = smem_addr(bar.sfull);
     sum.sempty = smem_addr(bar.sempty);
     sum.pfull = smem_addr(bar.pfull);
     sum.pempty = smem_addr(bar.pempty);
@@ -779,7 +804,7 @@ ep_status_t launch(ExpertsArgs a, cudaStream_t st) {
     if (!ready[dev]) {
       // the register split draws on what the block was launched with
       cudaFuncAttributes fa;
-      if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs < kLaunchRegs ||
+      if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs < C::kLaunchRegs ||
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
               cudaSuccess)
         return EP_ERR_CUDA;
@@ -799,7 +824,7 @@ ep_status_t launch(ExpertsArgs a, cudaStream_t st) {
     return EP_ERR_CUDA;
   const int width = kSwiglu ? 64 : 128;
   a.tiles = (a.N + width - 1) / width;
-  launch_pdl(kernel, props.sm_count, kThreads, C::kSmem, st, a, xmaps, wmap);
+  launch_pdl(kernel, props.sm_count, C::kThreads, C::kSmem, st, a, xmaps, wmap);
   return launch_status();
 }
 
