@@ -188,7 +188,14 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without building a Stream object (2 us a call on
+# the host of a GB300), where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device):
+    if _raw_stream is not None and device.index is not None:
+        return C.c_void_p(_raw_stream(device.index))
     return C.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
@@ -199,7 +206,7 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
         raise EPError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise EPError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise EPError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 

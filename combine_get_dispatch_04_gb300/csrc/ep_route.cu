@@ -1,11 +1,12 @@
 // ep_route.cu -- the router (logits -> topk_idx, topk_weights) and its
 // gradient.
 //
-// One warp per token.  Lane j holds VPL consecutive experts, so that among
-// equal keys the lowest lane, and in it the lowest register, is the lowest
-// index.  Keys are kept as unsigned integers in the keys' order (0: not to be
-// chosen), so that one warp-wide integer maximum finds the best key of a
-// round; K rounds give the choice in descending order.
+// The choice takes more instructions than bytes, so a warp works on as many
+// tokens as fit: LANES lanes hold a token, VPL consecutive experts each, and
+// all tokens of the warp go through the same rounds.  Keys are kept as
+// unsigned integers in the keys' order (0: not to be chosen); a round finds
+// the largest key of the token and then the lowest index that has it, K
+// rounds give the choice in descending order.
 #include <cuda_bf16.h>
 
 #include "ep_common.cuh"
@@ -67,55 +68,100 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// Lane k < K holds the chosen expert of slot k (-1: none); writes the slots.
+// The weights of the slots of one token, by the LANES lanes that hold it.
+// slots: this token's chosen experts (-1: none); u: room for K scores.
 // m, z: the softmax's maximum and sum (read when !renorm && !sigmoid).
-template <bool kBF16>
-__device__ __forceinline__ void write_slots(const RouteArgs& a, int64_t t, int lane, int mine,
-                                            float m, float z) {
-  const bool live = lane < a.K && mine >= 0;
-  const float l = live ? load_logit<kBF16>(a.logits, t * a.stride + mine) : -INFINITY;
-  float u = 0.0f;
-  if (a.sigmoid) {
-    u = live ? sigmoid_rn(l) : 0.0f;
-  } else if (a.renorm) {
-    const float top = warp_max(l);
-    u = live ? exp_from(l, top) : 0.0f;
-  } else {
-    u = live ? exp_from(l, m) / z : 0.0f;
+template <int LANES, bool kBF16>
+__device__ __forceinline__ void write_slots(const RouteArgs& a, int64_t t, bool in, int sl,
+                                            const int* slots, float* u, float m, float z) {
+  float top = -INFINITY, sum = 0.0f;
+  if (!a.sigmoid && a.renorm) {
+    for (int k = sl; k < a.K; k += LANES)
+      if (slots[k] >= 0) top = fmaxf(top, load_logit<kBF16>(a.logits, t * a.stride + slots[k]));
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
   }
-  if (a.renorm) {
-    const float s = warp_sum(u);
-    u = s > 0.0f ? u / s : 0.0f;
+  for (int k = sl; k < a.K; k += LANES) {
+    float v = 0.0f;
+    if (slots[k] >= 0) {
+      const float l = load_logit<kBF16>(a.logits, t * a.stride + slots[k]);
+      v = a.sigmoid ? sigmoid_rn(l) : a.renorm ? exp_from(l, top) : exp_from(l, m) / z;
+    }
+    u[k] = v;
+    sum += v;
   }
-  if (lane < a.K) {
-    a.idx[t * a.K + lane] = mine;
-    a.w[t * a.K + lane] = u * a.scale;
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  if (!in) return;
+  for (int k = sl; k < a.K; k += LANES) {
+    a.idx[t * a.K + k] = slots[k];
+    a.w[t * a.K + k] = (a.renorm ? (sum > 0.0f ? u[k] / sum : 0.0f) : u[k]) * a.scale;
   }
 }
 
-// E <= 32 * VPL, groups (if any) of a power of two of whole lanes.
+// This lane's VPL logits (-inf beyond E).  vec: rows are 16-byte aligned and
+// hold whole lanes.
 template <int VPL, bool kBF16>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, int group_lanes) {
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t row, int e0, bool vec,
+                                            float (&l)[VPL]) {
+  if (VPL == 8 && vec) {
+    if (e0 < a.E) {
+      if (kBF16) {
+        const int4 v = __ldg(reinterpret_cast<const int4*>(
+            static_cast<const __nv_bfloat16*>(a.logits) + row + e0));
+        float f[8];
+        unpack_bf16x8(v, f);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) l[i] = f[i & 7];
+      } else {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + row + e0);
+        const float4 v[2] = {__ldg(p), __ldg(p + 1)};
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) l[i] = (&v[i >> 2 & 1].x)[i & 3];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) l[i] = -INFINITY;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    l[i] = e0 + i < a.E ? load_logit<kBF16>(a.logits, row + e0 + i) : -INFINITY;
+}
+
+// E <= LANES * VPL, groups (if any) of a power of two of whole lanes.
+// kPacked: bf16 logits are the keys, so a key's high half says all, and its low
+// half can hold the index: one maximum gives both (28 instead of 52 integer
+// instructions a round at 8 experts a lane).
+template <int LANES, int VPL, bool kBF16, bool kPacked>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, int group_lanes, bool vec) {
   pdl_wait_then_release();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const int e0 = lane * VPL;
+  constexpr int kTokens = 32 / LANES;  // of a warp
+  __shared__ int slots[kWarps][kTokens][EP_MAX_TOPK];
+  __shared__ float score[kWarps][kTokens][EP_MAX_TOPK];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sl = lane % LANES, mine = lane / LANES, lane0 = lane - sl;
+  const int64_t first = ((int64_t)blockIdx.x * kWarps + warp) * kTokens;
+  if (first >= a.T) return;  // the whole warp
+  const bool in = first + mine < a.T;
+  const int64_t t = in ? first + mine : a.T - 1;  // lanes without a token repeat the last one
+  const int e0 = sl * VPL;
 
   float l[VPL];
-#pragma unroll
-  for (int v = 0; v < VPL; ++v)
-    l[v] = e0 + v < a.E ? load_logit<kBF16>(a.logits, t * a.stride + e0 + v) : -INFINITY;
+  load_logits<VPL, kBF16>(a, t * a.stride, e0, vec, l);
 
   float m = -INFINITY, z = 1.0f;
   if (!a.sigmoid && (a.bias || !a.renorm)) {
 #pragma unroll
     for (int v = 0; v < VPL; ++v) m = fmaxf(m, l[v]);  // fmaxf passes over NaN
-    m = warp_max(m);
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     z = 0.0f;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) z += l[v] > -INFINITY ? exp_from(l[v], m) : 0.0f;
-    z = warp_sum(z);
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
   }
   uint32_t key[VPL];
 #pragma unroll
@@ -129,7 +175,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, int gro
     key[v] = l[v] > -INFINITY ? ordered(c) : 0u;  // false for NaN
   }
 
-  if (a.G > 1) {
+  if (!kPacked && a.G > 1) {
     uint32_t m1 = 0, m2 = 0;  // the two largest keys of the group
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
@@ -143,11 +189,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, int gro
     }
     float g = from_ordered(m1);
     if (a.sigmoid && m2) g = __fadd_rn(g, from_ordered(m2));
-    const int mine = lane / group_lanes;
+    const int own = sl / group_lanes;
     int better = 0;
     for (int j = 0; j < a.G; ++j) {
-      const float other = __shfl_sync(kFull, g, j * group_lanes);
-      better += other > g || (other == g && j < mine);
+      const float other = __shfl_sync(kFull, g, lane0 + j * group_lanes);
+      better += other > g || (other == g && j < own);
     }
     if (better >= a.keep) {
 #pragma unroll
@@ -155,28 +201,47 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, int gro
     }
   }
 
-  int chosen = -1;
+  if (kPacked) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      if (key[v]) key[v] = (key[v] & 0xFFFF0000u) | (uint32_t)(0xFFFF - e0 - v);
+  }
   for (int k = 0; k < a.K; ++k) {
     uint32_t best = 0;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) best = max(best, key[v]);
-    const uint32_t top = __reduce_max_sync(kFull, best);
-    if (top == 0) break;  // uniform: nothing left to choose
-    const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
-    int e = 0;
-    bool taken = lane != owner;
+    uint32_t top = best;
+    if (LANES == 32) {
+      top = __reduce_max_sync(kFull, best);
+    } else {
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      if (!taken && key[v] == top) {
-        e = e0 + v;
-        key[v] = 0;
-        taken = true;
-      }
+      for (int o = LANES / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
     }
-    e = __shfl_sync(kFull, e, owner);
-    if (lane == k) chosen = e;
+    if (kPacked) {
+#pragma unroll
+      for (int v = 0; v < VPL; ++v)
+        if (key[v] == top) key[v] = 0;
+      if (sl == 0) slots[warp][mine][k] = top ? 0xFFFF - (int)(top & 0xFFFF) : -1;
+      continue;
+    }
+    // the lowest index that has it
+    int e = 0x7FFFFFFF;
+#pragma unroll
+    for (int v = VPL - 1; v >= 0; --v)
+      if (key[v] == top) e = e0 + v;
+    if (LANES == 32) {
+      e = (int)__reduce_min_sync(kFull, (unsigned)e);
+    } else {
+#pragma unroll
+      for (int o = LANES / 2; o; o >>= 1) e = min(e, __shfl_xor_sync(kFull, e, o));
+    }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      if (e - e0 == v) key[v] = 0;
+    if (sl == 0) slots[warp][mine][k] = top ? e : -1;
   }
-  write_slots<kBF16>(a, t, lane, chosen, m, z);
+  __syncwarp();
+  write_slots<LANES, kBF16>(a, t, in, sl, slots[warp][mine], score[warp][mine], m, z);
 }
 
 // Any E and any groups: the keys in shared memory, lanes over experts and
@@ -188,8 +253,10 @@ __global__ void route_any_kernel(RouteArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
   if (t >= a.T) return;
-  uint32_t* key = smem + warp * (a.E + kMaxGroups);
+  uint32_t* key = smem + warp * (a.E + kMaxGroups + 2 * EP_MAX_TOPK);
   float* gscore = reinterpret_cast<float*>(key + a.E);
+  int* slots = reinterpret_cast<int*>(gscore + kMaxGroups);
+  float* score = reinterpret_cast<float*>(slots + EP_MAX_TOPK);
 
   float m = -INFINITY, z = 1.0f;
   if (!a.sigmoid && (a.bias || !a.renorm)) {
@@ -248,7 +315,6 @@ __global__ void route_any_kernel(RouteArgs a) {
     __syncwarp();
   }
 
-  int chosen = -1;
   for (int k = 0; k < a.K; ++k) {
     uint32_t best = 0;
     int at = 0x7FFFFFFF;
@@ -259,13 +325,12 @@ __global__ void route_any_kernel(RouteArgs a) {
       }
     }
     const uint32_t top = __reduce_max_sync(kFull, best);
-    if (top == 0) break;
     const int e = (int)__reduce_min_sync(kFull, best == top ? (unsigned)at : 0x7FFFFFFFu);
-    if (lane == (e & 31)) key[e] = 0;
+    if (top && lane == (e & 31)) key[e] = 0;
+    if (lane == 0) slots[k] = top ? e : -1;
     __syncwarp();
-    if (lane == k) chosen = e;
   }
-  write_slots<kBF16>(a, t, lane, chosen, m, z);
+  write_slots<32, kBF16>(a, t, true, lane, slots, score, m, z);
 }
 
 struct GradArgs {
@@ -279,124 +344,207 @@ struct GradArgs {
   float scale;
   void* dl;
   int32_t* err;
+  bool vec;  // logits' rows are 16-byte aligned and whole vectors
 };
 
-template <bool kBF16>
-__device__ __forceinline__ void store_grad(void* base, int64_t i, float v) {
-  if (kBF16)
-    static_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
-  else
-    static_cast<float*>(base)[i] = v;
+// SL lanes hold a token, one slot each (K <= SL), and its row of gradients in
+// shared memory, where the slots are added; then the row is written in
+// 16-byte stores.  The rows written are most of the traffic: only the chosen
+// experts have a gradient, and only their logits are read, unless the weights
+// are softmax scores that are not renormalised (kDense: the row is read, and
+// kept in shared memory as exp(l - max)).  Everything stays within a warp.
+template <int SL>
+__device__ __forceinline__ float part_sum(float v) {
+#pragma unroll
+  for (int o = SL / 2; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+template <int SL>
+__device__ __forceinline__ float part_max(float v) {
+#pragma unroll
+  for (int o = SL / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
 }
 
-// One warp per token; lane k holds slot k.  Only the chosen experts have a
-// gradient unless the weights are softmax scores that are not renormalised.
-template <bool kBF16>
+// A row's place in shared memory: 16-byte aligned, and eight banks further
+// for every token of a warp.
+inline __host__ __device__ int grad_pitch(int E) { return (E + 7) / 8 * 8 + 8; }
+
+template <int SL, bool kBF16, bool kDense>
 __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(GradArgs a) {
   pdl_wait_then_release();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const int64_t row = t * a.E;
+  extern __shared__ __align__(16) float sm[];
+  constexpr int kTokens = 32 / SL, kVec = kBF16 ? 8 : 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % SL;
+  const int64_t first = ((int64_t)blockIdx.x * (blockDim.x >> 5) + warp) * kTokens;
+  if (first >= a.T) return;  // the whole warp
+  const bool in = first + lane / SL < a.T;
+  const int64_t t = in ? first + lane / SL : a.T - 1;  // a spare token repeats the last one
+  float* row = sm + (warp * kTokens + lane / SL) * grad_pitch(a.E);
 
-  const int64_t id = lane < a.K ? a.idx[t * a.K + lane] : -1;
+  const int64_t id = sub < a.K ? a.idx[t * a.K + sub] : -1;
   const bool bad = id < -1 || id >= a.E;
-  if (__any_sync(kFull, bad) && lane == 0 && a.err) atomicOr(a.err, EP_ERRBIT_BAD_EXPERT);
-  const int e = (id >= 0 && !bad) ? (int)id : -1;
+  if (bad && a.err) atomicOr(a.err, EP_ERRBIT_BAD_EXPERT);
+  const int e = id >= 0 && !bad ? (int)id : -1;
   const float l = e >= 0 ? load_logit<kBF16>(a.logits, t * a.stride + e) : -INFINITY;
-  const bool live = e >= 0 && l > -INFINITY;
-  const float dw = live ? a.scale * a.dw[t * a.K + lane] : 0.0f;
+  const bool live = l > -INFINITY;  // false for NaN
+  const float dw = live ? a.scale * a.dw[t * a.K + sub] : 0.0f;
 
-  // g: the gradient with respect to this slot's logit, before the slots of
-  // one expert are added up; dense: minus the factor of every score
-  float g, m = 0.0f, rz = 0.0f, dense = 0.0f;
-  if (a.sigmoid) {
+  float m = -INFINITY, rz = 0.0f;
+  if (kDense) {
+    if (a.vec) {
+      for (int i = sub * kVec; i < a.E; i += SL * kVec) {
+        float f[8];
+        const int4 v = __ldg(reinterpret_cast<const int4*>(
+            static_cast<const char*>(a.logits) + (t * a.stride + i) * (kBF16 ? 2 : 4)));
+        if (kBF16) {
+          unpack_bf16x8(v, f);
+        } else {
+          f[0] = __int_as_float(v.x), f[1] = __int_as_float(v.y);
+          f[2] = __int_as_float(v.z), f[3] = __int_as_float(v.w);
+        }
+#pragma unroll
+        for (int j = 0; j < kVec; j += 4)
+          *reinterpret_cast<float4*>(row + i + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) m = fmaxf(m, f[j]);
+      }
+    } else {
+      for (int i = sub; i < a.E; i += SL) {
+        const float li = load_logit<kBF16>(a.logits, t * a.stride + i);
+        row[i] = li;
+        m = fmaxf(m, li);
+      }
+    }
+    m = part_max<SL>(m);
+    __syncwarp();
+    float z = 0.0f;
+    for (int i = sub; i < a.E; i += SL) {
+      const float x = row[i] > -INFINITY ? exp_from(row[i], m) : 0.0f;
+      row[i] = x;
+      z += x;
+    }
+    z = part_sum<SL>(z);
+    rz = z > 0.0f ? 1.0f / z : 0.0f;
+  } else {
+    for (int i = sub * 4; i < a.E; i += SL * 4)
+      *reinterpret_cast<float4*>(row + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+
+  float g;  // this slot's part of its logit's gradient
+  if (kDense) {
+    const float p = live ? exp_from(l, m) * rz : 0.0f;
+    g = p * dw;
+    const float dot = part_sum<SL>(g) * -rz;
+    __syncwarp();
+    for (int i = sub; i < a.E; i += SL) row[i] *= dot;
+  } else if (a.sigmoid) {
     const float u = live ? sigmoid_rn(l) : 0.0f;
     float du = dw;
     if (a.renorm) {
-      const float s = warp_sum(u), r = s > 0.0f ? 1.0f / s : 0.0f;
-      du = (dw - warp_sum(dw * (u * r))) * r;
+      const float s = part_sum<SL>(u), r = s > 0.0f ? 1.0f / s : 0.0f;
+      du = (dw - part_sum<SL>(dw * (u * r))) * r;
     }
     g = du * u * (1.0f - u);
-  } else if (a.renorm) {
-    const float top = warp_max(live ? l : -INFINITY);
-    const float x = live ? exp_from(l, top) : 0.0f, s = warp_sum(x);
+  } else {
+    const float top = part_max<SL>(l);
+    const float x = live ? exp_from(l, top) : 0.0f, s = part_sum<SL>(x);
     const float w = s > 0.0f ? x / s : 0.0f;
-    g = w * (dw - warp_sum(w * dw));
-  } else {
-    m = -INFINITY;
-    for (int i = lane; i < a.E; i += 32)
-      m = fmaxf(m, load_logit<kBF16>(a.logits, t * a.stride + i));
-    m = warp_max(m);
-    float z = 0.0f;
-    for (int i = lane; i < a.E; i += 32) {
-      const float li = load_logit<kBF16>(a.logits, t * a.stride + i);
-      z += li > -INFINITY ? exp_from(li, m) : 0.0f;
-    }
-    z = warp_sum(z);
-    rz = z > 0.0f ? 1.0f / z : 0.0f;
-    const float p = live ? exp_from(l, m) * rz : 0.0f;
-    dense = warp_sum(p * dw);
-    g = p * dw;  // the dense part is added below, once per expert
-  }
-
-  if (!a.sigmoid && !a.renorm) {
-    for (int i = lane; i < a.E; i += 32) {
-      const float li = load_logit<kBF16>(a.logits, t * a.stride + i);
-      store_grad<kBF16>(a.dl, row + i, li > -INFINITY ? -(exp_from(li, m) * rz) * dense : 0.0f);
-    }
-    if (live) g -= exp_from(l, m) * rz * dense;
-  } else {
-    for (int i = lane; i < a.E; i += 32) store_grad<kBF16>(a.dl, row + i, 0.0f);
-  }
-
-  // slots that name the same expert are added in the order of k
-  const unsigned same = __match_any_sync(kFull, live ? e : -1 - lane);
-  const bool dup = __any_sync(kFull, __popc(same) > 1);
-  if (dup) {
-    float sum = 0.0f;
-    for (int k = 0; k < a.K; ++k) {
-      const float gk = __shfl_sync(kFull, g, k), pd = __shfl_sync(kFull, dense, k);
-      const float pk = __shfl_sync(kFull, live ? exp_from(l, m) * rz : 0.0f, k);
-      if (same >> k & 1) {
-        // the dense part belongs to the expert, not to each of its slots
-        sum += (k == __ffs(same) - 1) ? gk : gk + pk * pd;
-      }
-    }
-    g = sum;
+    g = w * (dw - part_sum<SL>(w * dw));
   }
   __syncwarp();
-  if (live && lane == __ffs(same) - 1) store_grad<kBF16>(a.dl, row + e, g);
+  // an expert that a token names twice gets its slots in the order of k
+  const unsigned same = __match_any_sync(kFull, live ? lane / SL << 16 | e : -1 - lane);
+  if (__any_sync(kFull, live && (same & (same - 1)))) {
+    for (int k = 0; k < SL; ++k) {
+      if (sub == k && live) row[e] += g;
+      __syncwarp();
+    }
+  } else if (live) {
+    row[e] += g;
+  }
+  __syncwarp();
+  if (!in) return;
+  const int64_t out = t * a.E;
+  if (a.E % kVec == 0) {  // rows of whole vectors
+    for (int i = sub * kVec; i < a.E; i += SL * kVec) {
+      int4 v;
+      const float4 f = *reinterpret_cast<const float4*>(row + i);
+      if (kBF16) {
+        const float4 h = *reinterpret_cast<const float4*>(row + i + 4);
+        const __nv_bfloat162 w[4] = {__floats2bfloat162_rn(f.x, f.y), __floats2bfloat162_rn(f.z, f.w),
+                                     __floats2bfloat162_rn(h.x, h.y), __floats2bfloat162_rn(h.z, h.w)};
+        v = *reinterpret_cast<const int4*>(w);
+        st_stream_v4(reinterpret_cast<int4*>(static_cast<__nv_bfloat16*>(a.dl) + out + i), v);
+      } else {
+        v = make_int4(__float_as_int(f.x), __float_as_int(f.y), __float_as_int(f.z),
+                      __float_as_int(f.w));
+        st_stream_v4(reinterpret_cast<int4*>(static_cast<float*>(a.dl) + out + i), v);
+      }
+    }
+  } else {
+    for (int i = sub; i < a.E; i += SL) {
+      if (kBF16)
+        static_cast<__nv_bfloat16*>(a.dl)[out + i] = __float2bfloat16_rn(row[i]);
+      else
+        static_cast<float*>(a.dl)[out + i] = row[i];
+    }
+  }
+}
+
+template <int SL, bool kBF16, bool kDense>
+ep_status_t launch_grad(const GradArgs& a, cudaStream_t st) {
+  const int warps = a.E <= 512 ? kWarps : 1;  // at most 33 KB of rows a block
+  const int64_t per = warps * (32 / SL);
+  launch_pdl(route_grad_kernel<SL, kBF16, kDense>, (unsigned)((a.T + per - 1) / per), warps * 32,
+             (size_t)per * grad_pitch(a.E) * 4, st, a);
+  return launch_status();
+}
+
+template <bool kBF16, bool kDense>
+ep_status_t launch_grad_lanes(const GradArgs& a, cudaStream_t st) {
+  // eight lanes a token where its slots fit them and four rows a warp fit
+  // shared memory
+  return a.K <= 8 && a.E <= 512 ? launch_grad<8, kBF16, kDense>(a, st)
+                                : launch_grad<32, kBF16, kDense>(a, st);
 }
 
 template <bool kBF16>
 void launch_route(const RouteArgs& a, cudaStream_t st) {
-  const unsigned blocks = (unsigned)((a.T + kWarps - 1) / kWarps);
   const int size = a.E / a.G;
-  // the smallest register tile that holds E and, with groups, splits them
-  // into a power of two of whole lanes
-  const auto fits = [&](int vpl) {
-    if (a.E > 32 * vpl) return false;
+  const bool vec = a.E % 8 == 0 && aligned16(a.logits) && a.stride * (kBF16 ? 2 : 4) % 16 == 0;
+  // the smallest tile that holds E and, with groups, splits them into a power
+  // of two of whole lanes; eight experts a lane where they fit
+  const auto fits = [&](int lanes, int vpl) {
+    if (a.E > lanes * vpl) return false;
     if (a.G == 1) return true;
     if (size % vpl) return false;
     const int n = size / vpl;
-    return (n & (n - 1)) == 0 && n <= 32;
+    return (n & (n - 1)) == 0 && n <= lanes;
   };
-#define EP_ROUTE_CASE(V)                                                                         \
-  if (fits(V)) {                                                                                 \
-    launch_pdl(route_kernel<V, kBF16>, blocks, kWarps * 32, 0, st, a, a.G > 1 ? size / V : 32); \
-    return;                                                                                      \
+#define EP_ROUTE_CASE(L, V)                                                              \
+  if (fits(L, V)) {                                                                      \
+    const int64_t per = kWarps * (32 / L);                                               \
+    if (kBF16 && !a.sigmoid && !a.bias && a.G == 1)                                      \
+      launch_pdl(route_kernel<L, V, kBF16, kBF16>, (unsigned)((a.T + per - 1) / per),    \
+                 kWarps * 32, 0, st, a, L, vec);                                         \
+    else                                                                                 \
+      launch_pdl(route_kernel<L, V, kBF16, false>, (unsigned)((a.T + per - 1) / per),    \
+                 kWarps * 32, 0, st, a, a.G > 1 ? size / V : L, vec);                    \
+    return;                                                                              \
   }
-  EP_ROUTE_CASE(1)
-  EP_ROUTE_CASE(2)
-  EP_ROUTE_CASE(4)
-  EP_ROUTE_CASE(5)
-  EP_ROUTE_CASE(8)
-  EP_ROUTE_CASE(16)
+  EP_ROUTE_CASE(2, 8)
+  EP_ROUTE_CASE(8, 8)
+  EP_ROUTE_CASE(16, 8)
+  EP_ROUTE_CASE(32, 5)
+  EP_ROUTE_CASE(32, 8)
+  EP_ROUTE_CASE(32, 2)
+  EP_ROUTE_CASE(32, 4)
+  EP_ROUTE_CASE(32, 16)
 #undef EP_ROUTE_CASE
-  const int warps = a.E <= 1024 ? 4 : 1;  // at most 17 KB of keys a block
+  const int warps = a.E <= 1024 ? 4 : 1;  // at most 18 KB of keys a block
   launch_pdl(route_any_kernel<kBF16>, (unsigned)((a.T + warps - 1) / warps), warps * 32,
-             (size_t)warps * (a.E + kMaxGroups) * 4, st, a);
+             (size_t)warps * (a.E + kMaxGroups + 2 * EP_MAX_TOPK) * 4, st, a);
 }
 
 bool score_ok(int score) { return score == EP_SCORE_SOFTMAX || score == EP_SCORE_SIGMOID; }
@@ -457,11 +605,12 @@ extern "C" ep_status_t ep_route_backward(const float* dweights, const void* logi
     return EP_ERR_INVALID_ARG;
   const GradArgs a = {dweights,    logits,           row_stride,       topk_idx,
                       num_tokens,  num_experts,      num_topk,         score == EP_SCORE_SIGMOID,
-                      renormalize != 0, scale,       dlogits,          err_word};
-  const unsigned blocks = (unsigned)((num_tokens + kWarps - 1) / kWarps);
+                      renormalize != 0, scale,       dlogits,          err_word,
+                      aligned16(logits) && row_stride * (logits_bf16 ? 2 : 4) % 16 == 0 &&
+                          num_experts % (logits_bf16 ? 8 : 4) == 0};
+  const bool dense = score == EP_SCORE_SOFTMAX && !renormalize;
+  cudaStream_t st = to_cuda(stream);
   if (logits_bf16)
-    launch_pdl(route_grad_kernel<true>, blocks, kWarps * 32, 0, to_cuda(stream), a);
-  else
-    launch_pdl(route_grad_kernel<false>, blocks, kWarps * 32, 0, to_cuda(stream), a);
-  return launch_status();
+    return dense ? launch_grad_lanes<true, true>(a, st) : launch_grad_lanes<true, false>(a, st);
+  return dense ? launch_grad_lanes<false, true>(a, st) : launch_grad_lanes<false, false>(a, st);
 }
