@@ -57,11 +57,11 @@ struct Cfg {
   static constexpr int kPart = kRows / kParts;
   static constexpr int kXBytes = kRows * (kFP8 ? 128 : 256);
   static constexpr int kStagesX = kFP8 ? 4 : 3;  // at least kSlotsA
-  static constexpr int kStagesW = 8;
+  static constexpr int kStagesW = !kFP8 && kGroup == 32 ? 6 : 8;  // what fits
   static constexpr int kColsA = kFP8 ? 32 : 64;  // tensor-memory columns per slot of A
   static constexpr int kSlotsA = 128 / kColsA;
   static constexpr int kPerStep = 128 / kGroup;  // groups in a step
-  static constexpr int kSlotsS = kGroup == 128 ? 8 : 4;
+  static constexpr int kSlotsS = 8;
   // words of a slot of scales: per group 128 scale words and 128 zero-point
   // words, then the rows' scales
   static constexpr int kSWords = kPerStep * 256 + (kFP8 ? kRows : 0);
@@ -76,8 +76,9 @@ struct XMaps {
 };
 
 struct Barriers {
-  // full: a step's x and A are in place; done: its products are finished
-  uint64_t full[5], done[5], wfull[9], wempty[9], sfull[8], sempty[8], pfull[2], pempty[2];
+  // full: a step's x (one arrival), A (four) and scales (32) are in place;
+  // done: its products are finished; sfull: its zero points are in place
+  uint64_t full[5], done[5], wfull[9], wempty[9], sfull[8], pfull[2], pempty[2];
 };
 
 // --- the items of a block ----------------------------------------------------
@@ -184,20 +185,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
       : "memory");
 }
 
-// The registers are written when tmem_wait returns; what uses them is volatile
-// too, and so stays behind it.
+// The load and its wait in one statement, so that no use moves between them.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];"
+      "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(addr)
       : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 // Waits for the phase of the barrier at `bar` (a shared address) with the
@@ -285,23 +282,22 @@ struct Ring {
 };
 
 // --- sums -> accumulators ---------------------------------------------------------
-// acc += v * scale, and acc += (v * x) * scale, for two rows at a time: half
-// the instructions of fmaf.  Volatile, so that they stay behind the loads.
-__device__ __forceinline__ void add2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t scale) {
-  asm volatile(
-      "{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
+// Two float32 at once: half the instructions of fmaf.
+__device__ __forceinline__ uint64_t mul2(uint32_t v0, uint32_t v1, uint64_t x) {
+  uint64_t t;
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tmul.rn.f32x2 %0, v, %3;\n\t}"
+      : "=l"(t)
+      : "r"(v0), "r"(v1), "l"(x));
+  return t;
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t scale) {
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
       : "+l"(acc)
       : "r"(v0), "r"(v1), "l"(scale));
 }
-__device__ __forceinline__ void add2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t x,
-                                     uint64_t scale) {
-  asm volatile(
-      "{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tmul.rn.f32x2 t, t, %3;\n\t"
-      "fma.rn.f32x2 %0, t, %4, %0;\n\t}"
-      : "+l"(acc)
-      : "r"(v0), "r"(v1), "l"(x), "l"(scale));
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t t, uint64_t scale) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(t), "l"(scale));
 }
-
 __device__ __forceinline__ float2 unpack2(uint64_t v) {
   float2 f;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
@@ -310,7 +306,7 @@ __device__ __forceinline__ float2 unpack2(uint64_t v) {
 
 // What the loop over the groups of an item needs.
 struct SumArgs {
-  uint32_t sempty, pfull, pempty;  // barriers (shared addresses)
+  uint32_t pfull, pempty;  // barriers (shared addresses)
   uint32_t scale, xs;                     // this lane's scale words, this part's row scales
   uint32_t src;                           // this part's columns of sums
   uint32_t odd;                           // whether the lane's first group is a word's high half
@@ -329,10 +325,8 @@ __device__ __forceinline__ bool add_groups(const SumArgs& s, int lane, uint32_t&
   for (int g = 0; g < s.groups; ++g) {
     const uint32_t slot = n % C::kSlotsS, buf = p & 1;
     const uint32_t in = C::kPerStep == 1 ? 0 : g % C::kPerStep;
-    // (the scales are there too: the warp that arrives here has waited for the
-    // unpacked codes, whose warps have waited for the scales)
+    // (the scales are there too: the warp that arrives here has waited for them)
     const bool fine = wait(s.pfull + buf * 8, p >> 1 & 1);
-    if (__any_sync(kFull, !fine)) return false;
     fence_after();
     // bf16 -> float32 is a shift; the word holds groups 2i and 2i + 1
     const uint32_t word = lds32(s.scale + slot * C::kSWords * 4 + in * 1024);
@@ -340,35 +334,32 @@ __device__ __forceinline__ bool add_groups(const SumArgs& s, int lane, uint32_t&
     uint64_t scale;
     asm("mov.b64 %0, {%1, %1};" : "=l"(scale) : "r"(sv));
     const uint32_t src = s.src + buf * C::kRows, xs = s.xs + slot * C::kSWords * 4;
-    uint32_t v[2][16];
-    tmem_ld16(src, v[0]);
-    tmem_wait_ld();
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const uint32_t(&u)[16] = v[c & 1];
-      if (c + 1 < kChunks) tmem_ld16(src + (c + 1) * 16, v[(c + 1) & 1]);
+      // the loads of a chunk together, then all products, then all sums:
+      // neighbours that wait for one another cost a latency each
+      uint64_t x[8];
+      if (kFP8) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        if (kFP8) {
-          uint64_t x0, x1;
-          lds_pairs(xs + c * 64 + i * 4, x0, x1);
-          add2(acc[c * 8 + i / 2], u[i], u[i + 1], x0, scale);
-          add2(acc[c * 8 + i / 2 + 1], u[i + 2], u[i + 3], x1, scale);
-        } else {
-          add2(acc[c * 8 + i / 2], u[i], u[i + 1], scale);
-          add2(acc[c * 8 + i / 2 + 1], u[i + 2], u[i + 3], scale);
-        }
+        for (int i = 0; i < 8; i += 2) lds_pairs(xs + c * 64 + i * 8, x[i], x[i + 1]);
       }
-      if (c + 1 < kChunks) tmem_wait_ld();
+      uint32_t v[16];
+      tmem_ld16(src + c * 16, v);
+      if (kFP8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = mul2(v[2 * i], v[2 * i + 1], x[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], x[i], scale);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], v[2 * i], v[2 * i + 1], scale);
+      }
     }
     fence_before();
-    __syncwarp();
+    if (__any_sync(kFull, !fine)) return false;
     ++p;
     const bool last = C::kPerStep == 1 || in == C::kPerStep - 1 || g == s.groups - 1;
-    if (lane == 0) {
-      arrive(s.pempty + buf * 8);
-      if (last) arrive(s.sempty + slot * 8);
-    }
+    if (lane == 0) arrive(s.pempty + buf * 8);
     if (last) ++n;
   }
   return true;
@@ -450,9 +441,9 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
   uint32_t* ss = reinterpret_cast<uint32_t*>(sw + C::kStagesW * kWBytes);
 
   if (tid == 0) {
-    for (int i = 0; i < C::kStagesX; ++i) mbar_init(&bar.full[i], 5), mbar_init(&bar.done[i], 1);
+    for (int i = 0; i < C::kStagesX; ++i) mbar_init(&bar.full[i], 37), mbar_init(&bar.done[i], 1);
     for (int i = 0; i < C::kStagesW; ++i) mbar_init(&bar.wfull[i], 1), mbar_init(&bar.wempty[i], 4);
-    for (int i = 0; i < C::kSlotsS; ++i) mbar_init(&bar.sfull[i], 32), mbar_init(&bar.sempty[i], 4 * kParts + 4);
+    for (int i = 0; i < C::kSlotsS; ++i) mbar_init(&bar.sfull[i], 32);
     for (int i = 0; i < 2; ++i) mbar_init(&bar.pfull[i], 2), mbar_init(&bar.pempty[i], 4 * kParts);
     fence_barrier_init();
     abort_flag = 0;
@@ -572,14 +563,19 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
       }
       if (!ok) give_up();
     } else if (warp == 3) {  // scales and zero points
+      // A slot is free once the products of two steps later are done: they went
+      // into the buffer whose sums it scaled.  The stages of x are fewer than
+      // the slots by more than that, so the x stage's barrier says it.
+      static_assert(C::kSlotsS >= C::kStagesX + 2, "a slot would be in use");
       Ring<C::kSlotsS> rs;
+      Ring<C::kStagesX> rx;
       for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
         const float* xs = kFP8 ? a.x_scales + ((int64_t)it.e * a.cap + it.r0) * steps : nullptr;
         int64_t at[4];  // this lane's four weight rows: their first group
 #pragma unroll
         for (int i = 0; i < 4; ++i) at[i] = lane_row<kSwiglu>(a, it, lane + 32 * i) * groups;
         for (int b = 0; b < steps; ++b) {
-          ok = wait_idle(&bar.sempty[rs.slot], rs.round ^ 1);
+          ok = wait_idle(&bar.done[rx.slot], rx.round ^ 1);
           if (!__all_sync(kFull, ok)) {
             ok = false;
             break;
@@ -603,8 +599,10 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
                 copy_word(dst + kPerStep * 256 + r, xs + min(r, it.rows - 1) * steps + b);
             }
           }
-          copies_arrive(&bar.sfull[rs.slot]);
+          if (a.zeros) copies_arrive(&bar.sfull[rs.slot]);
+          copies_arrive(&bar.full[rx.slot]);
           rs.next();
+          rx.next();
         }
       }
       if (!ok) give_up();
@@ -630,7 +628,7 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
         const uint32_t n = base + b, was = n - C::kSlotsA;  // the step that had the slot of A
         const uint32_t w_slot = n % C::kStagesW, s_slot = n % C::kSlotsS;
         bool fine = wait_idle(wfull0 + w_slot * 8, n / C::kStagesW & 1);
-        fine &= wait_idle(sfull0 + s_slot * 8, n / C::kSlotsS & 1);
+        if (a.zeros) fine &= wait_idle(sfull0 + s_slot * 8, n / C::kSlotsS & 1);
         if (n >= C::kSlotsA)
           fine &= wait_idle(done0 + was % C::kStagesX * 8, was / C::kStagesX & 1);
         if (__any_sync(kFull, !fine)) {
@@ -676,7 +674,6 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
         if (lane == 0) {
           mbar_arrive(&bar.full[n % C::kStagesX]);
           mbar_arrive(&bar.wempty[w_slot]);
-          mbar_arrive(&bar.sempty[s_slot]);
         }
       }
       base += steps;
@@ -686,7 +683,6 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSum));
     const int h = (warp - 4 - 4 * C::kTeams) >> 2, quad = warp & 3, r = quad * 32 + lane;
     SumArgs sum;
-    sum.sempty = smem_addr(bar.sempty);
     sum.pfull = smem_addr(bar.pfull);
     sum.pempty = smem_addr(bar.pempty);
     sum.scale = smem_addr(ss) + r * 4;
