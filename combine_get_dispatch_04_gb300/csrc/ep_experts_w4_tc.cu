@@ -2,9 +2,10 @@
 // with many rows: tcgen05 with the weights as operand A in tensor memory.
 //
 // D[channel][row] = sum over one group of (q - zero) * x: the codes less
-// their zero point are small integers, exact in bf16 and in E4M3, so A holds
-// them unscaled and the tensor cores add exact products in float32.  A
-// group's sums are then read from tensor memory, multiplied by the group's
+// their zero point are small integers, exact in bf16, and codes and zero
+// points are exact in E4M3 (as two operands: q and -zero), so A holds them
+// unscaled and the tensor cores add exact products in float32.  A group's
+// sums are then read from tensor memory, multiplied by the group's
 // scale (and, for E4M3 rows, the scale of the row's 128 channels) and added
 // to float32 accumulators in registers: no weight is ever rounded, and E4M3
 // rows are multiplied as they are, at the 8-bit rate.
@@ -58,9 +59,10 @@ struct Cfg {
   static constexpr int kXBytes = kRows * (kFP8 ? 128 : 256);
   static constexpr int kStagesX = kFP8 ? 4 : 3;  // at least kSlotsA
   static constexpr int kStagesW = !kFP8 && kGroup == 32 ? 6 : 8;  // what fits
-  static constexpr int kColsA = kFP8 ? 32 : 64;  // tensor-memory columns per slot of A
-  static constexpr int kSlotsA = 128 / kColsA;
   static constexpr int kPerStep = 128 / kGroup;  // groups in a step
+  // tensor-memory columns of a slot of A (E4M3: and of each group's zero points)
+  static constexpr int kColsA = kFP8 ? 32 + 8 * kPerStep : 64;
+  static constexpr int kSlotsA = (512 - 2 * kRows) / kColsA < 4 ? (512 - 2 * kRows) / kColsA : 4;
   static constexpr int kSlotsS = 8;
   // words of a slot of scales: per group 128 scale words and 128 zero-point
   // words, then the rows' scales
@@ -185,7 +187,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
       : "memory");
 }
 
-// The load and its wait in one statement, so that no use moves between them.
+// 16 columns of the thread's own lane.  The load and its wait are one statement,
+// so that no use moves between them.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -194,6 +197,20 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(addr)
+      : "memory");
+}
+// 16 columns of the warp's 32 lanes, in the layout of a matrix fragment: thread
+// 4g + q gets, of columns 2q, 2q + 1 (v[0..7]) and 8 + 2q, 8 + 2q + 1, the
+// lanes g, g + 8, g + 16, g + 24: v[8 * half + 2 * j + i], j the lane's eighth.
+__device__ __forceinline__ void tmem_ld_fragment(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%8,%9,%10,%11}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%4,%5,%6,%7,%12,%13,%14,%15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(addr), "r"(addr + (16u << 16))
       : "memory");
 }
 
@@ -244,8 +261,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t& a, uint64_t& b) {
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+__device__ __forceinline__ uint64_t lds64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
@@ -307,16 +326,21 @@ __device__ __forceinline__ float2 unpack2(uint64_t v) {
 // What the loop over the groups of an item needs.
 struct SumArgs {
   uint32_t pfull, pempty;  // barriers (shared addresses)
-  uint32_t scale, xs;                     // this lane's scale words, this part's row scales
-  uint32_t src;                           // this part's columns of sums
-  uint32_t odd;                           // whether the lane's first group is a word's high half
+  uint32_t scale, xs;      // this thread's first scale word, its part's row scales
+  uint32_t src;            // this part's columns of sums
+  uint32_t odd;            // bit j: whether row j's first group is a word's high half
   int groups;
 };
 
 // Adds up all groups of an item for 16 * kChunks rows; n and p count steps
-// and groups over the items.  One instance per number of chunks: a branch in
-// the inner loop costs as much as a chunk (measured 87 against 40 cycles for
-// a chunk of bf16 rows).
+// and groups over the items.  With bf16 rows a thread holds one weight row
+// times all rows of x; with E4M3 rows four weight rows (j) times a quarter of
+// the rows of x, since the rows' scales, which every thread needs in
+// registers, would else take 640 of the cycles of shared memory for a step,
+// instead of 160 (FP8 decode step 1942 us -> 1842; bf16 rows have none to
+// save, and four scales to read instead of one cost them 779 -> 832 us).  One
+// instance per number of chunks: a branch in the inner loop costs as much as
+// a chunk.
 template <bool kFP8, int kGroup, int kChunks>
 __device__ __forceinline__ bool add_groups(const SumArgs& s, int lane, uint32_t& n, uint32_t& p,
                                            uint64_t (&acc)[Cfg<kFP8, kGroup>::kPart / 2]) {
@@ -325,34 +349,38 @@ __device__ __forceinline__ bool add_groups(const SumArgs& s, int lane, uint32_t&
   for (int g = 0; g < s.groups; ++g) {
     const uint32_t slot = n % C::kSlotsS, buf = p & 1;
     const uint32_t in = C::kPerStep == 1 ? 0 : g % C::kPerStep;
-    // (the scales are there too: the warp that arrives here has waited for them)
+    // (the scales are there too: their copies arrive where the products wait)
     const bool fine = wait(s.pfull + buf * 8, p >> 1 & 1);
     fence_after();
-    // bf16 -> float32 is a shift; the word holds groups 2i and 2i + 1
-    const uint32_t word = lds32(s.scale + slot * C::kSWords * 4 + in * 1024);
-    const uint32_t sv = (s.odd + g) & 1 ? word & 0xFFFF0000u : word << 16;
-    uint64_t scale;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(scale) : "r"(sv));
+    const uint32_t at = slot * C::kSWords * 4 + in * 1024;
+    uint64_t scale[kFP8 ? 4 : 1];
+#pragma unroll
+    for (int j = 0; j < (kFP8 ? 4 : 1); ++j) {
+      // bf16 -> float32 is a shift; the word holds groups 2i and 2i + 1
+      const uint32_t word = lds32(s.scale + at + j * 32);
+      const uint32_t sv = (s.odd >> j ^ g) & 1 ? word & 0xFFFF0000u : word << 16;
+      // E4M3 codes are products of 2^-9
+      const float f = kFP8 ? __uint_as_float(sv) * 512.0f : __uint_as_float(sv);
+      asm("mov.b64 %0, {%1, %1};" : "=l"(scale[j]) : "f"(f));
+    }
     const uint32_t src = s.src + buf * C::kRows, xs = s.xs + slot * C::kSWords * 4;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       // the loads of a chunk together, then all products, then all sums:
       // neighbours that wait for one another cost a latency each
-      uint64_t x[8];
-      if (kFP8) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) lds_pairs(xs + c * 64 + i * 8, x[i], x[i + 1]);
-      }
       uint32_t v[16];
-      tmem_ld16(src + c * 16, v);
       if (kFP8) {
+        const uint64_t x[2] = {lds64(xs + c * 64), lds64(xs + c * 64 + 32)};
+        tmem_ld_fragment(src + c * 16, v);
+        uint64_t t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = mul2(v[2 * i], v[2 * i + 1], x[i]);
+        for (int i = 0; i < 8; ++i) t[i] = mul2(v[2 * i], v[2 * i + 1], x[i >> 2]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], x[i], scale);
+        for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], t[i], scale[i & 3]);
       } else {
+        tmem_ld16(src + c * 16, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], v[2 * i], v[2 * i + 1], scale);
+        for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], v[2 * i], v[2 * i + 1], scale[0]);
       }
     }
     fence_before();
@@ -379,46 +407,119 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t zp, uint32_t* ou
   }
 }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-
-// Eight codes as E4M3 bytes, looked up in the 16 bytes of (q - zero).
-__device__ __forceinline__ void codes_e4m3(uint32_t w, const uint4& t, uint32_t* out) {
-  const uint32_t idx = w & 0x77777777u, high = (w >> 3) & 0x11111111u;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t i = h ? idx >> 16 : idx, m = h ? high >> 16 : high;
-    const uint32_t lo = prmt(t.x, t.y, i), hi = prmt(t.z, t.w, i);
-    const uint32_t mask = prmt(0x0000FF00u, 0, m);
-    out[h] = (lo & ~mask) | (hi & mask);
-  }
-}
-
-// The E4M3 code of an integer of at most 15 in magnitude.
-__device__ __forceinline__ uint32_t e4m3_of_int(int v) {
-  const int m = v < 0 ? -v : v;
-  if (m == 0) return 0;
-  const int p = 31 - __clz(m);  // m = 2^p * (1 + frac), three fraction bits hold it
-  return (uint32_t)((v < 0 ? 0x80 : 0) | (7 + p) << 3 | ((m << 3 >> p) & 7));
+// Eight codes as E4M3 bytes in channel order: the codes themselves.  E4M3's
+// subnormals and first normal numbers are k * 2^-9 for k = 0..15, so a 4-bit
+// code is the E4M3 number q * 2^-9 as it stands: 5 instructions for 8 codes
+// instead of 13 that subtract the zero point by looking q - zero up.
+__device__ __forceinline__ void codes_e4m3(uint32_t w, uint32_t* out) {
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = w >> 4 & 0x0F0F0F0Fu;
+  out[0] = __byte_perm(even, odd, 0x5140);
+  out[1] = __byte_perm(even, odd, 0x7362);
 }
 
 // Lane r of tensor memory (0..127) holds the weight row of this channel of the
-// tile; with swiglu, lanes 16..31 of each 32 hold the up projection's.
-template <bool kSwiglu>
+// tile; with swiglu, lanes 16..31 of each 32 hold the up projection's.  With
+// E4M3 rows a thread of the summing warps gets lanes g, g + 8, g + 16 and
+// g + 24: four neighbouring channels, or two of the gate and the same two of
+// up, which it stores at once.  Within the four they are rotated, so that the
+// eight lanes that read their codes together do not meet a bank of shared
+// memory twice.
+template <bool kFP8, bool kSwiglu>
 __device__ __forceinline__ int lane_channel(int r) {
-  return kSwiglu ? (r >> 5) * 16 + (r & 15) : r;
+  const int g = r & 7, j = r >> 3 & 3;
+  if (!kFP8) return kSwiglu ? (r >> 5) * 16 + (r & 15) : r;
+  return kSwiglu ? (r >> 5) * 16 + 2 * g + ((j ^ g >> 2) & 1)
+                 : (r >> 5) * 32 + 4 * g + ((j + (g >> 1)) & 3);
 }
 template <bool kSwiglu>
 __device__ __forceinline__ bool lane_is_up(int r) {
   return kSwiglu && (r & 16);
 }
-template <bool kSwiglu>
+template <bool kFP8, bool kSwiglu>
 __device__ __forceinline__ int64_t lane_row(const ExpertsArgs& a, const Item& it, int r) {
-  const int c = min(it.tile * (kSwiglu ? 64 : 128) + lane_channel<kSwiglu>(r), a.N - 1);
+  const int c = min(it.tile * (kSwiglu ? 64 : 128) + lane_channel<kFP8, kSwiglu>(r), a.N - 1);
   return (int64_t)it.e * a.rows + c + (lane_is_up<kSwiglu>(r) ? a.N : 0);
+}
+
+// Writes one part of an item's rows, bf16 rows of x: acc[i] holds rows 2i and
+// 2i + 1 of the thread's own channel.
+template <bool kSwiglu, int kPart>
+__device__ __forceinline__ void store_rows(const ExpertsArgs& a, const Item& it, int h, int quad,
+                                           int lane, const uint64_t (&acc)[kPart / 2]) {
+  const int n0 = it.tile * (kSwiglu ? 64 : 128) + lane_channel<false, kSwiglu>(quad * 32 + lane);
+  const int left = min(it.rows - h * it.np, it.np);  // live rows of this part
+  __nv_bfloat16* dst =
+      a.y + ((int64_t)it.e * a.cap + it.r0 + h * it.np + (kSwiglu ? lane >> 4 : 0)) * a.N + n0;
+  if (n0 >= a.N) {
+    // a channel beyond the last tile's end
+  } else if (kSwiglu) {
+    // lanes 0-15 hold the gate, 16-31 the up projection of the same
+    // channels: the lower lanes finish the first row of each pair, the
+    // upper ones the second
+    const unsigned in = __activemask();
+#pragma unroll
+    for (int i = 0; i < kPart / 2; ++i) {
+      if (2 * i >= left) break;
+      const float2 v = unpack2(acc[i]);
+      const float other = __shfl_xor_sync(in, lane < 16 ? v.y : v.x, 16);
+      const float gate = lane < 16 ? v.x : other, up = lane < 16 ? other : v.y;
+      // a few units in the last place of float32, rounded to bf16 next
+      const float out = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+      if (2 * i + (lane >> 4) < left) *dst = __float2bfloat16_rn(out);
+      dst += 2 * a.N;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPart / 2; ++i) {
+      if (2 * i >= left) break;
+      const float2 v = unpack2(acc[i]);
+      dst[0] = __float2bfloat16_rn(v.x);
+      if (2 * i + 1 < left) dst[a.N] = __float2bfloat16_rn(v.y);
+      dst += 2 * a.N;
+    }
+  }
+}
+
+// The same for E4M3 rows, in the layout of a matrix fragment.
+template <bool kSwiglu, int kPart>
+__device__ __forceinline__ void store_fragment(const ExpertsArgs& a, const Item& it, int h, int quad,
+                                               int lane, const uint64_t (&acc)[kPart / 2]) {
+  const int g = lane >> 2, q = lane & 3;
+  // acc[8c + 4b + j]: rows 16c + 8b + 2q and the next, weight row j
+  const int n0 = it.tile * (kSwiglu ? 64 : 128) + (kSwiglu ? quad * 16 + 2 * g : quad * 32 + 4 * g);
+  const int left = min(it.rows - h * it.np, it.np);  // live rows of this part
+  __nv_bfloat16* dst = a.y + ((int64_t)it.e * a.cap + it.r0 + h * it.np + 2 * q) * a.N + n0;
+  if (n0 < a.N) {  // else beyond the last tile's end
+#pragma unroll
+    for (int i = 0; i < kPart / 8; ++i) {
+      if (8 * i >= left) break;
+      const float2 v[4] = {unpack2(acc[4 * i]), unpack2(acc[4 * i + 1]), unpack2(acc[4 * i + 2]),
+                           unpack2(acc[4 * i + 3])};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float f[4] = {k ? v[0].y : v[0].x, k ? v[1].y : v[1].x, k ? v[2].y : v[2].x,
+                            k ? v[3].y : v[3].x};
+        if (8 * i + 2 * q + k < left) {
+          if (kSwiglu) {
+            // a few units in the last place of float32, rounded to bf16 next
+            const float o0 = __fdividef(f[0], 1.0f + __expf(-f[0])) * f[2];
+            const float o1 = __fdividef(f[1], 1.0f + __expf(-f[1])) * f[3];
+            *reinterpret_cast<__nv_bfloat162*>(dst + k * a.N) =
+                g < 4 ? __floats2bfloat162_rn(o0, o1) : __floats2bfloat162_rn(o1, o0);
+          } else {
+            // back by g / 2 places: one, then two
+            const bool one = g & 2, two = g & 4;
+            const float r0 = one ? f[3] : f[0], r1 = one ? f[0] : f[1];
+            const float r2 = one ? f[1] : f[2], r3 = one ? f[2] : f[3];
+            __nv_bfloat162 o[2] = {__floats2bfloat162_rn(two ? r2 : r0, two ? r3 : r1),
+                                   __floats2bfloat162_rn(two ? r0 : r2, two ? r1 : r3)};
+            *reinterpret_cast<uint2*>(dst + k * a.N) = *reinterpret_cast<const uint2*>(o);
+          }
+        }
+      }
+      dst += 8 * (int64_t)a.N;
+    }
+  }
 }
 
 template <bool kFP8, bool kSwiglu, int kGroup>
@@ -432,7 +533,6 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
   __shared__ Barriers bar;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  __shared__ uint4 tables[16];  // E4M3 of (q - zero), one 16-byte table per zero point
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -448,14 +548,6 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
     fence_barrier_init();
     abort_flag = 0;
   }
-  if (kFP8 && tid < 16) {
-    uint32_t w[4];
-    for (int i = 0; i < 4; ++i) {
-      w[i] = 0;
-      for (int b = 0; b < 4; ++b) w[i] |= e4m3_of_int(4 * i + b - tid) << (8 * b);
-    }
-    tables[tid] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_addr(&tmem_base))
@@ -466,7 +558,7 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_base;
-  const uint32_t tmem_a = tmem + 384;
+  const uint32_t tmem_a = tmem + 2 * C::kRows;
   const volatile int* abort = &abort_flag;
 
   pdl_wait_then_release();
@@ -526,8 +618,10 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
               for (int j = 0; j < kMmaPerGroup; ++j) {
                 const int k = g * kMmaPerGroup + j;  // matrix step within the step
                 const uint32_t off = kFP8 ? k * 32 : (k >> 2) * C::kRows * 128 + (k & 3) * 32;
-                mma<kFP8>(tmem + rp.slot * C::kRows, a0 + k * 8, desc0 | (uint64_t)((x0 + off) >> 4),
-                          idesc, j > 0);
+                const uint64_t xd = desc0 | (uint64_t)((x0 + off) >> 4);
+                mma<kFP8>(tmem + rp.slot * C::kRows, a0 + k * 8, xd, idesc, j > 0);
+                // less zero * x: the same rows of x with the group's zero points
+                if (kFP8) mma<kFP8>(tmem + rp.slot * C::kRows, a0 + 32 + g * 8, xd, idesc, true);
               }
               commit(&bar.pfull[rp.slot]);
               mbar_arrive(&bar.pfull[rp.slot]);  // releases what this warp has waited for
@@ -573,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
         const float* xs = kFP8 ? a.x_scales + ((int64_t)it.e * a.cap + it.r0) * steps : nullptr;
         int64_t at[4];  // this lane's four weight rows: their first group
 #pragma unroll
-        for (int i = 0; i < 4; ++i) at[i] = lane_row<kSwiglu>(a, it, lane + 32 * i) * groups;
+        for (int i = 0; i < 4; ++i) at[i] = lane_row<kFP8, kSwiglu>(a, it, lane + 32 * i) * groups;
         for (int b = 0; b < steps; ++b) {
           ok = wait_idle(&bar.done[rx.slot], rx.round ^ 1);
           if (!__all_sync(kFull, ok)) {
@@ -613,17 +707,16 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
     // codes -> operand A: this thread's weight row is lane 32 * quad + lane of
     // tensor memory
     const int team = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const int srow = lane_channel<kSwiglu>(r) + (lane_is_up<kSwiglu>(r) ? 64 : 0);
+    const int srow = lane_channel<kFP8, kSwiglu>(r) + (lane_is_up<kSwiglu>(r) ? 64 : 0);
     const uint32_t swz = (uint32_t)((srow >> 1) & 3) << 4;
     const uint32_t row_addr = smem_addr(sw) + srow * 64;
     const uint32_t zero_addr = smem_addr(ss) + (128 + r) * 4;
-    const uint32_t table_addr = smem_addr(tables);
     const uint32_t a_addr = tmem_a + ((uint32_t)(quad * 32) << 16);
     const uint32_t wfull0 = smem_addr(bar.wfull), sfull0 = smem_addr(bar.sfull);
     const uint32_t done0 = smem_addr(bar.done);
     uint32_t base = 0;  // steps of the items before
     for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
-      const int at4 = (int)(lane_row<kSwiglu>(a, it, r) * groups & 3);
+      const int at4 = (int)(lane_row<kFP8, kSwiglu>(a, it, r) * groups & 3);
       for (int b = (int)((team + base) % C::kTeams); b < steps; b += C::kTeams) {
         const uint32_t n = base + b, was = n - C::kSlotsA;  // the step that had the slot of A
         const uint32_t w_slot = n % C::kStagesW, s_slot = n % C::kSlotsS;
@@ -639,7 +732,6 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
         const uint32_t src = row_addr + w_slot * kWBytes;
         const uint32_t dst = a_addr + n % C::kSlotsA * C::kColsA;
         uint32_t zero = 8;
-        uint4 t = {};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // 32 channels
           const uint4 w = lds128(src + (i << 4 ^ swz));
@@ -649,14 +741,18 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
               const int gi = at4 + min(b * kPerStep + g, groups - 1);
               zero = lds32(zero_addr + s_slot * C::kSWords * 4 + g * 1024) >> (8 * (gi & 3)) & 15;
             }
-            if (kFP8) t = lds128(table_addr + zero * 16);
+            if (kFP8) {  // -zero * 2^-9, for every channel of a matrix step
+              const uint32_t z4 = (zero | 0x80u) * 0x01010101u;
+              const uint32_t v[8] = {z4, z4, z4, z4, z4, z4, z4, z4};
+              tmem_st8(dst + 32 + i * kPerStep / 4 * 8, v);
+            }
           }
           if (kFP8) {
             uint32_t v[8];
-            codes_e4m3(w.x, t, v);
-            codes_e4m3(w.y, t, v + 2);
-            codes_e4m3(w.z, t, v + 4);
-            codes_e4m3(w.w, t, v + 6);
+            codes_e4m3(w.x, v);
+            codes_e4m3(w.y, v + 2);
+            codes_e4m3(w.z, v + 4);
+            codes_e4m3(w.w, v + 6);
             tmem_st8(dst + i * 8, v);
           } else {
             const uint32_t zp = 0x43004300u | zero * 0x00010001u;
@@ -681,17 +777,22 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
     if (!ok) give_up();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSum));
-    const int h = (warp - 4 - 4 * C::kTeams) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const int h = (warp - 4 - 4 * C::kTeams) >> 2, quad = warp & 3;
+    // E4M3 rows: this thread's lanes 8j + g, columns 2q and 2q + 1 of eight
+    const int g = kFP8 ? lane >> 2 : lane, q = kFP8 ? lane & 3 : 0;
     SumArgs sum;
     sum.pfull = smem_addr(bar.pfull);
     sum.pempty = smem_addr(bar.pempty);
-    sum.scale = smem_addr(ss) + r * 4;
+    sum.scale = smem_addr(ss) + (quad * 32 + g) * 4;
     sum.groups = groups;
     uint32_t n = 0, p = 0;  // steps and groups
     for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
-      sum.odd = (uint32_t)(lane_row<kSwiglu>(a, it, r) * groups & 1);
+      sum.odd = 0;
+#pragma unroll
+      for (int j = 0; j < (kFP8 ? 4 : 1); ++j)
+        sum.odd |= (uint32_t)(lane_row<kFP8, kSwiglu>(a, it, quad * 32 + j * 8 + g) * groups & 1) << j;
       sum.src = tmem + ((uint32_t)(quad * 32) << 16) + h * it.np;
-      sum.xs = smem_addr(ss) + (kPerStep * 256 + h * it.np) * 4;
+      sum.xs = smem_addr(ss) + (kPerStep * 256 + h * it.np + 2 * q) * 4;
       uint64_t acc[C::kPart / 2];
 #pragma unroll
       for (int i = 0; i < C::kPart / 2; ++i) acc[i] = 0;
@@ -704,38 +805,10 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
         default: ok = add_groups<kFP8, kGroup, C::kPart / 16>(sum, lane, n, p, acc); break;
       }
       if (!ok) break;
-      const int n0 = it.tile * (kSwiglu ? 64 : 128) + lane_channel<kSwiglu>(r);
-      const int left = min(it.rows - h * it.np, it.np);  // live rows of this part
-      __nv_bfloat16* dst =
-          a.y + ((int64_t)it.e * a.cap + it.r0 + h * it.np + (kSwiglu ? lane >> 4 : 0)) * a.N + n0;
-      if (n0 >= a.N) {
-        // a channel beyond the last tile's end
-      } else if (kSwiglu) {
-        // lanes 0-15 hold the gate, 16-31 the up projection of the same
-        // channels: the lower lanes finish the first row of each pair, the
-        // upper ones the second
-        const unsigned in = __activemask();
-#pragma unroll
-        for (int i = 0; i < C::kPart / 2; ++i) {
-          if (2 * i >= left) break;
-          const float2 v = unpack2(acc[i]);
-          const float other = __shfl_xor_sync(in, lane < 16 ? v.y : v.x, 16);
-          const float gate = lane < 16 ? v.x : other, up = lane < 16 ? other : v.y;
-          // a few units in the last place of float32, rounded to bf16 next
-          const float out = __fdividef(gate, 1.0f + __expf(-gate)) * up;
-          if (2 * i + (lane >> 4) < left) *dst = __float2bfloat16_rn(out);
-          dst += 2 * a.N;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < C::kPart / 2; ++i) {
-          if (2 * i >= left) break;
-          const float2 v = unpack2(acc[i]);
-          dst[0] = __float2bfloat16_rn(v.x);
-          if (2 * i + 1 < left) dst[a.N] = __float2bfloat16_rn(v.y);
-          dst += 2 * a.N;
-        }
-      }
+      if constexpr (kFP8)
+        store_fragment<kSwiglu, C::kPart>(a, it, h, quad, lane, acc);
+      else
+        store_rows<kSwiglu, C::kPart>(a, it, h, quad, lane, acc);
       __syncwarp();
     }
     if (!ok) give_up();
