@@ -4,12 +4,13 @@
 // A warp multiplies a tile of 64 weight rows (swiglu: 32 of the gate and the
 // same 32 of the up projection) by up to 8 rows of x with mma.sync m16n8k16
 // (weights as A, rows as B, float32 accumulators): at a few rows the tensor
-// rate is not what counts, and A can come from registers.  The dot product may run over the channels in any
-// order, as long as both operands use the same one.  A step is 128 channels;
-// thread t of a quad takes the t-th quarter of every 64 channels (32 where those
-// have a scale of their own), so that one matrix step never mixes groups, and
-// unpacks the codes of its bytes without moving them to another thread.  The
-// sums of a group are scaled in float32; no weight is rounded.
+// rate is not what counts, and A can come from registers.  The dot product may
+// run over the channels in any order, as long as both operands use the same
+// one.  A step is 128 channels; thread t of a quad takes the t-th quarter of
+// every 64 channels (32 where those have a scale of their own), so that one
+// matrix step never mixes groups, and unpacks the codes of its bytes without
+// moving them to another thread.  The sums of a group are scaled in float32;
+// no weight is rounded.
 //
 // bf16 rows: the codes become 128 + q (the bits of q are the low mantissa
 // bits of 128) and the sum over the group less (128 + zero) * sum(x), which
@@ -17,13 +18,20 @@
 // instead of 11.  E4M3 rows: both sides as f16, where codes less their zero
 // point and E4M3 values are exact.
 //
-// What bounds it is the stream of the codes, and close behind it the integer
-// pipe, which takes two cycles an instruction: so every warp keeps two
-// steps on their way with asynchronous copies, across the ends of its
-// tiles, pointers advance instead of being computed, and lanes without a row
-// of x read the last one instead of zeros (their columns are not stored).
-// The warps of a block share a tile by its channels when there are too few
-// tiles for all warps.
+// The floor is the stream of the codes, which the copies alone reach (306 us
+// for 256 experts of 7168 x 2048); what bounds it is the warps' own time: 640
+// instructions a step, two cycles each for those of the integer pipe, and the
+// latencies that four warps a scheduler leave open (the register file holds
+// no more).  So every warp keeps two steps on their way with asynchronous
+// copies, across the ends of its tiles, pointers advance instead of being
+// computed, and lanes without a row of x read the last one instead of zeros
+// (their columns are not stored).  The warps of a block share a tile by its
+// channels when there are too few tiles for all warps.
+//
+// Measured at 256 experts of 7168 x 2048 (1.9 GB of codes), about two rows
+// each: 534 us with groups of 128 (3.6 TB/s), 610 us with groups of 64 and
+// zero points; E4M3 rows 437 us.  One token, 8 experts, gate and up of
+// 2048 x 7168: 39.5 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -40,7 +48,8 @@ constexpr int kMT = 4;                     // 16-row weight tiles per warp
 constexpr int kTileRows = kMT * 16;
 constexpr int kStages = 3;                 // of a warp's codes
 constexpr int kStage = kTileRows * 64;     // bytes of codes of a step
-constexpr int kSmem = kWarps * kStages * kStage;
+constexpr int kScales = kTileRows * 12;    // of a warp: scales and zero points of four groups
+constexpr int kSmem = kWarps * (kStages * kStage + kScales);
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -122,6 +131,21 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
 // Row i * 8 + g of a tile of weight rows, relative to the tile's
 // first: rows beyond the last channel read the last one (32-bit indices and
 // one multiply-add an address, instead of a pointer for each row).
@@ -131,8 +155,8 @@ __device__ __forceinline__ uint32_t tile_row(int i, int g, int last, int N) {
   return i < kMT ? (uint32_t)min(g + 8 * i, last) : (uint32_t)(min(g + 8 * (i - kMT), last) + N);
 }
 
-// What a warp reads with its own lanes for the products of a tile: pointers
-// to this step's first byte, advanced from step to step.
+// What a warp reads with its own lanes for the products of a tile; pointers
+// to x and its scales advance from step to step.
 struct Sources {
   const uint8_t* x;             // the row of x: this lane's channels
   const float* xs;              // scales of the expert's E4M3 rows, and which two
@@ -142,54 +166,62 @@ struct Sources {
   int last;                     // last row of the tile that is a channel
 };
 
-// The scales (pairs of bf16) and zero points (bytes) of the kPer groups of a
-// step, g0 the first one.  Where whole steps make up a row they are aligned
-// to be read at once; else one by one, groups beyond the row's end as any.
-template <int kPer>
-__device__ __forceinline__ void load_scales(const __nv_bfloat16* p, int g0, bool ragged,
-                                            uint32_t groups, uint32_t (&v)[(kPer + 1) / 2]) {
-  const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
-  if (kPer == 1) {
-    v[0] = __ldg(u);
-  } else if (!ragged && groups % kPer == 0) {
-    if (kPer == 2) {
-      v[0] = __ldg(reinterpret_cast<const uint32_t*>(u));
-    } else {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(u));
-      v[0] = w.x;
-      v[(kPer + 1) / 2 - 1] = w.y;
-    }
-  } else {
+// Scales and zero points of four groups of a tile's rows.  A lane loads those
+// of rows lane and lane + 32 while a step is multiplied, and puts them
+// into shared memory after it: 64 rows of 4 scales, then 64 of 4 zero points.
+// Where every thread loads what it needs itself, each step, 16 loads and their
+// addresses (677 us, with groups of 64 and zero points, against 610).
+struct Scales {
+  uint2 s[2];
+  uint32_t z[2];
+};
+// Where the row's groups come in fours they are aligned to be read at once;
+// else one by one, groups beyond the row's end as any.
+template <bool kSwiglu, bool kZeros>
+__device__ __forceinline__ void load_scales(const Sources& src, int g0, int lane, int N,
+                                            uint32_t groups, Scales& v) {
 #pragma unroll
-    for (int q = 0; q < kPer; q += 2) {
-      const uint32_t lo = __ldg(u + (g0 + q < (int)groups ? q : 0));
-      const uint32_t hi = __ldg(u + (g0 + q + 1 < (int)groups ? q + 1 : 0));
-      v[q / 2] = lo | hi << 16;
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t at =
+        (uint64_t)tile_row<kSwiglu>((lane >> 3) + 4 * i, lane & 7, src.last, N) * groups + g0;
+    const uint16_t* u = reinterpret_cast<const uint16_t*>(src.scale) + at;
+    const uint8_t* z = src.zero + at;
+    if (groups % 4 == 0) {
+      v.s[i] = __ldg(reinterpret_cast<const uint2*>(u));
+      if (kZeros) v.z[i] = __ldg(reinterpret_cast<const uint32_t*>(z));
+    } else {
+      uint32_t f[4], w = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int k = g0 + q < (int)groups ? q : 0;
+        f[q] = __ldg(u + k);
+        if (kZeros) w |= (uint32_t)__ldg(z + k) << (8 * q);
+      }
+      v.s[i] = make_uint2(f[0] | f[1] << 16, f[2] | f[3] << 16);
+      if (kZeros) v.z[i] = w;
     }
   }
 }
-template <int kPer>
-__device__ __forceinline__ uint32_t load_zeros(const uint8_t* p, int g0, bool ragged,
-                                               uint32_t groups) {
-  if (kPer == 1) return __ldg(p);
-  if (!ragged && groups % kPer == 0)
-    return kPer == 2 ? __ldg(reinterpret_cast<const uint16_t*>(p))
-                     : __ldg(reinterpret_cast<const uint32_t*>(p));
-  uint32_t v = 0;
+template <bool kZeros>
+__device__ __forceinline__ void store_scales(uint32_t at, int lane, const Scales& v) {
 #pragma unroll
-  for (int q = 0; q < kPer; ++q)
-    v |= (uint32_t)__ldg(p + (g0 + q < (int)groups ? q : 0)) << (8 * q);
-  return v;
+  for (int i = 0; i < 2; ++i) {
+    const int row = lane + 32 * i;
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + row * 8), "r"(v.s[i].x),
+                 "r"(v.s[i].y) : "memory");
+    if (kZeros)
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + kTileRows * 8 + row * 4), "r"(v.z[i])
+                   : "memory");
+  }
 }
 
 // The products of step s of a tile.  ragged: channels end within the step.
 template <bool kFP8, bool kSwiglu, int kGroup, bool kZeros>
 __device__ __forceinline__ void step_products(const ExpertsArgs& a, const Sources& src,
-                                              int s, bool ragged, uint32_t stage, int lane,
-                                              float (&acc)[kMT][4]) {
+                                              int s, bool ragged, uint32_t stage,
+                                              uint32_t scales, int lane, float (&acc)[kMT][4]) {
   constexpr int kPer = 128 / kGroup;
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t groups = (uint32_t)a.I / kGroup;
   // everything that comes from global memory goes out before the wait for
   // the codes
   uint4 xv[kFP8 ? 2 : 4];
@@ -215,24 +247,26 @@ __device__ __forceinline__ void step_products(const ExpertsArgs& a, const Source
     xs[0] = __ldg(src.xs + src.xrow[0]);
     xs[1] = __ldg(src.xs + src.xrow[1]);
   }
-  // a row's scales and zero points of this step, in one load each
-  uint32_t sv[kMT][2][(kPer + 1) / 2], zv[kMT][2];
-#pragma unroll
-  for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint64_t at = (uint64_t)tile_row<kSwiglu>(mt * 2 + h, g, src.last, a.N) * groups;
-      load_scales<kPer>(src.scale + at, s * kPer, ragged, groups, sv[mt][h]);
-      zv[mt][h] = 0x08080808u;
-      if (kZeros) zv[mt][h] = load_zeros<kPer>(src.zero + at, s * kPer, ragged, groups);
-    }
   asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
   __syncwarp();
 
+  // this thread's first row, this step's first group of the four
+  const int in = kPer == 4 ? 0 : s * kPer & (4 - kPer);
+  const uint32_t scale0 = scales + g * 8 + in * 2;
+  const uint32_t zero0 = scales + kTileRows * 8 + g * 4 + in;
   float ones[4] = {}, part[kMT][4] = {};
+  uint32_t z[kMT][2];
+  uint2 w[kMT][2];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int q = j / (4 / kPer);  // the word's group
+    if (j % (4 / kPer) == 0) {
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          z[mt][h] = kZeros ? lds8(zero0 + mt * 64 + h * 32 + q) : 8;
+    }
     uint32_t b[4];
     if (kFP8) {
       const uint4 v = xv[j >> 1];
@@ -245,10 +279,22 @@ __device__ __forceinline__ void step_products(const ExpertsArgs& a, const Source
     }
     const int byte = word_channel<kGroup>(t, j) / 2;
     const uint32_t at = stage + ((byte >> 4 ^ chunk_swizzle(g)) << 4) + (byte & 15) + g * 64;
+    if (kGroup == 32 || j % 2 == 0) {  // else the words lie side by side
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (kGroup == 32)
+            w[mt][h].x = lds32(at + mt * 1024 + h * 512);
+          else
+            w[mt][h] = lds64(at + mt * 1024 + h * 512);
+        }
+    }
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
-      const uint32_t w0 = lds32(at + mt * 1024), w1 = lds32(at + mt * 1024 + 512);
-      const uint32_t z0 = zv[mt][0] >> (8 * q) & 0xFF, z1 = zv[mt][1] >> (8 * q) & 0xFF;
+      const bool second = kGroup != 32 && j % 2;
+      const uint32_t w0 = second ? w[mt][0].y : w[mt][0].x, w1 = second ? w[mt][1].y : w[mt][1].x;
+      const uint32_t z0 = z[mt][0], z1 = z[mt][1];
       uint32_t lo[4], hi[4];
       if (kFP8) {
         // -(1024 + z) and -(64 + z) as f16: 0xE400 | z, 0xD400 | z << 4
@@ -266,10 +312,9 @@ __device__ __forceinline__ void step_products(const ExpertsArgs& a, const Source
     if ((j + 1) % (4 / kPer) == 0) {  // the end of a group
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
-        const uint32_t z0 = zv[mt][0] >> (8 * q) & 0xFF, z1 = zv[mt][1] >> (8 * q) & 0xFF;
-        const uint32_t w0 = sv[mt][0][q / 2], w1 = sv[mt][1][q / 2];
-        const float s0 = __uint_as_float(q & 1 ? w0 & 0xFFFF0000u : w0 << 16);
-        const float s1 = __uint_as_float(q & 1 ? w1 & 0xFFFF0000u : w1 << 16);
+        const uint32_t z0 = z[mt][0], z1 = z[mt][1];
+        const float s0 = __uint_as_float(lds16(scale0 + mt * 128 + q * 2) << 16);
+        const float s1 = __uint_as_float(lds16(scale0 + mt * 128 + 64 + q * 2) << 16);
         // -(128 + z): z << 16 is z in units of 128's last mantissa places
         const float f0 = __uint_as_float(0xC3000000u | z0 << 16);
         const float f1 = __uint_as_float(0xC3000000u | z1 << 16);
@@ -340,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(ExpertsArgs a) {
   const int kw = warp % ks, team = warp / ks, teams = kWarps / ks;
   const int first = blockIdx.x * teams + team, stride = gridDim.x * teams;
   const uint32_t stage0 = smem_addr(smem) + warp * kStages * kStage;
+  const uint32_t scales = smem_addr(smem) + kWarps * kStages * kStage + warp * kScales;
 
   const auto enter = [&](Cursor& c) {
     if (c.item < items) {
@@ -387,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(ExpertsArgs a) {
     Sources src;
     {
       const int64_t row = (int64_t)use.e * a.cap;
-      const int64_t at = ((int64_t)use.e * a.rows + use.n0) * groups + use.s * (128 / kGroup);
+      const int64_t at = ((int64_t)use.e * a.rows + use.n0) * groups;
       src.x = a.x + ((row + min(g, nrows - 1)) * a.I + use.s * 128 + word_channel<kGroup>(t, 0)) *
                         (kFP8 ? 1 : 2);
 #pragma unroll
@@ -398,14 +444,23 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(ExpertsArgs a) {
       src.last = min(kChannels, a.N - use.n0) - 1;
     }
     float acc[kMT][4] = {};
+    constexpr int kPer = 128 / kGroup;
+    Scales sc;
+    if (use.s < steps) {
+      load_scales<kSwiglu, kZeros>(src, use.s * kPer & ~3, lane, a.N, groups, sc);
+      __syncwarp();
+      store_scales<kZeros>(scales, lane, sc);
+    }
     for (; use.s < steps; use.s += ks) {
+      const int next = (use.s + ks) * kPer & ~3;
+      const bool fresh = next != (use.s * kPer & ~3) && use.s + ks < steps;
+      if (fresh) load_scales<kSwiglu, kZeros>(src, next, lane, a.N, groups, sc);
       step_products<kFP8, kSwiglu, kGroup, kZeros>(a, src, use.s, !kFP8 && use.s * 128 + 128 > a.I,
-                                                   stage0 + slot * kStage, lane, acc);
+                                                   stage0 + slot * kStage, scales, lane, acc);
       src.x += ks * 128 * (kFP8 ? 1 : 2);
       src.xs += ks;
-      src.scale += ks * (128 / kGroup);
-      src.zero += ks * (128 / kGroup);
       __syncwarp();
+      if (fresh) store_scales<kZeros>(scales, lane, sc);
       issue(stage0 + (slot == 0 ? kStages - 1 : slot - 1) * kStage);
       slot = slot == kStages - 1 ? 0 : slot + 1;
     }
