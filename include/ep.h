@@ -599,7 +599,8 @@ typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score_t;
  *   row_stride elements apart (>= E), any alignment of the element type; bias
  *   [E] float32 (nullable).
  * score: an ep_score_t.  1 <= num_topk <= min(E, EP_MAX_TOPK); num_groups
- *   divides E, 1 <= topk_groups <= num_groups; 1 and 1: no groups.
+ *   divides E and is at most 64, 1 <= topk_groups <= num_groups; 1 and 1: no
+ *   groups.
  * Out (device), every element written: topk_idx [T, K] int64, topk_weights
  *   [T, K] float32.
  */
@@ -680,9 +681,14 @@ ep_status_t ep_ll_combine_backward(const void* dout, const void* y, int hidden, 
  *   byte each in [0, 16) (nullable: every zero point is 8).
  * group_size 32, 64 or 128, dividing I; x_fp8: I % 128 == 0; N % 8 == 0.
  * Out (device): y [E*cap, N] bf16; rows at or beyond n_e are not touched.
- * Rounding: E4M3 codes, and 4-bit codes less their zero point, are exact in
- * bf16.  Scales that do not span a whole matrix step are multiplied into the
- * weight and rounded to bf16 once; the sums are float32 throughout.
+ * E * cap and E * N' below 2^31.
+ * Rounding: codes and zero points are multiplied as the integers they are,
+ * which no type rounds; a group's sum is scaled in float32, and the sums are
+ * float32 throughout.  The zero point may be taken off after the sum (sum q x
+ * - zero sum x), so a group whose weights are all 0 gives a rounding error of
+ * its float32 sums, not always 0, and an infinite x[row][i] may give NaN in its
+ * row where the formula gives an infinity.  Other rows never see it.
+ * err_word (nullable): EP_ERRBIT_TIMEOUT if a wait inside the kernel ran out.
  * ------------------------------------------------------------------------ */
 typedef enum { EP_ACT_NONE = 0, EP_ACT_SWIGLU = 1 } ep_act_t;
 

@@ -2,10 +2,10 @@
 
 Per product p = sum w x: the float32 sum of I terms is off by at most
 I * 2^-23 * sum |w x| (each addition of the tensor cores rounds or truncates
-once), and weights whose scale does not span a step of the kernel are rounded
-to bf16 once (2^-9 of sum |w x|; over a row these are independent, so the
-error of all outputs together is held to 2^-9 of their norm).  The result is
-rounded to bf16 once (2^-9 |y|, 2^-8 here).  silu has a slope of at most 1.1."""
+once).  The bounds below also leave room for a form that rounds each weight to
+bf16 once (2^-9 of sum |w x|; over a row these are independent, so the error
+of all outputs together is held to 2^-9 of their norm).  The result is rounded
+to bf16 once (2^-9 |y|, 2^-8 here).  silu has a slope of at most 1.1."""
 from __future__ import annotations
 
 import numpy as np
