@@ -587,7 +587,8 @@ ep_status_t ep_debug_e4m3_range(uint32_t first, int64_t n, uint8_t* out, ep_stre
  *          weights are computed as the softmax over the chosen logits.
  * Ties, of experts and of groups, go to the lowest index.  An expert whose
  * logit is -inf or NaN is never chosen and counts nowhere, also not in its
- * group's score (a group with none left scores -inf); a slot for which no
+ * group's score (a group with none left scores -inf); one whose bias makes its
+ * key -inf or NaN is never chosen either.  A slot for which no
  * expert is left gets idx -1 and weight 0, the masked slot of every other
  * call.  If the largest softmax logit is +inf, the experts at +inf share the
  * mass equally.  All arithmetic is float32.

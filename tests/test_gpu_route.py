@@ -133,6 +133,57 @@ def test_route_special_rows(ep, E, G, keep, score, renorm):
     assert np.all(np.abs(w - want) <= 4e-6 * np.abs(want) + 1e-30)
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("E,K", [(1, 1), (7, 3), (8, 8), (32, 8), (33, 5), (64, 6), (100, 8), (256, 8),
+                                 (257, 8), (1000, 7), (1024, 8), (1025, 8), (256, 9)])
+def test_route_bf16_keys(ep, E, K, offset, renorm):
+    """Ties, zeros of both signs, NaN of both signs, infinities, the largest
+    and the smallest numbers, in rows aligned or not (offset)."""
+    rng = np.random.default_rng(E + K)
+    x = rng.integers(-2, 3, (70, E)).astype(np.float32)
+    x[x == 0] *= rng.choice([-1.0, 1.0], (x == 0).sum())
+    x[1] = -np.inf
+    x[2] = np.nan
+    x[3] = np.copysign(np.nan, -1)
+    x[4, ::2] = -np.inf
+    x[5, ::3] = np.nan
+    x[6, ::3] = np.copysign(np.nan, -1)
+    x[7, -1] = np.inf
+    x[8] = 2.0 ** -133 * rng.integers(-3, 4, E)  # subnormal
+    x[9] = np.where(rng.random(E) < 0.5, -3.3895314e38, 3.3895314e38)
+    x[10] = rng.standard_normal(E)
+    buf = torch.full((70, E + 8 - E % 8 + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    logits = buf[:, offset:offset + E]
+    logits.copy_(torch.from_numpy(x))
+    idx, w = run_route(ep, logits, K, renormalize=renorm, scale=0.5)
+    back = logits.float().cpu().numpy()
+    assert np.array_equal(idx, ref.choose(ref.route_keys(back, "softmax"), K))
+    want = ref.route_weights(back, idx, "softmax", renorm, 0.5)
+    assert np.all(np.abs(w - want) <= 4e-6 * np.abs(want) + 1e-30)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,keep", [(16, 1, 1), (16, 4, 2), (600, 1, 1), (600, 4, 2)])
+def test_route_bias_that_rules_experts_out(ep, E, G, keep, score):
+    rng = np.random.default_rng(E + G)
+    x = rng.standard_normal((40, E)).astype(np.float32)
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    bias[::2] = -np.inf
+    bias[1] = np.nan
+    bias[E // 2:] = -np.inf  # with groups: some have no expert left
+    idx, w = run_route(ep, torch.from_numpy(x).cuda(), 4, score=score, num_groups=G,
+                       topk_groups=keep, bias=torch.from_numpy(bias).cuda())
+    live = idx[idx >= 0]
+    assert np.isfinite(bias[live]).all() and np.isfinite(w).all() and (w[idx < 0] == 0).all()
+    left = np.isfinite(bias).reshape(G, -1).sum(1)
+    assert ((idx >= 0).sum(1) <= min(4, left.sum())).all()
+    if G == 1:
+        assert ((idx >= 0).sum(1) == min(4, left.sum())).all()
+    want = ref.route_weights(x, idx, score, True, 1.0)
+    assert np.all(np.abs(w - want) <= 4e-6 * np.abs(want) + 1e-30)
+
+
 def test_route_strided_and_unaligned_logits(ep):
     base = torch.randn((41, 300), device="cuda")
     for dtype in (torch.float32, torch.bfloat16):
