@@ -5,7 +5,10 @@
 // one rounding to bf16, and dweights = <dout, y> in float32.  A block takes
 // one token: dout is read once, each of the token's rows of y is read once
 // and its row of dy written once, which is all the traffic there is, so the
-// kernel is bound by DRAM.
+// kernel is bound by DRAM.  Measured: 131072 tokens of 4096 channels, 64
+// experts on 16 ranks, 9.5 GB: 1406 us, 6.8 TB/s (the copy rate); 4096 tokens of
+// 7168 channels, eight expert-major rows each, 1.0 GB: 153 us.  512 tokens of
+// 256 channels: 3.3 us, the launch.
 #include <cuda_bf16.h>
 
 #include "ep_common.cuh"

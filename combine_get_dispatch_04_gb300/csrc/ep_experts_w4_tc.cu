@@ -11,20 +11,29 @@
 // rows are multiplied as they are, at the 8-bit rate.
 //
 // A block takes 128 weight rows (swiglu: 64 of the gate and the same 64 of
-// the up projection) times up to 192 (E4M3: 160) rows of x, with two buffers of sums in
-// tensor memory (2 x 192 columns; the last 128 columns hold A), so that one
-// group's sums are read while the next group is multiplied:
+// the up projection) times up to 192 (E4M3: 160) rows of x, with two buffers of
+// sums in tensor memory (the columns behind them hold A), so that one group's
+// sums are read while the next group is multiplied:
 //   warp 0       TMA of the x tiles (128 channels x the rows, swizzled 128 B)
 //   warp 1       tensor memory, and the tcgen05.mma
 //   warp 2       TMA of the weight codes (128 rows x 64 bytes)
 //   warp 3       group scales, zero points and scales of E4M3 rows, by
 //                4-byte asynchronous copies into shared memory
-//   then         four warps (E4M3: two times four, a step each in turn): codes
-//                -> integers -> operand A
-//   and eight    sums -> scaled -> registers, each four of them for half of
+//   4 to 7       codes -> integers -> operand A
+//   8 to 15      sums -> scaled -> registers, each four of them for half of
 //                the rows; the epilogue
 // Every wait is bounded; a block whose wait runs out reports
 // EP_ERRBIT_TIMEOUT and leaves.
+//
+// What bounds it is the scaling beside the products: every group's sums are
+// read from tensor memory and multiplied into the accumulators (E4M3 rows:
+// after a product with the row's scale), two to an instruction, by the summing
+// warps; without that work the same launch took 712 instead of 779 us (bf16)
+// and 1.50 instead of 1.84 ms (E4M3).  Measured in long runs (960 W): 8 experts of 4096 x 4096, 16384
+// tokens of two experts, bf16 rows: 840 us, 1.31 PFLOP/s; 256 experts, gate and
+// up of 2048 x 7168, 4096 tokens of eight experts, E4M3 rows: 1.95 ms, 0.99
+// PFLOP/s (short runs 774 us and 1.79 ms); about 28 rows an expert, 7168 x
+// 2048: bf16 898 us, E4M3 819 us.
 #include <cuda.h>
 
 #include "ep_experts_w4.cuh"
@@ -41,17 +50,13 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 // one slot of scales.
 template <bool kFP8, int kGroup>
 struct Cfg {
-  // teams of four warps that unpack codes, a step each in turn: E4M3 codes
-  // take 13 integer instructions for 8, bf16 9
-  static constexpr int kTeams = kFP8 ? 2 : 1;
-  static constexpr int kThreads = 128 * (1 + kTeams + kParts);
+  static constexpr int kThreads = 128 * (2 + kParts);
   // registers per thread: at launch, then for the copying, unpacking and
   // summing warps; the split draws on what the launch gave
-  static constexpr int kLaunchRegs = kTeams == 2 ? 96 : 128;
-  static constexpr int kRegsCopy = 56, kRegsUnpack = kTeams == 2 ? 56 : 104;
-  static constexpr int kRegsSum = kTeams == 2 ? 152 : 176;
-  static_assert(128 * (kRegsCopy + kTeams * kRegsUnpack + kParts * kRegsSum) <=
-                    kThreads * kLaunchRegs, "the split would wait for ever");
+  static constexpr int kLaunchRegs = 128;
+  static constexpr int kRegsCopy = 56, kRegsUnpack = 104, kRegsSum = 176;
+  static_assert(128 * (kRegsCopy + kRegsUnpack + kParts * kRegsSum) <= kThreads * kLaunchRegs,
+                "the split would wait for ever");
   // rows of x per block: what the accumulators of two teams hold in registers
   // without moves (E4M3 rows need registers for their scales as well)
   static constexpr int kRows = kFP8 ? 160 : 192;
@@ -77,10 +82,12 @@ struct XMaps {
   CUtensorMap rows[kBoxes];  // [i]: 32 * (i + 1) rows
 };
 
+template <typename C>
 struct Barriers {
   // full: a step's x (one arrival), A (four) and scales (32) are in place;
   // done: its products are finished; sfull: its zero points are in place
-  uint64_t full[5], done[5], wfull[9], wempty[9], sfull[8], pfull[2], pempty[2];
+  uint64_t full[C::kStagesX], done[C::kStagesX], wfull[C::kStagesW], wempty[C::kStagesW];
+  uint64_t sfull[C::kSlotsS], pfull[2], pempty[2];
 };
 
 // --- the items of a block ----------------------------------------------------
@@ -530,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
   constexpr int kPerStep = C::kPerStep;
   constexpr int kMmaPerGroup = kGroup / (kFP8 ? 32 : 16);
   extern __shared__ uint8_t raw[];
-  __shared__ Barriers bar;
+  __shared__ Barriers<C> bar;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
 
@@ -702,11 +709,11 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
       if (!ok) give_up();
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
-  } else if (warp < 4 + 4 * C::kTeams) {
+  } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsUnpack));
     // codes -> operand A: this thread's weight row is lane 32 * quad + lane of
     // tensor memory
-    const int team = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const int quad = warp & 3, r = quad * 32 + lane;
     const int srow = lane_channel<kFP8, kSwiglu>(r) + (lane_is_up<kSwiglu>(r) ? 64 : 0);
     const uint32_t swz = (uint32_t)((srow >> 1) & 3) << 4;
     const uint32_t row_addr = smem_addr(sw) + srow * 64;
@@ -717,7 +724,7 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
     uint32_t base = 0;  // steps of the items before
     for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
       const int at4 = (int)(lane_row<kFP8, kSwiglu>(a, it, r) * groups & 3);
-      for (int b = (int)((team + base) % C::kTeams); b < steps; b += C::kTeams) {
+      for (int b = 0; b < steps; ++b) {
         const uint32_t n = base + b, was = n - C::kSlotsA;  // the step that had the slot of A
         const uint32_t w_slot = n % C::kStagesW, s_slot = n % C::kSlotsS;
         bool fine = wait_idle(wfull0 + w_slot * 8, n / C::kStagesW & 1);
@@ -777,7 +784,7 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
     if (!ok) give_up();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSum));
-    const int h = (warp - 4 - 4 * C::kTeams) >> 2, quad = warp & 3;
+    const int h = (warp - 8) >> 2, quad = warp & 3;
     // E4M3 rows: this thread's lanes 8j + g, columns 2q and 2q + 1 of eight
     const int g = kFP8 ? lane >> 2 : lane, q = kFP8 ? lane & 3 : 0;
     SumArgs sum;
