@@ -29,9 +29,8 @@
 // channels when there are too few tiles for all warps.
 //
 // Measured at 256 experts of 7168 x 2048 (1.9 GB of codes), about two rows
-// each: 534 us with groups of 128 (3.6 TB/s), 610 us with groups of 64 and
-// zero points; E4M3 rows 437 us.  One token, 8 experts, gate and up of
-// 2048 x 7168: 39.5 us.
+// each: 510 us with groups of 128 (3.7 TB/s), 585 us with groups of 64 and
+// zero points.  One token, 8 experts, gate and up of 2048 x 7168: 38 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
