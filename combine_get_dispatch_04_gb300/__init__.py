@@ -195,8 +195,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(device: torch.device):
     if _raw_stream is not None and device.index is not None:
-        return C.c_void_p(_raw_stream(device.index))
-    return C.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
