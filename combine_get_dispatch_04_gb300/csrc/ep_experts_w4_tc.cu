@@ -33,7 +33,7 @@
 // tokens of two experts, bf16 rows: 840 us, 1.31 PFLOP/s; 256 experts, gate and
 // up of 2048 x 7168, 4096 tokens of eight experts, E4M3 rows: 1.95 ms, 0.99
 // PFLOP/s (short runs 774 us and 1.79 ms); about 28 rows an expert, 7168 x
-// 2048: bf16 898 us, E4M3 819 us.
+// 2048: bf16 898 us, E4M3 742 us.
 #include <cuda.h>
 
 #include "ep_experts_w4.cuh"
@@ -69,11 +69,13 @@ struct Cfg {
   static constexpr int kColsA = kFP8 ? 32 + 8 * kPerStep : 64;
   static constexpr int kSlotsA = (512 - 2 * kRows) / kColsA < 4 ? (512 - 2 * kRows) / kColsA : 4;
   static constexpr int kSlotsS = 8;
-  // words of a slot of scales: per group 128 scale words and 128 zero-point
-  // words, then the rows' scales
-  static constexpr int kSWords = kPerStep * 256 + (kFP8 ? kRows : 0);
-  static constexpr int kSmem =
-      1024 + kStagesX * kXBytes + kStagesW * kWBytes + kSlotsS * kSWords * 4;
+  // words of a slot of scales: per group 128 scale words and 128 zero-point words
+  static constexpr int kSWords = kPerStep * 256;
+  // slots for the rows' scales, four steps of all rows each
+  static constexpr int kSlotsXs = kStagesX + 2;
+  static constexpr int kXsBytes = kFP8 ? kRows * 16 : 0;
+  static constexpr int kSmem = 1024 + kStagesX * kXBytes + kStagesW * kWBytes +
+                               kSlotsS * kSWords * 4 + kSlotsXs * kXsBytes;
 };
 
 // One tensor map per height of a box, so that a step of x is one copy (two
@@ -340,7 +342,7 @@ struct SumArgs {
 };
 
 // Adds up all groups of an item for 16 * kChunks rows; n and p count steps
-// and groups over the items.  With bf16 rows a thread holds one weight row
+// and groups over the items, q the slots of the rows' scales.  With bf16 rows a thread holds one weight row
 // times all rows of x; with E4M3 rows four weight rows (j) times a quarter of
 // the rows of x, since the rows' scales, which every thread needs in
 // registers, would else take 640 of the cycles of shared memory for a step,
@@ -350,6 +352,7 @@ struct SumArgs {
 // a chunk.
 template <bool kFP8, int kGroup, int kChunks>
 __device__ __forceinline__ bool add_groups(const SumArgs& s, int lane, uint32_t& n, uint32_t& p,
+                                           uint32_t& q,
                                            uint64_t (&acc)[Cfg<kFP8, kGroup>::kPart / 2]) {
   using C = Cfg<kFP8, kGroup>;
 #pragma unroll 1
@@ -370,7 +373,8 @@ __device__ __forceinline__ bool add_groups(const SumArgs& s, int lane, uint32_t&
       const float f = kFP8 ? __uint_as_float(sv) * 512.0f : __uint_as_float(sv);
       asm("mov.b64 %0, {%1, %1};" : "=l"(scale[j]) : "f"(f));
     }
-    const uint32_t src = s.src + buf * C::kRows, xs = s.xs + slot * C::kSWords * 4;
+    const uint32_t src = s.src + buf * C::kRows, b = g / C::kPerStep;
+    const uint32_t xs = s.xs + q % C::kSlotsXs * C::kXsBytes + (b & 3) * C::kRows * 4;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       // the loads of a chunk together, then all products, then all sums:
@@ -396,6 +400,7 @@ __device__ __forceinline__ bool add_groups(const SumArgs& s, int lane, uint32_t&
     const bool last = C::kPerStep == 1 || in == C::kPerStep - 1 || g == s.groups - 1;
     if (lane == 0) arrive(s.pempty + buf * 8);
     if (last) ++n;
+    if (kFP8 && last && ((b & 3) == 3 || g == s.groups - 1)) ++q;
   }
   return true;
 }
@@ -546,6 +551,7 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
   uint8_t* sx = base;
   uint8_t* sw = sx + C::kStagesX * C::kXBytes;
   uint32_t* ss = reinterpret_cast<uint32_t*>(sw + C::kStagesW * kWBytes);
+  uint8_t* sxs = reinterpret_cast<uint8_t*>(ss + C::kSlotsS * C::kSWords);
 
   if (tid == 0) {
     for (int i = 0; i < C::kStagesX; ++i) mbar_init(&bar.full[i], 37), mbar_init(&bar.done[i], 1);
@@ -682,7 +688,9 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
       // into the buffer whose sums it scaled.  The stages of x are fewer than
       // the slots by more than that, so the x stage's barrier says it.
       static_assert(C::kSlotsS >= C::kStagesX + 2, "a slot would be in use");
+      // The same holds for the slots of the rows' scales, a step at least each.
       Ring<C::kSlotsS> rs;
+      Ring<C::kSlotsXs> rq;
       Ring<C::kStagesX> rx;
       for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
         const float* xs = kFP8 ? a.x_scales + ((int64_t)it.e * a.cap + it.r0) * steps : nullptr;
@@ -706,13 +714,21 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
                 copy_word(dst + g * 256 + 128 + lane + 32 * i, word_of(a.zeros + at[i] + gi));
             }
           }
-          if (kFP8) {
+          if (kFP8 && b % 4 == 0) {
+            // a row's scales of four steps lie in one line: at once they look
+            // it up while it is there (256 experts of 7168 x 2048, 28 rows
+            // each: 742 us; a scale a row each step, 818 us)
+            uint8_t* to = sxs + rq.slot * C::kXsBytes;
 #pragma unroll
             for (int i = 0; i < C::kRows / 32; ++i) {
               const int r = lane + 32 * i;
-              if (r < kParts * it.np)
-                copy_word(dst + kPerStep * 256 + r, xs + min(r, it.rows - 1) * steps + b);
+              if (r >= kParts * it.np) break;
+              const float* from = xs + min(r, it.rows - 1) * steps + b;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (b + j < steps) copy_word(to + (j * C::kRows + r) * 4, from + j);
             }
+            rq.next();
           }
           if (a.zeros) copies_arrive(&bar.sfull[rs.slot]);
           copies_arrive(&bar.full[rx.slot]);
@@ -806,24 +822,24 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
     sum.pempty = smem_addr(bar.pempty);
     sum.scale = smem_addr(ss) + (quad * 32 + g) * 4;
     sum.groups = groups;
-    uint32_t n = 0, p = 0;  // steps and groups
+    uint32_t n = 0, p = 0, c = 0;  // steps, groups, slots of the rows' scales
     for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
       sum.odd = 0;
 #pragma unroll
       for (int j = 0; j < (kFP8 ? 4 : 1); ++j)
         sum.odd |= (uint32_t)(lane_row<kFP8, kSwiglu>(a, it, quad * 32 + j * 8 + g) * groups & 1) << j;
       sum.src = tmem + ((uint32_t)(quad * 32) << 16) + h * it.np;
-      sum.xs = smem_addr(ss) + (kPerStep * 256 + h * it.np + 2 * q) * 4;
+      sum.xs = smem_addr(sxs) + (h * it.np + 2 * q) * 4;
       uint64_t acc[C::kPart / 2];
 #pragma unroll
       for (int i = 0; i < C::kPart / 2; ++i) acc[i] = 0;
       switch (it.np / 16) {
-        case 1: ok = add_groups<kFP8, kGroup, 1>(sum, lane, n, p, acc); break;
-        case 2: ok = add_groups<kFP8, kGroup, 2>(sum, lane, n, p, acc); break;
-        case 3: ok = add_groups<kFP8, kGroup, 3>(sum, lane, n, p, acc); break;
-        case 4: ok = add_groups<kFP8, kGroup, 4>(sum, lane, n, p, acc); break;
-        case 5: ok = add_groups<kFP8, kGroup, 5>(sum, lane, n, p, acc); break;
-        default: ok = add_groups<kFP8, kGroup, C::kPart / 16>(sum, lane, n, p, acc); break;
+        case 1: ok = add_groups<kFP8, kGroup, 1>(sum, lane, n, p, c, acc); break;
+        case 2: ok = add_groups<kFP8, kGroup, 2>(sum, lane, n, p, c, acc); break;
+        case 3: ok = add_groups<kFP8, kGroup, 3>(sum, lane, n, p, c, acc); break;
+        case 4: ok = add_groups<kFP8, kGroup, 4>(sum, lane, n, p, c, acc); break;
+        case 5: ok = add_groups<kFP8, kGroup, 5>(sum, lane, n, p, c, acc); break;
+        default: ok = add_groups<kFP8, kGroup, C::kPart / 16>(sum, lane, n, p, c, acc); break;
       }
       if (!ok) break;
       if constexpr (kFP8)
