@@ -12,11 +12,12 @@
 // moving them to another thread.  The sums of a group are scaled in float32;
 // no weight is rounded.
 //
-// bf16 rows: the codes become 128 + q (the bits of q are the low mantissa
-// bits of 128) and the sum over the group less (128 + zero) * sum(x), which
-// the tensor cores add up with a tile of ones: 7 instructions for 8 codes
-// instead of 11.  E4M3 rows: both sides as f16, where codes less their zero
-// point and E4M3 values are exact.
+// Codes become integers less their zero point before they are multiplied: in
+// bf16 from 128 + q (the bits of q are the low mantissa bits of 128), in f16
+// beside E4M3 rows, both exact.  (Multiplying 128 + q and taking (128 + zero)
+// * sum(x) off afterwards takes 7 instructions for 8 bf16 codes instead of 11
+// and 509 us instead of 531 below, but its sums round at some 30 times the
+// size of the products, and overflow before them.)
 //
 // The floor is the stream of the codes, which the copies alone reach (306 us
 // for 256 experts of 7168 x 2048); what bounds it is the warps' own time: 640
@@ -29,8 +30,9 @@
 // channels when there are too few tiles for all warps.
 //
 // Measured at 256 experts of 7168 x 2048 (1.9 GB of codes), about two rows
-// each: 510 us with groups of 128 (3.7 TB/s), 585 us with groups of 64 and
-// zero points.  One token, 8 experts, gate and up of 2048 x 7168: 38 us.
+// each: 531 us with groups of 128 (3.5 TB/s), 566 us with groups of 64 and
+// zero points; E4M3 rows 410 us.  One token, 8 experts, gate and up of 2048 x
+// 7168: 40.5 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -78,12 +80,16 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 
-// Codes i and i + 4 of the 8 in w (i = 0..3), less nothing (bf16: 128 + q) ...
-__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t (&o)[4]) {
+// Codes i and i + 4 of the 8 in w (i = 0..3) less their zero point, as bf16:
+// 0x4300 | q is 128 + q; zp = 128 + zero, both exact, and so is the difference.
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t zp, uint32_t (&o)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(v), "r"(zp));
+  }
 }
-// ... or less their zero point (f16): 0x6400 | q is 1024 + q, and with q in
+// The same as f16: 0x6400 | q is 1024 + q, and with q in
 // the next four bits 1024 + 16 q, so two of four need no shift.
 // low = -(1024 + zero), high = -(64 + zero), as f16 pairs.
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t low, uint32_t high,
@@ -253,7 +259,7 @@ __device__ __forceinline__ void step_products(const ExpertsArgs& a, const Source
   const int in = kPer == 4 ? 0 : s * kPer & (4 - kPer);
   const uint32_t scale0 = scales + g * 8 + in * 2;
   const uint32_t zero0 = scales + kTileRows * 8 + g * 4 + in;
-  float ones[4] = {}, part[kMT][4] = {};
+  float part[kMT][4] = {};
   uint32_t z[kMT][2];
   uint2 w[kMT][2];
 #pragma unroll
@@ -271,10 +277,7 @@ __device__ __forceinline__ void step_products(const ExpertsArgs& a, const Source
       const uint4 v = xv[j >> 1];
       pairs_e4m3(j & 1 ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y), b);
     } else {
-      constexpr uint32_t k1 = 0x3F803F80u;  // ones
       pairs_bf16(xv[kFP8 ? 0 : j], b);
-      mma_bf16(ones, k1, k1, k1, k1, b[0], b[1]);
-      mma_bf16(ones, k1, k1, k1, k1, b[2], b[3]);
     }
     const int byte = word_channel<kGroup>(t, j) / 2;
     const uint32_t at = stage + ((byte >> 4 ^ chunk_swizzle(g)) << 4) + (byte & 15) + g * 64;
@@ -302,8 +305,8 @@ __device__ __forceinline__ void step_products(const ExpertsArgs& a, const Source
         mma_f16(part[mt], lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
         mma_f16(part[mt], lo[2], hi[2], lo[3], hi[3], b[2], b[3]);
       } else {
-        codes_bf16(w0, lo);
-        codes_bf16(w1, hi);
+        codes_bf16(w0, 0x43004300u | z0 * 0x00010001u, lo);
+        codes_bf16(w1, 0x43004300u | z1 * 0x00010001u, hi);
         mma_bf16(part[mt], lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
         mma_bf16(part[mt], lo[2], hi[2], lo[3], hi[3], b[2], b[3]);
       }
@@ -311,21 +314,15 @@ __device__ __forceinline__ void step_products(const ExpertsArgs& a, const Source
     if ((j + 1) % (4 / kPer) == 0) {  // the end of a group
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
-        const uint32_t z0 = z[mt][0], z1 = z[mt][1];
         const float s0 = __uint_as_float(lds16(scale0 + mt * 128 + q * 2) << 16);
         const float s1 = __uint_as_float(lds16(scale0 + mt * 128 + 64 + q * 2) << 16);
-        // -(128 + z): z << 16 is z in units of 128's last mantissa places
-        const float f0 = __uint_as_float(0xC3000000u | z0 << 16);
-        const float f1 = __uint_as_float(0xC3000000u | z1 << 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float v = kFP8 ? part[mt][i] * xs[i & 1] : fmaf(i < 2 ? f0 : f1, ones[i], part[mt][i]);
+          const float v = kFP8 ? part[mt][i] * xs[i & 1] : part[mt][i];
           acc[mt][i] = fmaf(v, i < 2 ? s0 : s1, acc[mt][i]);
           part[mt][i] = 0.0f;
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ones[i] = 0.0f;
     }
   }
 }

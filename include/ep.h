@@ -683,12 +683,13 @@ ep_status_t ep_ll_combine_backward(const void* dout, const void* y, int hidden, 
  * group_size 32, 64 or 128, dividing I; x_fp8: I % 128 == 0; N % 8 == 0.
  * Out (device): y [E*cap, N] bf16; rows at or beyond n_e are not touched.
  * E * cap and E * N' below 2^31.
- * Rounding: codes and zero points are multiplied as the integers they are,
- * which no type rounds; a group's sum is scaled in float32, and the sums are
- * float32 throughout.  The zero point may be taken off after the sum (sum q x
- * - zero sum x), so a group whose weights are all 0 gives a rounding error of
- * its float32 sums, not always 0, and an infinite x[row][i] may give NaN in its
- * row where the formula gives an infinity.  Other rows never see it.
+ * Rounding: q - zero is multiplied as the integer it is, which no type rounds;
+ * a group's sum is scaled in float32, and the sums are float32 throughout.  For
+ * E4M3 rows of an expert with more than 8 rows, q x and zero x are two products
+ * of the same float32 sum, so a group whose weights are all 0 gives a rounding
+ * error of that sum there, not always 0.  Experts with more than 8 rows are
+ * added up in another order than those with fewer: results may differ in their
+ * last bits between the two.  Infinities and NaN stay in their row of x.
  * err_word (nullable): EP_ERRBIT_TIMEOUT if a wait inside the kernel ran out.
  * ------------------------------------------------------------------------ */
 typedef enum { EP_ACT_NONE = 0, EP_ACT_SWIGLU = 1 } ep_act_t;

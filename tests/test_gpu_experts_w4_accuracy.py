@@ -110,6 +110,32 @@ def test_accuracy_of_long_rows_with_a_mean(ep, rows, fp8):
     run(ep, 1, rows, 7168, 136, 128, "none", fp8, True, [rows], seed=rows, mean=1.0)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [3, 40])
+def test_large_channel_at_its_zero_point(ep, rows, fp8):
+    """A channel whose codes are the zero points adds nothing, however large:
+    the other channels' sum keeps its accuracy.  (E4M3: 448 is the largest;
+    with many rows its code and its zero point are separate products.)"""
+    I, N = 512, 64
+    x, xs, W, L = make(ep, 1, rows, I, N, 128, "none", fp8, False, [rows], 1)
+    W.q[:, :, 10] = 8 | 8 << 4
+    x[:, 20:22] = 0x7E if fp8 else 2.0 ** 20
+    out = torch.full((rows, N), -7.0, dtype=torch.bfloat16, device="cuda")
+    ep.ll_experts_w4(x, W, L, x_scales=xs, out=out)
+    check(out, W, L, x, xs, [rows], "none")
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+def test_large_finite_rows_stay_finite(ep, rows):
+    """(q - zero) * x is at most 8 * 2^122 here, far from float32's limit."""
+    I, N = 256, 64
+    x, xs, W, L = make(ep, 1, rows, I, N, 128, "none", False, False, [rows], 2)
+    x[:, 5] = 2.0 ** 122
+    out = torch.full((rows, N), -7.0, dtype=torch.bfloat16, device="cuda")
+    ep.ll_experts_w4(x, W, L, out=out)
+    check(out, W, L, x, xs, [rows], "none")
+
+
 def sm_count():
     return torch.cuda.get_device_properties(0).multi_processor_count
 
