@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(GradArgs a) {
       const float s = part_sum<SL>(u), r = s > 0.0f ? 1.0f / s : 0.0f;
       du = (dw - part_sum<SL>(dw * (u * r))) * r;
     }
-    g = du * u * (1.0f - u);
+    g = du * u * sigmoid_rn(-l);  // 1 - u would cancel: 0 from l = 17 on
   } else {
     const float top = part_max<SL>(l);
     const float x = live ? exp_from(l, top) : 0.0f, s = part_sum<SL>(x);
