@@ -1,4 +1,5 @@
-"""GPU: the router's gradient where float32 is tight: confident sigmoid scores.
+"""GPU: the router's gradient where float32 is tight: confident sigmoid scores,
+and scores near the smallest that float32 holds.
 
 Without renormalisation a gradient is scale * dw * s * (1 - s): two exponentials
 (2 ulp each), two sums, two reciprocals and three products, 16 roundings of
@@ -39,3 +40,23 @@ def test_gradient_of_confident_sigmoid_scores(ep, E, K, dtype):
     if dtype == torch.bfloat16:  # rounded once: between the roundings of the ends
         lo, hi = (torch.from_numpy(v).float().to(dtype).double().numpy() for v in (lo, hi))
     assert ((got >= lo) & (got <= hi)).all(), np.abs(got / np.where(want, want, 1) - 1).max()
+
+
+@pytest.mark.parametrize("E,K", [(16, 4), (600, 12)])
+def test_renormalised_gradient_of_the_smallest_sigmoid_scores(ep, E, K):
+    """Scores of 3e-39 to 1e-38 (good to 2^-149: 5e-7) still have weights of order
+    one, so the gradient is finite: w (dw - sum w dw) (1 - s), within 1e-5 of
+    scale * max |dw|."""
+    rng = np.random.default_rng(K)
+    T = 40
+    logits = rng.uniform(-88.6, -87.4, (T, E)).astype(np.float32)
+    ids = np.stack([rng.permutation(E)[:K] for _ in range(T)]).astype(np.int64)
+    dw = (rng.standard_normal((T, K)) * 100).astype(np.float32)
+    got = ep.route_backward(torch.from_numpy(dw).cuda(), torch.from_numpy(logits).cuda(),
+                            torch.from_numpy(ids).cuda(), score="sigmoid").double().cpu().numpy()
+    u = sigmoid64(np.take_along_axis(logits.astype(np.float64), ids, 1))
+    w = u / u.sum(1, keepdims=True)
+    want = np.zeros((T, E))
+    np.put_along_axis(want, ids, w * (dw - (w * dw).sum(1, keepdims=True)) * (1 - u), 1)
+    assert np.isfinite(got).all()
+    assert np.abs(got - want).max() <= 1e-5 * np.abs(dw).max()
