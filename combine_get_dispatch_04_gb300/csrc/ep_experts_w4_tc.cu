@@ -462,13 +462,14 @@ __device__ __forceinline__ void store_rows(const ExpertsArgs& a, const Item& it,
   const int left = min(it.rows - h * it.np, it.np);  // live rows of this part
   __nv_bfloat16* dst =
       a.y + ((int64_t)it.e * a.cap + it.r0 + h * it.np + (kSwiglu ? lane >> 4 : 0)) * a.N + n0;
+  // the lanes that stay (a lane and the one 16 further have the same channel)
+  const unsigned in = __ballot_sync(kFull, n0 < a.N);
   if (n0 >= a.N) {
     // a channel beyond the last tile's end
   } else if (kSwiglu) {
     // lanes 0-15 hold the gate, 16-31 the up projection of the same
     // channels: the lower lanes finish the first row of each pair, the
     // upper ones the second
-    const unsigned in = __activemask();
 #pragma unroll
     for (int i = 0; i < kPart / 2; ++i) {
       if (2 * i >= left) break;
