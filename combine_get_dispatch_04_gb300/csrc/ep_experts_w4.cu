@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(ExpertsArgs a) {
           v0 += p[ch * 8 + r];
           if (kSwiglu) v1 += p[(kChannels + ch) * 8 + r];
         }
-        if (kSwiglu) v0 = v0 / (1.0f + expf(-v0)) * v1;
+        if (kSwiglu) v0 = silu_times(v0, v1);
         if (use.n0 + ch < a.N) y[(int64_t)r * a.N + use.n0 + ch] = __float2bfloat16_rn(v0);
       }
       asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(ks * 32) : "memory");
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(ExpertsArgs a) {
 #pragma unroll
         for (int mt = 0; mt < (kSwiglu ? kMT / 2 : kMT); ++mt) {
           float v = acc[mt][i];
-          if (kSwiglu) v = v / (1.0f + expf(-v)) * acc[mt + kMT / 2][i];
+          if (kSwiglu) v = silu_times(v, acc[mt + kMT / 2][i]);
           if (ch + mt * 16 < a.N) y[(int64_t)r * a.N + ch + mt * 16] = __float2bfloat16_rn(v);
         }
       }

@@ -476,8 +476,7 @@ __device__ __forceinline__ void store_rows(const ExpertsArgs& a, const Item& it,
       const float2 v = unpack2(acc[i]);
       const float other = __shfl_xor_sync(in, lane < 16 ? v.y : v.x, 16);
       const float gate = lane < 16 ? v.x : other, up = lane < 16 ? other : v.y;
-      // a few units in the last place of float32, rounded to bf16 next
-      const float out = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+      const float out = silu_times(gate, up);
       if (2 * i + (lane >> 4) < left) *dst = __float2bfloat16_rn(out);
       dst += 2 * a.N;
     }
@@ -514,9 +513,7 @@ __device__ __forceinline__ void store_fragment(const ExpertsArgs& a, const Item&
                             k ? v[3].y : v[3].x};
         if (8 * i + 2 * q + k < left) {
           if (kSwiglu) {
-            // a few units in the last place of float32, rounded to bf16 next
-            const float o0 = __fdividef(f[0], 1.0f + __expf(-f[0])) * f[2];
-            const float o1 = __fdividef(f[1], 1.0f + __expf(-f[1])) * f[3];
+            const float o0 = silu_times(f[0], f[2]), o1 = silu_times(f[1], f[3]);
             *reinterpret_cast<__nv_bfloat162*>(dst + k * a.N) =
                 g < 4 ? __floats2bfloat162_rn(o0, o1) : __floats2bfloat162_rn(o1, o0);
           } else {

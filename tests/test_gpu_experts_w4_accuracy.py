@@ -136,6 +136,28 @@ def test_large_finite_rows_stay_finite(ep, rows):
     check(out, W, L, x, xs, [rows], "none")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [3, 12])
+def test_swiglu_of_very_negative_gates(ep, rows, fp8):
+    """exp(gate) down to 1e-40 (a subnormal, good to 2^-149 / 1e-40 < 2e-5)
+    times an up projection of 2^115: results that bf16 holds."""
+    gates = [60.0, 87.0, 87.5, 88.0, 88.5, 89.0, 90.0, 91.0]
+    N = len(gates)
+    q = torch.full((1, 2 * N, 64), 0x88, dtype=torch.uint8, device="cuda")
+    q[0, :N, 0], q[0, N:, 0] = 0x87, 0x89  # channel 0: -1 for the gate, +1 for up
+    scales = torch.tensor(gates + [2.0 ** 115] * N, device="cuda").to(torch.bfloat16).reshape(1, 2 * N, 1)
+    L = ep.LLLayout(None, torch.tensor([rows], dtype=torch.int32, device="cuda"), None, 1, 1, rows)
+    xs = None
+    if fp8:
+        x, xs = torch.full((rows, 128), 0x38, dtype=torch.uint8, device="cuda"), torch.ones((rows, 1), device="cuda")
+    else:
+        x = torch.ones((rows, 128), dtype=torch.bfloat16, device="cuda")
+    got = ep.ll_experts_w4(x, ep.W4Weights(q, scales), L, x_scales=xs, act="swiglu").double()
+    g = -scales[0, :N, 0].double()
+    want = g * torch.sigmoid(g) * 2.0 ** 115
+    assert between(got, want, 1e-4 * want.abs()), (got[0], want)
+
+
 def sm_count():
     return torch.cuda.get_device_properties(0).multi_processor_count
 
