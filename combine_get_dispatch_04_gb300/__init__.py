@@ -847,7 +847,7 @@ class W4Weights:
     and zero point per group of consecutive input channels."""
     q: torch.Tensor             # [E, N', I / 2] uint8, channel 2j low half, 2j + 1 high half of byte j
     scales: torch.Tensor        # [E, N', I / group] bfloat16
-    zeros: torch.Tensor | None = None  # [E, N', I / group] uint8 in [0, 16); None: 8 everywhere
+    zeros: torch.Tensor | None = None  # [E, N', I / group] uint8, the low four bits; None: 8 everywhere
 
 
 def quantize_w4(weight: torch.Tensor, group_size: int = 128, *,

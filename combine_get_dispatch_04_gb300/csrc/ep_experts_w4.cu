@@ -193,7 +193,7 @@ __device__ __forceinline__ void load_scales(const Sources& src, int g0, int lane
     const uint8_t* z = src.zero + at;
     if (groups % 4 == 0) {
       v.s[i] = __ldg(reinterpret_cast<const uint2*>(u));
-      if (kZeros) v.z[i] = __ldg(reinterpret_cast<const uint32_t*>(z));
+      if (kZeros) v.z[i] = __ldg(reinterpret_cast<const uint32_t*>(z)) & 0x0F0F0F0Fu;
     } else {
       uint32_t f[4], w = 0;
 #pragma unroll
@@ -203,7 +203,7 @@ __device__ __forceinline__ void load_scales(const Sources& src, int g0, int lane
         if (kZeros) w |= (uint32_t)__ldg(z + k) << (8 * q);
       }
       v.s[i] = make_uint2(f[0] | f[1] << 16, f[2] | f[3] << 16);
-      if (kZeros) v.z[i] = w;
+      if (kZeros) v.z[i] = w & 0x0F0F0F0Fu;
     }
   }
 }

@@ -679,7 +679,7 @@ ep_status_t ep_ll_combine_backward(const void* dout, const void* y, int hidden, 
  *   [E*cap, I/128] float32, as ep_ll_dispatch leaves them; ll_count [E] int32;
  *   q [E, N', I/2] bytes, channel i in the low (i even) or high (i odd) half of
  *   byte i/2; scales [E, N', I/group_size] bf16; zeros of the same shape, one
- *   byte each in [0, 16) (nullable: every zero point is 8).
+ *   byte each, of which the low four bits count (nullable: every zero point is 8).
  * group_size 32, 64 or 128, dividing I; x_fp8: I % 128 == 0; N % 8 == 0.
  * Out (device): y [E*cap, N] bf16; rows at or beyond n_e are not touched.
  * E * cap and E * N' below 2^31.

@@ -158,6 +158,18 @@ def test_swiglu_of_very_negative_gates(ep, rows, fp8):
     assert between(got, want, 1e-4 * want.abs()), (got[0], want)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [3, 12])
+def test_zero_points_count_by_their_low_four_bits(ep, rows, fp8):
+    x, xs, W, L = make(ep, 2, rows, 384, 40, 128, "none", fp8, True, [rows, 1], 3)
+    a = torch.zeros((2 * rows, 40), dtype=torch.bfloat16, device="cuda")
+    b = torch.zeros_like(a)
+    ep.ll_experts_w4(x, W, L, x_scales=xs, out=a)
+    W.zeros |= 0xF0
+    ep.ll_experts_w4(x, W, L, x_scales=xs, out=b)
+    assert torch.equal(a, b)
+
+
 def sm_count():
     return torch.cuda.get_device_properties(0).multi_processor_count
 
