@@ -194,7 +194,9 @@ bool grad_ok(const void* dout, const void* y, int hidden, int64_t rows, const fl
   if (T == 0) return true;
   if (!dout || !slot || !w || !aligned16(dout) || !aligned16(y) || !aligned16(dy)) return false;
   if (dw && !y && rows > 0) return false;
-  return true;
+  // a row of dy is written while other tokens still read dout and y
+  const uint64_t row = 2 * (uint64_t)hidden;
+  return !overlap(dy, rows * row, dout, T * row) && !overlap(dy, rows * row, y, rows * row);
 }
 
 }  // namespace

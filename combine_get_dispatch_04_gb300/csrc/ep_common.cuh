@@ -20,6 +20,12 @@ inline cudaStream_t to_cuda(ep_stream_t s) { return reinterpret_cast<cudaStream_
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether two buffers of these sizes (in bytes; a null one: none) share a byte.
+inline bool overlap(const void* p, uint64_t pn, const void* q, uint64_t qn) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && pn && qn && (a < b ? b - a < pn : a - b < qn);
+}
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 inline ep_status_t launch_status() {

@@ -577,6 +577,10 @@ extern "C" ep_status_t ep_ll_experts_w4(const void* x, int x_fp8, const float* x
   if (!aligned16(x) || !aligned16(x_scales) || !aligned16(q) || !aligned16(scales) ||
       !aligned16(zeros) || !aligned16(y) || !aligned16(ll_count))
     return EP_ERR_INVALID_ARG;
+  // rows of y are written while other tiles still read x
+  const uint64_t all = (uint64_t)num_experts * expert_capacity;
+  if (overlap(y, all * out_channels * 2, x, all * in_channels * (x_fp8 ? 1 : 2)))
+    return EP_ERR_INVALID_ARG;
   ExpertsArgs a = {};
   a.x = static_cast<const uint8_t*>(x);
   a.x_scales = x_scales;

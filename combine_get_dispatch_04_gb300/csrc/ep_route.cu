@@ -775,6 +775,10 @@ extern "C" ep_status_t ep_route_backward(const float* dweights, const void* logi
   if (!dweights || !topk_idx || !dlogits || !aligned16(dweights) || !aligned16(topk_idx) ||
       !aligned16(dlogits))
     return EP_ERR_INVALID_ARG;
+  const uint64_t size = logits_bf16 ? 2 : 4;
+  if (overlap(dlogits, num_tokens * num_experts * size, logits,
+              ((num_tokens - 1) * row_stride + num_experts) * size))
+    return EP_ERR_INVALID_ARG;
   const GradArgs a = {dweights,    logits,           row_stride,       topk_idx,
                       num_tokens,  num_experts,      num_topk,         score == EP_SCORE_SIGMOID,
                       renormalize != 0, scale,       dlogits,          err_word,

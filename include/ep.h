@@ -681,7 +681,8 @@ ep_status_t ep_ll_combine_backward(const void* dout, const void* y, int hidden, 
  *   byte i/2; scales [E, N', I/group_size] bf16; zeros of the same shape, one
  *   byte each, of which the low four bits count (nullable: every zero point is 8).
  * group_size 32, 64 or 128, dividing I; x_fp8: I % 128 == 0; N % 8 == 0.
- * Out (device): y [E*cap, N] bf16; rows at or beyond n_e are not touched.
+ * Out (device): y [E*cap, N] bf16; rows at or beyond n_e are not touched.  y and
+ *   x must not overlap.
  * E * cap and E * N' below 2^31.
  * Rounding: q - zero is multiplied as the integer it is, which no type rounds;
  * a group's sum is scaled in float32, and the sums are float32 throughout.  For
