@@ -855,7 +855,7 @@ def quantize_w4(weight: torch.Tensor, group_size: int = 128, *,
     """Rounds weights [E, N', I] to W4Weights, on the weights' device (set-up
     work in torch, once per model).  Without zero points the scale maps a
     group's largest magnitude to 7; with them, its range to [0, 15]."""
-    if weight.dim() != 3 or weight.shape[2] % group_size or group_size not in (32, 64, 128):
+    if group_size not in (32, 64, 128) or weight.dim() != 3 or weight.shape[2] % group_size:
         raise EPError("weight must be [E, N, I] with I a multiple of group_size (32, 64 or 128)")
     E, N, I = weight.shape
     w = weight.float().reshape(E, N, I // group_size, group_size)
