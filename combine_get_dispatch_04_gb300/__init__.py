@@ -54,7 +54,7 @@ EXPORTED = ("ep_status_string", "ep_workspace_bytes", "ep_get_dispatch_layout",
             "ep_shard_workspace_bytes", "ep_shard_layout", "ep_shard_offsets",
             "ep_shard_recv_tokens_per_expert", "ep_debug_e4m3_range",
             "ep_route", "ep_route_backward", "ep_combine_backward", "ep_ll_combine_backward",
-            "ep_ll_experts_w4")
+            "ep_ll_experts_w4", "ep_debug_set_experts_stall")
 
 # 64-bit words of a combine's scheduling counters (EP_COMBINE_SCHED_WORDS)
 COMBINE_SCHED_WORDS = 2
@@ -128,6 +128,8 @@ def load(path: str | None = None) -> C.CDLL:
     L.ep_combine_backward.argtypes = [P, P, i32, i64, P, P, i64, i32, i32, i32, P, P, P, P, P]
     L.ep_ll_combine_backward.argtypes = [P, P, i32, i64, P, i64, i32, P, P, P, P, P]
     L.ep_ll_experts_w4.argtypes = [P, i32, P, i32, P, i32, i64, P, P, P, i32, i32, i32, P, P, P]
+    L.ep_debug_set_experts_stall.argtypes = [i32]
+    L.ep_debug_set_experts_stall.restype = None
     for name in ("ep_route", "ep_route_backward", "ep_combine_backward",
                  "ep_ll_combine_backward", "ep_ll_experts_w4"):
         getattr(L, name).restype = i32

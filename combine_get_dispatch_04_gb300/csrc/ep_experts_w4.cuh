@@ -34,6 +34,7 @@ struct ExpertsArgs {
   int tiles;  // tiles of output channels per expert
   __nv_bfloat16* y;
   int32_t* err;
+  int stall;  // test hook: a step of x that block 0 does not load (-1: off)
 };
 
 // g / (1 + exp(-g)) * up with the exponential of -|g|, which cannot overflow: the

@@ -224,12 +224,11 @@ __device__ __forceinline__ void tmem_ld_fragment(uint32_t addr, uint32_t (&v)[16
 }
 
 // Waits for the phase of the barrier at `bar` (a shared address) with the
-// given parity; false if it has not completed after kTries tries.  A try
-// takes some tens of cycles, and the hardware may suspend it for up to a
-// microsecond: the limit is between a tenth of a second and a few seconds.
+// given parity; false if it has not completed after kTries tries.  The hardware
+// suspends a try for 3.7 us (measured: 2^20 tries took 3.9 s): about 1 s in all.
 // (Four instructions a try: the warps that wait share their schedulers with
-// those that work.)
-constexpr uint32_t kTries = 1u << 22;
+// those that work, and a limit by the clock after the tries took 2% longer.)
+constexpr uint32_t kTries = 1u << 18;
 #define EP_WAIT(kPause)                                                       \
   uint32_t left;                                                              \
   asm volatile(                                                               \
@@ -602,6 +601,7 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsCopy));
     if (warp == 0 && lane == 0) {  // x tiles
       Ring<C::kStagesX> rx;
+      int unarmed = blockIdx.x == 0 ? a.stall : -1;  // test hook: steps until one is left out
       for (int item = blockIdx.x; ok && walk.at<C::kRows>(a, item, &it) && !*abort; item += gridDim.x) {
         const int row = (int)(it.e * a.cap) + it.r0;
         const CUtensorMap* map = &xmaps.rows[it.np / (32 / kParts) - 1];
@@ -609,10 +609,12 @@ __global__ void __launch_bounds__(Cfg<kFP8, kGroup>::kThreads, 1)
         for (int b = 0; b < steps; ++b) {
           ok = wait_idle(&bar.done[rx.slot], rx.round ^ 1);
           if (!ok) break;
-          uint8_t* dst = sx + rx.slot * C::kXBytes;
-          mbar_arrive_expect_tx(&bar.full[rx.slot], bytes);
-          tma_2d(dst, map, b * 128, row, &bar.full[rx.slot]);
-          if (!kFP8) tma_2d(dst + C::kRows * 128, map, b * 128 + 64, row, &bar.full[rx.slot]);
+          if (unarmed-- != 0) {
+            uint8_t* dst = sx + rx.slot * C::kXBytes;
+            mbar_arrive_expect_tx(&bar.full[rx.slot], bytes);
+            tma_2d(dst, map, b * 128, row, &bar.full[rx.slot]);
+            if (!kFP8) tma_2d(dst + C::kRows * 128, map, b * 128 + 64, row, &bar.full[rx.slot]);
+          }
           rx.next();
         }
       }
@@ -892,6 +894,8 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, uint
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+thread_local int g_stall_step = -1;  // set by ep_debug_set_experts_stall, used once
+
 template <bool kFP8, bool kSwiglu, int kGroup>
 ep_status_t launch(ExpertsArgs a, cudaStream_t st) {
   using C = Cfg<kFP8, kGroup>;
@@ -927,6 +931,8 @@ ep_status_t launch(ExpertsArgs a, cudaStream_t st) {
     return EP_ERR_CUDA;
   const int width = kSwiglu ? 64 : 128;
   a.tiles = (a.N + width - 1) / width;
+  a.stall = g_stall_step;
+  g_stall_step = -1;
   launch_pdl(kernel, props.sm_count, C::kThreads, C::kSmem, st, a, xmaps, wmap);
   return launch_status();
 }
@@ -949,3 +955,5 @@ ep_status_t launch_experts_many(const ExpertsArgs& a, bool fp8, bool swiglu, int
 }
 
 }  // namespace ep
+
+extern "C" void ep_debug_set_experts_stall(int step) { ep::g_stall_step = step < 0 ? -1 : step; }

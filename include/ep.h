@@ -691,7 +691,8 @@ ep_status_t ep_ll_combine_backward(const void* dout, const void* y, int hidden, 
  * error of that sum there, not always 0.  Experts with more than 8 rows are
  * added up in another order than those with fewer: results may differ in their
  * last bits between the two.  Infinities and NaN stay in their row of x.
- * err_word (nullable): EP_ERRBIT_TIMEOUT if a wait inside the kernel ran out.
+ * err_word (nullable): EP_ERRBIT_TIMEOUT if a wait inside the kernel ran out
+ *   (after about 1 s; rows of y are then missing).
  * ------------------------------------------------------------------------ */
 typedef enum { EP_ACT_NONE = 0, EP_ACT_SWIGLU = 1 } ep_act_t;
 
@@ -700,6 +701,16 @@ ep_status_t ep_ll_experts_w4(const void* x, int x_fp8, const float* x_scales, in
                              const uint8_t* q, const void* scales, const uint8_t* zeros,
                              int group_size, int out_channels, int act, void* y,
                              int32_t* err_word, ep_stream_t stream);
+
+/*
+ * Test hook for the bounded waits of ep_ll_experts_w4: the next launch from this
+ * host thread of its kernel for more than 8 rows an expert leaves step `step`
+ * (128 channels; counted over the block's work) of its first block unloaded,
+ * so the waits on it run out after about 1 s.  The launch then reports
+ * EP_ERRBIT_TIMEOUT, the block's remaining results are missing, and it returns.
+ * One-shot; -1 cancels it.
+ */
+void ep_debug_set_experts_stall(int step);
 
 #ifdef __cplusplus
 }
