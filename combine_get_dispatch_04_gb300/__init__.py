@@ -801,7 +801,8 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, topk_idx: torch.Tensor
                      ) -> tuple[torch.Tensor, torch.Tensor]:
     """Gradient of combine(y, topk_idx, topk_weights, layout) for the gradient
     dout [T, H] of its output: (dy like y, dweights [T, K] float32).  Rows of
-    dy that no slot names keep what `out` holds (zeros without `out`).
+    dy that no slot names keep what `out` holds (zeros without `out`, at the
+    cost of writing all of dy first).
     Enqueued on the current stream."""
     if topk_idx.dim() != 2:
         raise EPError("topk_idx must be [num_tokens, num_topk]")

@@ -20,8 +20,8 @@
 // size of the products, and overflow before them.)
 //
 // The floor is the stream of the codes, which the copies alone reach (306 us
-// for 256 experts of 7168 x 2048); what bounds it is the warps' own time: 640
-// instructions a step, two cycles each for those of the integer pipe, and the
+// for 256 experts of 7168 x 2048); what bounds it is the warps' own time: about
+// 670 instructions a step, two cycles each for those of the integer pipe, and the
 // latencies that four warps a scheduler leave open (the register file holds
 // no more).  So every warp keeps two steps on their way with asynchronous
 // copies, across the ends of its tiles, pointers advance instead of being
@@ -29,10 +29,10 @@
 // (their columns are not stored).  The warps of a block share a tile by its
 // channels when there are too few tiles for all warps.
 //
-// Measured at 256 experts of 7168 x 2048 (1.9 GB of codes), about two rows
-// each: 531 us with groups of 128 (3.5 TB/s), 566 us with groups of 64 and
-// zero points; E4M3 rows 410 us.  One token, 8 experts, gate and up of 2048 x
-// 7168: 40.5 us.
+// Measured at 256 experts of 2048 -> 7168 channels (1.9 GB of codes), about two
+// rows each: 531 us with groups of 128 (3.5 TB/s), 566-595 us with groups of 64
+// and zero points; 7168 -> 2048 channels, 457 us, E4M3 rows 409 us.  One token,
+// 8 experts, gate and up of 2048 x 7168: 40.3 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 

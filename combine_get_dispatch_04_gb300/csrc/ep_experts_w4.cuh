@@ -4,11 +4,12 @@
 // An expert with at most kFewRows rows is bound by reading its weights and
 // goes to the register kernel (ep_experts_w4.cu); one with more goes to the
 // tcgen05 kernel (ep_experts_w4_tc.cu).  The counts are on the device, so
-// each kernel skips the other's experts.  Measured on 256 experts of 7168 x
-// 2048, bf16 rows, register against tcgen05 kernel: about 2 rows each 531
-// against 769 us, 6 rows 636 against 898 (E4M3 rows 572 against 810).  A form
-// of the register kernel for up to 32 rows took 983 us at 10 rows and 2144 at
-// 20, where the tcgen05 kernel of that time took 831 and 985.
+// each kernel skips the other's experts.  Measured on 256 experts of 7168 ->
+// 2048 channels, register against tcgen05 kernel: about 2 rows each 457 against
+// 772 us, 4 rows 550 against 878, 6 rows 635 against 879, 8 rows (some experts
+// have more) 711 against 879; E4M3 rows: 2 rows 409 against 607, 6 rows 565
+// against 690.  A form of the register kernel for up to 32 rows took 983 us at
+// 10 rows and 2144 at 20, where the tcgen05 kernel of that time took 831 and 985.
 #pragma once
 
 #include <cuda_bf16.h>

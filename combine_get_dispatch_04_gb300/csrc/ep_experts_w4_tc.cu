@@ -29,11 +29,11 @@
 // read from tensor memory and multiplied into the accumulators (E4M3 rows:
 // after a product with the row's scale), two to an instruction, by the summing
 // warps; without that work the same launch took 712 instead of 779 us (bf16)
-// and 1.50 instead of 1.84 ms (E4M3).  Measured in long runs (960 W): 8 experts of 4096 x 4096, 16384
-// tokens of two experts, bf16 rows: 840 us, 1.31 PFLOP/s; 256 experts, gate and
-// up of 2048 x 7168, 4096 tokens of eight experts, E4M3 rows: 1.95 ms, 0.99
-// PFLOP/s (short runs 774 us and 1.79 ms); about 28 rows an expert, 7168 x
-// 2048: bf16 898 us, E4M3 742 us.
+// and 1.50 instead of 1.84 ms (E4M3).  Measured in long runs (960 W): 8 experts
+// of 4096 x 4096, 16384 tokens of two experts, bf16 rows: 820-840 us, 1.31-1.34
+// PFLOP/s; 256 experts, gate and up of 2048 x 7168, 4096 tokens of eight experts,
+// E4M3 rows: 1.89-1.95 ms, 0.99-1.02 PFLOP/s (short runs 780 us and 1.84 ms);
+// about 28 rows an expert, 7168 -> 2048 channels: bf16 874 us, E4M3 696 us.
 #include <cuda.h>
 
 #include "ep_experts_w4.cuh"

@@ -500,7 +500,7 @@ struct GradArgs {
 // kept in shared memory as exp(l - max)).  Everything stays within a warp.
 // Bound by DRAM, and by the passes over the row in shared memory where that is
 // kept: 32768 tokens of 256 experts, float32, sigmoid scores: 12.0 us (its
-// bytes take 5.7); 131072 tokens of 64 experts, bf16, dense: 20.3 us (6.4).
+// bytes take 5.7); 131072 tokens of 64 experts, bf16, dense: 20.4 us (6.4).
 template <int SL>
 __device__ __forceinline__ float part_sum(float v) {
 #pragma unroll
