@@ -32,6 +32,9 @@ EP_ERRBIT_SCHED = 8
 EP_MAX_RANKS = 64
 EP_MAX_TOPK = 32
 EP_MAX_EXPERTS = 4096
+EP_LAYER_MAX_TOKENS = 16
+EP_LAYER_MAX_EXPERTS = 1024
+EP_NORM_MAX_HIDDEN = 16384
 
 # ep_layout_path_t
 LAYOUT_PATHS = {"auto": 0, "multi": 1, "single": 2}
@@ -39,6 +42,8 @@ LAYOUT_PATHS = {"auto": 0, "multi": 1, "single": 2}
 # ep_score_t, ep_act_t
 SCORES = {"softmax": 0, "sigmoid": 1}
 ACTS = {"none": 0, "swiglu": 1}
+# ep_gate_t
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = range(4)
 
 # every entry point declared in include/ep.h
 EXPORTED = ("ep_status_string", "ep_workspace_bytes", "ep_get_dispatch_layout",
@@ -54,7 +59,10 @@ EXPORTED = ("ep_status_string", "ep_workspace_bytes", "ep_get_dispatch_layout",
             "ep_shard_workspace_bytes", "ep_shard_layout", "ep_shard_offsets",
             "ep_shard_recv_tokens_per_expert", "ep_debug_e4m3_range",
             "ep_route", "ep_route_backward", "ep_combine_backward", "ep_ll_combine_backward",
-            "ep_ll_experts_w4", "ep_debug_set_experts_stall")
+            "ep_ll_experts_w4", "ep_debug_set_experts_stall",
+            "ep_layer_w4", "ep_layer_w4_workspace_bytes", "ep_block_norm",
+            "ep_block_norm_backward", "ep_block_norm_backward_workspace_bytes",
+            "ep_ll_swiglu", "ep_ll_swiglu_backward")
 
 # 64-bit words of a combine's scheduling counters (EP_COMBINE_SCHED_WORDS)
 COMBINE_SCHED_WORDS = 2
@@ -130,8 +138,21 @@ def load(path: str | None = None) -> C.CDLL:
     L.ep_ll_experts_w4.argtypes = [P, i32, P, i32, P, i32, i64, P, P, P, i32, i32, i32, P, P, P]
     L.ep_debug_set_experts_stall.argtypes = [i32]
     L.ep_debug_set_experts_stall.restype = None
+    L.ep_layer_w4_workspace_bytes.argtypes = [i64, i32, i32]
+    L.ep_layer_w4_workspace_bytes.restype = sz
+    L.ep_layer_w4.argtypes = [P, i32, i32, i64, P, i32, i64, P, i32, i32, i32, i32, i32, i32, f32,
+                              P, P, P, i32, P, P, P, i32, P, P, P, P, sz, P]
+    L.ep_block_norm.argtypes = [P, i32, P, i64, P, i32, P, i64, i32, P, i32, P, P, i32, f32, f32,
+                                P, P, P, P, P]
+    L.ep_block_norm_backward_workspace_bytes.argtypes = [i64, i32]
+    L.ep_block_norm_backward_workspace_bytes.restype = sz
+    L.ep_block_norm_backward.argtypes = [P, P, P, i32, P, i64, i32, P, i32, P, P, i32, f32, f32,
+                                         P, P, P, P, P, P, sz, P]
+    L.ep_ll_swiglu.argtypes = [P, i32, i64, P, i64, i32, P, P, P, P, P, P]
+    L.ep_ll_swiglu_backward.argtypes = [P, P, P, P, i32, i64, P, i64, i32, P, P, P, P, P]
     for name in ("ep_route", "ep_route_backward", "ep_combine_backward",
-                 "ep_ll_combine_backward", "ep_ll_experts_w4"):
+                 "ep_ll_combine_backward", "ep_ll_experts_w4", "ep_layer_w4", "ep_block_norm",
+                 "ep_block_norm_backward", "ep_ll_swiglu", "ep_ll_swiglu_backward"):
         getattr(L, name).restype = i32
     for name in ("ep_get_dispatch_layout", "ep_get_dispatch_layout_path",
                  "ep_layout_total_rows", "ep_dispatch", "ep_combine",
@@ -916,3 +937,351 @@ def ll_experts_w4(x: torch.Tensor, weights: W4Weights, layout: LLLayout, *,
            "ep_ll_experts_w4")
     _debug_check("ll_experts_w4", err, x.device)
     return out
+
+
+# --------------------------------------------------------------------------
+# a whole layer for a few tokens
+# --------------------------------------------------------------------------
+def _same_device(first: torch.Tensor, *others: torch.Tensor | None) -> torch.device:
+    """The tensors' device, which has to be the current one: a kernel launched on another
+    device's stream would run where its buffers are not."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise EPError(f"tensors are on different devices ({dev} and {t.device})")
+    if dev.type == "cuda" and torch.cuda.current_device() != dev.index:
+        raise EPError(f"tensors are on {dev}, but the current device is "
+                      f"cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _w4_shape(w: W4Weights, name: str, experts: int) -> tuple[int, int, int]:
+    """Checks 4-bit weights; returns their rows, input channels and group size."""
+    _need(w.q, f"{name}.q", torch.uint8)
+    _need(w.scales, f"{name}.scales", torch.bfloat16)
+    if w.q.dim() != 3 or w.scales.dim() != 3 or w.q.shape[0] != experts:
+        raise EPError(f"{name}.q must be [{experts}, N, I / 2] and {name}.scales "
+                      f"[{experts}, N, I / group]")
+    rows, inner, groups = w.q.shape[1], 2 * w.q.shape[2], w.scales.shape[2]
+    if tuple(w.scales.shape[:2]) != (experts, rows) or groups == 0 or inner % groups:
+        raise EPError(f"{name}.scales must have one value per group of input channels")
+    if w.zeros is not None:
+        _need(w.zeros, f"{name}.zeros", torch.uint8, w.scales.shape)
+    return rows, inner, inner // groups
+
+
+def layer_w4(x: torch.Tensor, logits: torch.Tensor, gate_up: W4Weights, down: W4Weights,
+             num_topk: int, *, score: str = "softmax", bias: torch.Tensor | None = None,
+             num_groups: int = 1, topk_groups: int = 1, renormalize: bool = True,
+             scale: float = 1.0, out: torch.Tensor | None = None
+             ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """A whole mixture-of-experts layer for a few tokens (at most
+    EP_LAYER_MAX_TOKENS), in two launches: the choice of route(logits, ...), both
+    products of the chosen experts (gate_up [E, 2 N, H], down [E, H, N]) with SwiGLU
+    between them, and the weighted sum over the experts.  x [T, H] bfloat16;
+    returns (out [T, H] bfloat16, topk_idx [T, K] int64, topk_weights [T, K]
+    float32).  `out` may be x.  Enqueued on the current stream."""
+    _need(x, "x", torch.bfloat16)
+    stride = _need_logits(logits)
+    T, E = logits.shape
+    if x.dim() != 2 or x.shape[0] != T:
+        raise EPError(f"x must be [{T}, hidden], a row for each row of logits")
+    H, K = x.shape[1], int(num_topk)
+    if T > EP_LAYER_MAX_TOKENS or E > EP_LAYER_MAX_EXPERTS:
+        raise EPError(f"layer_w4 takes at most {EP_LAYER_MAX_TOKENS} tokens and "
+                      f"{EP_LAYER_MAX_EXPERTS} experts, got {T} and {E}")
+    rows, inner, group = _w4_shape(gate_up, "gate_up", E)
+    rows2, N, group2 = _w4_shape(down, "down", E)
+    if inner != H or rows2 != H or rows != 2 * N:
+        raise EPError(f"gate_up must be weights of [{E}, 2 N, {H}] and down of [{E}, {H}, N], got "
+                      f"{(E, rows, inner)} and {(E, rows2, N)}")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,))
+    dev = _same_device(x, logits, gate_up.q, gate_up.scales, gate_up.zeros, down.q, down.scales,
+                       down.zeros, bias, out)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, (T, H))
+    idx = torch.empty((T, K), dtype=torch.int64, device=dev)
+    w = torch.empty((T, K), dtype=torch.float32, device=dev)
+    n = lib().ep_layer_w4_workspace_bytes(T, N, K)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _check(lib().ep_layer_w4(
+        x.data_ptr(), H, N, T, logits.data_ptr(), int(logits.dtype == torch.bfloat16), stride,
+        _ptr(bias), E, K, _enum(SCORES, score, "score"), int(num_groups), int(topk_groups),
+        int(renormalize), float(scale), gate_up.q.data_ptr(), gate_up.scales.data_ptr(),
+        _ptr(gate_up.zeros), group, down.q.data_ptr(), down.scales.data_ptr(), _ptr(down.zeros),
+        group2, idx.data_ptr(), w.data_ptr(), out.data_ptr(), ws.data_ptr(), n, _stream(dev)),
+        "ep_layer_w4")
+    _debug_check("layer_w4", None, dev)
+    return out, idx, w
+
+
+# --------------------------------------------------------------------------
+# between two blocks: norms, gate, residual scale
+# --------------------------------------------------------------------------
+@dataclass
+class BlockNorm:
+    """Outputs of block_norm and ll_combine_norm."""
+    z: torch.Tensor | None         # [T, H] of the stream's type: the stream after the block
+    h: torch.Tensor | None         # [T, H] bfloat16: the next block's input
+    y: torch.Tensor | None = None  # [T, H] bfloat16: the combined rows (ll_combine_norm, save=True)
+
+
+@dataclass
+class BlockNormGrad:
+    """Outputs of block_norm_backward (None: nothing to differentiate)."""
+    dx: torch.Tensor                    # [T, H] of the stream's type
+    dy: torch.Tensor                    # [T, H] bfloat16
+    dgate: torch.Tensor | None          # the gate's shape; float32, or a [T, H] gate's own type
+    dpost_weight: torch.Tensor | None   # [H] float32
+    dpre_weight: torch.Tensor | None    # [H] float32
+
+
+_STREAMS = (torch.bfloat16, torch.float32)
+
+
+def _norm_arguments(x, gate, post_weight, pre_weight):
+    """Checks what both directions take; returns T, H, the gate's kind and whether
+    gate and weights are bfloat16."""
+    if x.dtype not in _STREAMS:
+        raise EPError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    _need(x, "x", x.dtype)
+    if x.dim() != 2:
+        raise EPError("x must be [num_tokens, hidden]")
+    T, H = x.shape
+    if H % 8 or not 8 <= H <= EP_NORM_MAX_HIDDEN:
+        raise EPError(f"hidden must be a multiple of 8 and at most {EP_NORM_MAX_HIDDEN}, got {H}")
+    kind, dtype = GATE_NONE, None
+    for name, v in (("post_weight", post_weight), ("pre_weight", pre_weight), ("gate", gate)):
+        if v is None:
+            continue
+        dtype = dtype or v.dtype
+        if dtype not in _STREAMS:
+            raise EPError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
+        _need(v, name, dtype, None if name == "gate" else (H,))
+    if gate is not None:
+        shape = tuple(gate.shape)
+        if shape == (H,):
+            kind = GATE_CHANNEL
+        elif shape == (T, 1):
+            kind = GATE_TOKEN
+        elif shape == (T, H):
+            kind = GATE_FULL
+        else:
+            raise EPError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}], got {list(shape)}")
+    return T, H, kind, int(dtype == torch.bfloat16)
+
+
+def _block_norm(x, y, rows, topk_weights, slot, gate, post_weight, pre_weight, scale, eps, save,
+                err, out):
+    T, H, kind, bf16 = _norm_arguments(x, gate, post_weight, pre_weight)
+    if err is not None:
+        _need(err, "err", torch.int32)
+    dev = _same_device(x, y, topk_weights, slot, gate, post_weight, pre_weight, err, out)
+    z = None
+    if y is not None:
+        z = torch.empty_like(x) if out is None else out
+        _need(z, "out", x.dtype, (T, H))
+    elif out is not None:
+        raise EPError("without y there is no new stream to write")
+    h = c = None
+    if pre_weight is not None:
+        h = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if save:
+        c = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    _check(lib().ep_block_norm(
+        x.data_ptr(), int(x.dtype == torch.float32), _ptr(y), rows, _ptr(topk_weights),
+        0 if slot is None else slot.shape[1], _ptr(slot), T, H, _ptr(gate), kind,
+        _ptr(post_weight), _ptr(pre_weight), bf16, float(scale), float(eps), _ptr(z), _ptr(h),
+        _ptr(c), _ptr(err), _stream(dev)), "ep_block_norm")
+    return BlockNorm(z, h, c)
+
+
+def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *,
+               gate: torch.Tensor | None = None, post_weight: torch.Tensor | None = None,
+               pre_weight: torch.Tensor | None = None, scale: float = 1.0, eps: float = 1e-6,
+               out: torch.Tensor | None = None) -> BlockNorm:
+    """Between two blocks: z = x + scale * gate * norm(y) and h = norm(z), in one
+    pass.  x [T, H] is the residual stream (bfloat16 or float32), y [T, H] bfloat16 the
+    block's output (None: only h = norm(x)); norm(y) is y / rms(y) *
+    post_weight, or y without a post_weight; h = z / rms(z) * pre_weight, None without a
+    pre_weight.  gate: [H], [T, 1] or [T, H]; gate and weights are all
+    float32 or all bfloat16.  `out` takes z and may be x.  Enqueued on the current stream."""
+    if y is None and (gate is not None or post_weight is not None):
+        raise EPError("gate and post_weight belong to a block's output y")
+    if y is None and pre_weight is None:
+        raise EPError("nothing to compute without y and without pre_weight")
+    if y is not None:
+        _need(y, "y", torch.bfloat16, x.shape)
+    r = _block_norm(x, y, x.shape[0], None, None, gate, post_weight, pre_weight, scale, eps, False,
+                    None, out)
+    _debug_check("block_norm", None, x.device)
+    return r
+
+
+def ll_combine_norm(y: torch.Tensor, topk_weights: torch.Tensor | None, layout: LLLayout,
+                    x: torch.Tensor, *, gate: torch.Tensor | None = None,
+                    post_weight: torch.Tensor | None = None,
+                    pre_weight: torch.Tensor | None = None, scale: float = 1.0, eps: float = 1e-6,
+                    save: bool = False, err: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None) -> BlockNorm:
+    """block_norm(x, ll_combine(y, topk_weights, layout), ...) in one pass over the
+    experts' rows y [E * cap, H].  save: the combined rows are returned too, as
+    block_norm_backward and ll_combine_backward need them.  Enqueued on the current stream."""
+    _need(y, "y", torch.bfloat16)
+    T, K = layout.ll_slot.shape
+    _need(layout.ll_slot, "ll_slot", torch.int32, (T, K))
+    if x.dim() != 2 or y.dim() != 2 or x.shape[0] != T or x.shape[1] != y.shape[1]:
+        raise EPError(f"x must be [{T}, hidden] and y [rows, hidden]")
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", torch.float32, (T, K))
+    r = _block_norm(x, y, y.shape[0], topk_weights, layout.ll_slot, gate, post_weight, pre_weight,
+                    scale, eps, save, err, out)
+    _debug_check("ll_combine_norm", err, y.device)
+    return r
+
+
+def block_norm_backward(dz: torch.Tensor | None, dh: torch.Tensor | None, z: torch.Tensor,
+                        y: torch.Tensor | None = None, *, gate: torch.Tensor | None = None,
+                        post_weight: torch.Tensor | None = None,
+                        pre_weight: torch.Tensor | None = None, scale: float = 1.0,
+                        eps: float = 1e-6) -> BlockNormGrad:
+    """Gradient of block_norm for the gradients dz of z (the stream's type) and dh
+    of h (bfloat16), at the stored z and y.  Either gradient may be None (zero); dh goes
+    with pre_weight, and y is needed with a post_weight or a gate.
+    Enqueued on the current stream."""
+    T, H, kind, bf16 = _norm_arguments(z, gate, post_weight, pre_weight)
+    if dz is None and dh is None:
+        raise EPError("one of dz and dh is needed")
+    if (dh is None) != (pre_weight is None):
+        raise EPError("dh is the gradient of the norm with pre_weight: both or neither")
+    if dz is not None:
+        _need(dz, "dz", z.dtype, (T, H))
+    if dh is not None:
+        _need(dh, "dh", torch.bfloat16, (T, H))
+    if y is not None:
+        _need(y, "y", torch.bfloat16, (T, H))
+    elif post_weight is not None or gate is not None:
+        raise EPError("the gradients of gate and post_weight need y")
+    dev = _same_device(z, dz, dh, y, gate, post_weight, pre_weight)
+    f32 = dict(dtype=torch.float32, device=dev)
+    dx = torch.empty((T, H), dtype=z.dtype, device=dev)
+    dy = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    dpost = None if post_weight is None else torch.empty(H, **f32)
+    dpre = None if pre_weight is None else torch.empty(H, **f32)
+    dgate = None
+    if gate is not None:
+        dgate = torch.empty_like(gate) if kind == GATE_FULL else torch.empty(gate.shape, **f32)
+    ws, n = None, 0
+    if dpost is not None or dpre is not None or kind == GATE_CHANNEL:
+        n = lib().ep_block_norm_backward_workspace_bytes(T, H)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _check(lib().ep_block_norm_backward(
+        _ptr(dz), _ptr(dh), z.data_ptr(), int(z.dtype == torch.float32), _ptr(y), T, H, _ptr(gate),
+        kind, _ptr(post_weight), _ptr(pre_weight), bf16, float(scale), float(eps), dx.data_ptr(),
+        dy.data_ptr(), _ptr(dgate), _ptr(dpost), _ptr(dpre), _ptr(ws), n, _stream(dev)),
+        "ep_block_norm_backward")
+    _debug_check("block_norm_backward", None, dev)
+    return BlockNormGrad(dx, dy, dgate, dpost, dpre)
+
+
+# --------------------------------------------------------------------------
+# the gated activation with an 8-bit checkpoint, and its gradient
+# --------------------------------------------------------------------------
+@dataclass
+class Checkpoint8:
+    """Rows kept in 8 bits for a backward pass: E4M3 codes and one scale per 128 channels."""
+    codes: torch.Tensor   # [rows, C] uint8
+    scales: torch.Tensor  # [rows, C / 128] float32
+
+
+def alloc_checkpoint8(rows: int, channels: int, device: torch.device) -> Checkpoint8:
+    """Room for a checkpoint of [rows, channels] (channels a multiple of 128)."""
+    if channels % 128:
+        raise EPError(f"channels must be a multiple of 128, got {channels}")
+    return Checkpoint8(torch.empty((rows, channels), dtype=torch.uint8, device=device),
+                       torch.empty((rows, channels // 128), dtype=torch.float32, device=device))
+
+
+def _need_checkpoint(c: Checkpoint8, rows: int, channels: int):
+    if channels % 256:
+        raise EPError(f"a checkpoint needs N to be a multiple of 128, got {channels // 2}")
+    _need(c.codes, "checkpoint.codes", torch.uint8, (rows, channels))
+    _need(c.scales, "checkpoint.scales", torch.float32, (rows, channels // 128))
+
+
+def ll_swiglu(gate_up: torch.Tensor, layout: LLLayout, topk_weights: torch.Tensor | None = None, *,
+              checkpoint: Checkpoint8 | None = None, err: torch.Tensor | None = None,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gated activation on the rows of the expert-major layout: h = w * silu(g) *
+    u for the rows [g | u] of gate_up [rows, 2 N] bfloat16 that the layout's slots
+    name, w the slot's top-k weight (1 without topk_weights; with them the
+    combine takes none).  checkpoint (alloc_checkpoint8(rows, 2 N)) receives
+    gate_up in 8 bits, for ll_swiglu_backward.  Rows that no slot names keep what `out`
+    and the checkpoint hold (nothing defined without `out`).  Enqueued on the current
+    stream."""
+    _need(gate_up, "gate_up", torch.bfloat16)
+    T, K = layout.ll_slot.shape
+    _need(layout.ll_slot, "ll_slot", torch.int32, (T, K))
+    if gate_up.dim() != 2 or gate_up.shape[1] % 16 or gate_up.shape[1] == 0:
+        raise EPError("gate_up must be [rows, 2 N] with N a multiple of 8")
+    rows, N = gate_up.shape[0], gate_up.shape[1] // 2
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", torch.float32, (T, K))
+    codes = scales = None
+    if checkpoint is not None:
+        _need_checkpoint(checkpoint, rows, 2 * N)
+        codes, scales = checkpoint.codes, checkpoint.scales
+    if err is not None:
+        _need(err, "err", torch.int32)
+    dev = _same_device(gate_up, layout.ll_slot, topk_weights, codes, scales, err, out)
+    if out is None:
+        out = torch.empty((rows, N), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, (rows, N))
+    _check(lib().ep_ll_swiglu(gate_up.data_ptr(), N, rows, _ptr(topk_weights), T, K,
+                              layout.ll_slot.data_ptr(), out.data_ptr(), _ptr(codes), _ptr(scales),
+                              _ptr(err), _stream(dev)), "ep_ll_swiglu")
+    _debug_check("ll_swiglu", err, dev)
+    return out
+
+
+def ll_swiglu_backward(dh: torch.Tensor, kept: Checkpoint8 | torch.Tensor, layout: LLLayout,
+                       topk_weights: torch.Tensor | None = None, *,
+                       err: torch.Tensor | None = None, out: torch.Tensor | None = None
+                       ) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Gradient of ll_swiglu for the gradient dh [rows, N] bfloat16 of its output:
+    (dgate_up [rows, 2 N] bfloat16, dweights [T, K] float32, or None without
+    topk_weights).  kept: the checkpoint, or gate_up itself.  Rows of dgate_up that
+    no slot names keep what `out` holds (zeros without `out`, at the cost of writing
+    all of it first).  Enqueued on the current stream."""
+    _need(dh, "dh", torch.bfloat16)
+    T, K = layout.ll_slot.shape
+    _need(layout.ll_slot, "ll_slot", torch.int32, (T, K))
+    if dh.dim() != 2 or dh.shape[1] % 8 or dh.shape[1] == 0:
+        raise EPError("dh must be [rows, N] with N a multiple of 8")
+    rows, N = dh.shape
+    gate_up = codes = scales = None
+    if isinstance(kept, Checkpoint8):
+        _need_checkpoint(kept, rows, 2 * N)
+        codes, scales = kept.codes, kept.scales
+    else:
+        gate_up = kept
+        _need(gate_up, "gate_up", torch.bfloat16, (rows, 2 * N))
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", torch.float32, (T, K))
+    if err is not None:
+        _need(err, "err", torch.int32)
+    dev = _same_device(dh, gate_up, codes, scales, layout.ll_slot, topk_weights, err, out)
+    if out is None:
+        out = torch.zeros((rows, 2 * N), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, (rows, 2 * N))
+    dw = None
+    if topk_weights is not None:
+        dw = torch.empty((T, K), dtype=torch.float32, device=dev)
+    _check(lib().ep_ll_swiglu_backward(dh.data_ptr(), _ptr(gate_up), _ptr(codes), _ptr(scales), N,
+                                       rows, _ptr(topk_weights), T, K, layout.ll_slot.data_ptr(),
+                                       out.data_ptr(), _ptr(dw), _ptr(err), _stream(dev)),
+           "ep_ll_swiglu_backward")
+    _debug_check("ll_swiglu_backward", err, dev)
+    return out, dw

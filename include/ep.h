@@ -712,6 +712,156 @@ ep_status_t ep_ll_experts_w4(const void* x, int x_fp8, const float* x_scales, in
  */
 void ep_debug_set_experts_stall(int step);
 
+/* ------------------------------------------------------------------------
+ * A whole mixture-of-experts layer for a few tokens, in two launches: what
+ * ep_route, ep_ll_get_dispatch_layout, ep_ll_dispatch, ep_ll_experts_w4 (twice)
+ * and ep_ll_combine compute one after the other.
+ *
+ *   e_k, w_k  the choice and the weights of ep_route for the logits' row
+ *   h_k[n]  = w_k * silu(G_{e_k} x)[n] * (U_{e_k} x)[n]
+ *   out     = bf16_rne( sum_k D_{e_k} h_k )
+ *
+ * G and U are rows [0, N) and [N, 2N) of the gate_up weights, D the down weights,
+ * held as in ep_ll_experts_w4; the two may differ in their group sizes and in
+ * having zero points.  A slot for which no expert is left contributes nothing;
+ * a token without any gives zeros.  Codes are multiplied as the integers they
+ * are and all sums are float32; h is kept in 16 bits of mantissa (two bf16), so only out is
+ * rounded noticeably.  Infinities and NaN stay in their token.
+ * In (device): x [T, H] bf16; logits, row_stride, bias, score, num_groups,
+ *   topk_groups, renormalize, scale: as ep_route; gate_up_q [E, 2N, H/2],
+ *   gate_up_scales [E, 2N, H/gate_up_group] bf16, gate_up_zeros of the same
+ *   shape (nullable); down_q [E, H, N/2], down_scales [E, H, N/down_group],
+ *   down_zeros (nullable).
+ * Limits: T <= EP_LAYER_MAX_TOKENS, E <= EP_LAYER_MAX_EXPERTS, H a multiple of
+ *   gate_up_group and N of down_group, H * N < 2^31; those of ep_route.
+ * Out (device): topk_idx [T, K] int64, topk_weights [T, K] float32, out [T, H]
+ *   bf16, every element written.  out may be x; nothing else may overlap.
+ * workspace (device): ep_layer_w4_workspace_bytes(T, N, K) bytes, no
+ *   initialisation needed (EP_ERR_CAPACITY if smaller).  Calls that can overlap on
+ *   the GPU need workspaces of their own.
+ * ------------------------------------------------------------------------ */
+#define EP_LAYER_MAX_TOKENS 16
+#define EP_LAYER_MAX_EXPERTS 1024
+
+/* Bytes of device scratch for ep_layer_w4 (0 for invalid sizes). */
+size_t ep_layer_w4_workspace_bytes(int64_t num_tokens, int inter, int num_topk);
+
+ep_status_t ep_layer_w4(const void* x, int hidden, int inter, int64_t num_tokens,
+                        const void* logits, int logits_bf16, int64_t row_stride, const float* bias,
+                        int num_experts, int num_topk, int score, int num_groups, int topk_groups,
+                        int renormalize, float scale, const uint8_t* gate_up_q,
+                        const void* gate_up_scales, const uint8_t* gate_up_zeros,
+                        int gate_up_group, const uint8_t* down_q, const void* down_scales,
+                        const uint8_t* down_zeros, int down_group, int64_t* topk_idx,
+                        float* topk_weights, void* out, void* workspace, size_t workspace_bytes,
+                        ep_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * What stands between two blocks: the norm after a block, its gate and
+ * residual scale, the addition to the residual stream, and the norm before
+ * the next block, in one pass.  For every token, with rms(v) = sqrt(mean(v^2) +
+ * eps) over the H channels:
+ *   n = y / rms(y) * post_weight       (y without a post_weight)
+ *   z = x + scale * gate * n           (gate 1 for EP_GATE_NONE)
+ *   h = z / rms(z) * pre_weight
+ * y is the block's output per token (ll_slot NULL), or the rows of the
+ * expert-major layout, which are combined first, as by ep_ll_combine but without
+ * its rounding: y[t] = sum over slots k with ll_slot[t][k] >= 0 of w[t][k] * rows[ll_slot[t][k]].
+ * h is made from z before its rounding.  All arithmetic is float32, and every
+ * output is rounded once.  (Squares of magnitudes beyond 2^63 overflow.)
+ * In (device): x [T, H] bf16, or (stream_f32 != 0) float32; y [T, H] or
+ *   [num_rows, H] bf16 (NULL without ll_slot: no block's output, h = x / rms(x) *
+ *   pre_weight); ll_slot [T, K] int32 and topk_weights [T, K] float32 (nullable: 1
+ *   each) with num_rows, num_topk; gate by gate_kind: [H] (EP_GATE_CHANNEL), [T]
+ *   (EP_GATE_TOKEN) or [T, H] (EP_GATE_FULL); post_weight, pre_weight [H] (nullable).
+ *   gate and the weights are float32, or (weights_bf16 != 0) bfloat16.  eps > 0.
+ * Out (device), every element written: z [T, H] of x's type (NULL if and only if there
+ *   is no y), h [T, H] bf16 (NULL if and only if pre_weight is), combined [T, H] bf16
+ *   (nullable; the combined rows, for the gradient).  z may be x; nothing else may overlap.
+ * H % 8 == 0, H <= EP_NORM_MAX_HIDDEN.
+ * err_word (nullable): EP_ERRBIT_CAPACITY for a slot >= num_rows (left out).
+ * ------------------------------------------------------------------------ */
+#define EP_NORM_MAX_HIDDEN 16384
+typedef enum {
+  EP_GATE_NONE = 0,
+  EP_GATE_CHANNEL = 1,
+  EP_GATE_TOKEN = 2,
+  EP_GATE_FULL = 3
+} ep_gate_t;
+
+ep_status_t ep_block_norm(const void* x, int stream_f32, const void* y, int64_t num_rows,
+                          const float* topk_weights, int num_topk, const int32_t* ll_slot,
+                          int64_t num_tokens, int hidden, const void* gate, int gate_kind,
+                          const void* post_weight, const void* pre_weight, int weights_bf16,
+                          float scale, float eps, void* z, void* h, void* combined,
+                          int32_t* err_word, ep_stream_t stream);
+
+/*
+ * The gradient of ep_block_norm, from those of z (dz, of the stream's type) and of h
+ * (dh, bf16), at the stored z and y (with rows: the combined y; the gradient of the
+ * combine itself is ep_ll_combine_backward).  With d = dh * pre_weight, r_z =
+ * 1 / rms(z), r_y = 1 / rms(y):
+ *   dx    = dz + r_z d - r_z^3 mean(z d) z
+ *   dn    = scale * gate * dx
+ *   dy    = r_y dn post_weight - r_y^3 mean(y dn post_weight) y   (dn without a post_weight)
+ *   dpre  = sum_t dh z r_z,  dpost = sum_t dn y r_y
+ *   dgate = scale * n * dx, summed over what the gate is shared by
+ * Either of dz and dh may be NULL (zero; dh is NULL if and only if pre_weight is);
+ * z may be NULL without dh, y without post_weight and gate.
+ * Out (device): dx [T, H] of the stream's type; dy [T, H] bf16, dpost_weight and
+ *   dpre_weight [H] float32 (each nullable); dgate (nullable): [H] or [T]
+ *   float32, or [T, H] of the gate's type.  Sums over tokens are added in an order that the
+ *   sizes and the GPU fix, so results repeat.  No output may overlap anything.
+ * workspace (device): ep_block_norm_backward_workspace_bytes(T, H) bytes
+ *   (EP_ERR_CAPACITY if smaller) where dpre_weight, dpost_weight or a channel's dgate
+ *   is asked for, else unused.
+ */
+size_t ep_block_norm_backward_workspace_bytes(int64_t num_tokens, int hidden);
+
+ep_status_t ep_block_norm_backward(const void* dz, const void* dh, const void* z, int stream_f32,
+                                   const void* y, int64_t num_tokens, int hidden, const void* gate,
+                                   int gate_kind, const void* post_weight, const void* pre_weight,
+                                   int weights_bf16, float scale, float eps, void* dx, void* dy,
+                                   void* dgate, float* dpost_weight, float* dpre_weight,
+                                   void* workspace, size_t workspace_bytes, ep_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' gated activation on the rows of the expert-major layout, for
+ * training: unlike ep_ll_experts_w4's it keeps what its gradient needs, in 8 bits.
+ * For every slot (t, k) with row = ll_slot[t][k] >= 0, [g | u] = gate_up[row]:
+ *   h[row]      = bf16_rne( w[t][k] * g / (1 + exp(-g)) * u )    (w NULL: 1 each)
+ *   codes[row], scales[row] = g and u as E4M3 with one scale per 128 channels,
+ *                 rounded as ep_dispatch rounds its rows (use_fp8); a block of 128
+ *                 that holds an infinity or a NaN reads back as NaN throughout
+ * With the weights here, the combine takes none (topk_weights NULL), and the
+ * gradient of the weights comes from these rows instead of the experts' outputs.
+ * In (device): gate_up [num_rows, 2N] bf16; topk_weights [T, K] float32
+ *   (nullable); ll_slot [T, K] int32, in which no row is named twice.
+ * Out (device): h [num_rows, N] bf16; codes [num_rows, 2N] and scales [num_rows, 2N/128]
+ *   float32 (both or neither).  Rows that no slot names are not touched.
+ * N % 8 == 0, with codes N % 128 == 0.  Nothing may overlap.
+ * err_word (nullable): EP_ERRBIT_CAPACITY for a slot >= num_rows (skipped).
+ * ------------------------------------------------------------------------ */
+ep_status_t ep_ll_swiglu(const void* gate_up, int inter, int64_t num_rows,
+                         const float* topk_weights, int64_t num_tokens, int num_topk,
+                         const int32_t* ll_slot, void* h, uint8_t* codes, float* scales,
+                         int32_t* err_word, ep_stream_t stream);
+
+/*
+ * Its gradient, from the checkpoint (codes, scales; gate_up NULL) or from gate_up
+ * itself (codes and scales NULL).  With s = 1 / (1 + exp(-g)):
+ *   dgate_up[row] = [ w dh u s (1 + g (1 - s)) | w dh g s ]     (bf16, rounded once)
+ *   dweights[t][k] = sum_n dh g s u     (float32; 0 for a slot without a row)
+ * In (device): dh [num_rows, N] bf16; the rest as ep_ll_swiglu.
+ * Out (device): dgate_up [num_rows, 2N] bf16: rows that no slot names are not
+ *   touched; dweights [T, K] float32 (nullable), every element written.
+ */
+ep_status_t ep_ll_swiglu_backward(const void* dh, const void* gate_up, const uint8_t* codes,
+                                  const float* scales, int inter, int64_t num_rows,
+                                  const float* topk_weights, int64_t num_tokens, int num_topk,
+                                  const int32_t* ll_slot, void* dgate_up, float* dweights,
+                                  int32_t* err_word, ep_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
