@@ -5,89 +5,135 @@
 namespace ep {
 namespace {
 
-// The tokens' choices, by all blocks alike, and the lists made of them.
-__device__ void route_all(const LayerArgs& a, uint8_t* scratch, int64_t* idx, float* w, Lists& l) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int K = a.route.K, slots = a.T * K;
-  __shared__ uint32_t words[kMaxExperts / 32];
-  if (tid < kMaxExperts / 32) words[tid] = 0;
-  for (int i = tid; i < (int)(sizeof(l.slot) / 16); i += kThreads)
-    reinterpret_cast<int4*>(l.slot)[i] = make_int4(0, 0, 0, 0);
-  for (int i = tid; i < kMaxSlots; i += kThreads) l.mask[i] = 0;
-  if (warp < a.T) {
-    uint32_t* key = reinterpret_cast<uint32_t*>(scratch) +
-                    warp * (a.route.E + kMaxGroups + 2 * EP_MAX_TOPK);
-    float* gscore = reinterpret_cast<float*>(key + a.route.E);
-    int* slot = reinterpret_cast<int*>(gscore + kMaxGroups);
-    float* score = reinterpret_cast<float*>(slot + EP_MAX_TOPK);
-    RouteArgs r = a.route;
-    r.idx = idx;
-    r.w = w;
-    float m, z;
-    if (a.logits_bf16) {
-      if (a.group_lanes)
-        choose_in_registers<32, 8, true>(r, warp, lane, a.group_lanes, a.vec, slot, m, z);
-      else
-        choose_in_shared<true>(r, warp, lane, key, gscore, slot, m, z);
-      __syncwarp();
-      write_slots<32, true>(r, warp, true, lane, slot, score, m, z);
-    } else {
-      if (a.group_lanes)
-        choose_in_registers<32, 8, false>(r, warp, lane, a.group_lanes, a.vec, slot, m, z);
-      else
-        choose_in_shared<false>(r, warp, lane, key, gscore, slot, m, z);
-      __syncwarp();
-      write_slots<32, false>(r, warp, true, lane, slot, score, m, z);
-    }
+// What the lists are made of, in shared memory: the experts that some token
+// chose, in order, and who chose them.
+struct Chosen {
+  uint32_t words[kMaxExperts / 32];       // a bit for each expert
+  int mask[kMaxSlots];                    // a bit for each token
+  uint16_t expert[kMaxSlots];
+  uint8_t slot[kMaxSlots][kMaxTokens];    // the token's slot + 1, 0: not chosen
+  int sums[kWarps];
+};
+
+// The tokens' choices, a warp each; every block computes them alike.
+__device__ void route_all(const LayerArgs& a, uint8_t* scratch, int64_t* idx, float* w) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp >= a.T) return;
+  uint32_t* key = reinterpret_cast<uint32_t*>(scratch) +
+                  warp * (a.route.E + kMaxGroups + 2 * EP_MAX_TOPK);
+  float* gscore = reinterpret_cast<float*>(key + a.route.E);
+  int* slot = reinterpret_cast<int*>(gscore + kMaxGroups);
+  float* score = reinterpret_cast<float*>(slot + EP_MAX_TOPK);
+  RouteArgs r = a.route;
+  r.idx = idx;
+  r.w = w;
+  float m, z;
+  if (a.logits_bf16) {
+    if (a.group_lanes)
+      choose_in_registers<32, 8, true>(r, warp, lane, a.group_lanes, a.vec, slot, m, z);
+    else
+      choose_in_shared<true>(r, warp, lane, key, gscore, slot, m, z);
+    __syncwarp();
+    write_slots<32, true>(r, warp, true, lane, slot, score, m, z);
+  } else {
+    if (a.group_lanes)
+      choose_in_registers<32, 8, false>(r, warp, lane, a.group_lanes, a.vec, slot, m, z);
+    else
+      choose_in_shared<false>(r, warp, lane, key, gscore, slot, m, z);
+    __syncwarp();
+    write_slots<32, false>(r, warp, true, lane, slot, score, m, z);
+  }
+}
+
+// Which experts the slots name, and for each the tokens; returns their number.
+__device__ int gather_chosen(const LayerArgs& a, const int64_t* idx, Chosen& c) {
+  const int tid = threadIdx.x, K = a.route.K, slots = a.T * K;
+  if (tid < kMaxExperts / 32) c.words[tid] = 0;
+  for (int i = tid; i < slots; i += kThreads) {
+    c.mask[i] = 0;
+    *reinterpret_cast<int4*>(c.slot[i]) = make_int4(0, 0, 0, 0);
   }
   __syncthreads();
   for (int i = tid; i < slots; i += kThreads)
-    if (idx[i] >= 0) atomicOr(&words[idx[i] >> 5], 1u << (idx[i] & 31));
+    if (idx[i] >= 0) atomicOr(&c.words[idx[i] >> 5], 1u << (idx[i] & 31));
   __syncthreads();
+  int total = 0;
+  for (int j = 0; j < (a.route.E + 31) / 32; ++j) total += __popc(c.words[j]);
   for (int i = tid; i < slots; i += kThreads) {
     if (idx[i] < 0) continue;
     const int e = (int)idx[i], t = i / K;
-    int at = __popc(words[e >> 5] & ((1u << (e & 31)) - 1u));
-    for (int j = 0; j < (e >> 5); ++j) at += __popc(words[j]);
-    l.expert[at] = (uint16_t)e;  // by every slot that names it, alike
-    l.slot[at * kMaxTokens + t] = (uint8_t)(i - t * K + 1);
-    atomicOr(&l.mask[at], 1 << t);
+    int at = __popc(c.words[e >> 5] & ((1u << (e & 31)) - 1u));
+    for (int j = 0; j < (e >> 5); ++j) at += __popc(c.words[j]);
+    c.expert[at] = (uint16_t)e;  // by every slot that names it, alike
+    c.slot[at][t] = (uint8_t)(i - t * K + 1);
+    atomicOr(&c.mask[at], 1 << t);
   }
-  if (tid == 0) {
-    int n = 0;
-    for (int j = 0; j < kMaxExperts / 32; ++j) n += __popc(words[j]);
-    l.count = n;
+  __syncthreads();
+  return total;
+}
+
+// The entries of `total` experts, each of at most `most` tokens.
+__device__ void make_lists(const LayerArgs& a, Chosen& c, int total, int most, Lists& l) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  static_assert(kMaxSlots <= kThreads, "a thread for every chosen expert");
+  const int mask = tid < total ? c.mask[tid] : 0;
+  const int own = (__popc(mask) + most - 1) / most;
+  int at = own;  // sums up to and with this thread
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, at, o);
+    if (lane >= o) at += v;
+  }
+  if (lane == 31) c.sums[warp] = at;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) at += c.sums[i];
+  if (tid == kThreads - 1) l.count = at;
+  int k = (at - own) * most;  // entry and column of the next token
+  for (int rest = mask; rest; rest &= rest - 1, ++k) {
+    const int t = __ffs(rest) - 1;
+    Entry& e = l.entry[k / most];
+    e.expert = c.expert[tid];
+    e.n = min(__popc(rest) + k % most, most);
+    e.tok[k % most] = (uint8_t)t;
+    e.row[k % most] = (uint16_t)(t * a.route.K + c.slot[tid][t] - 1);
   }
   __syncthreads();
 }
 
-template <int NT, int kGroup, bool kZeros>
+template <int kGroup, bool kZeros>
 __global__ void __launch_bounds__(kThreads, 1) layer_up_kernel(LayerArgs a) {
-  using S = Shared<false, NT>;
+  using S = Sizes<false, kGroup, kZeros>;
   pdl_wait_then_release();
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int64_t idx[kMaxSlots];
   __shared__ float weight[kMaxSlots];
+  // before the products the ring is free
+  static_assert(kWarps * (kMaxExperts + kMaxGroups + 2 * EP_MAX_TOPK) * 4 <= S::kRing &&
+                    sizeof(Chosen) <= S::kRing,
+                "the choice fits into the ring");
+  Chosen& c = *reinterpret_cast<Chosen*>(smem);
   Lists& l = *reinterpret_cast<Lists*>(smem + S::kBytes - sizeof(Lists));
-  route_all(a, smem, idx, weight, l);
-  if (blockIdx.x == 0) {
+  route_all(a, smem, idx, weight);
+  __syncthreads();
+  const int total = gather_chosen(a, idx, c);
+  if (blockIdx.x == gridDim.x - 1) {  // the block with the fewest tiles
+    make_lists(a, c, total, Sizes<true, 128, false>::kColumns, l);
     for (int i = threadIdx.x; i < a.T * a.route.K; i += kThreads) {
       a.route.idx[i] = idx[i];
       a.route.w[i] = weight[i];
     }
-    for (int i = threadIdx.x; i < (int)(sizeof(Lists) / 16); i += kThreads)
+    for (int i = threadIdx.x; i < 1 + l.count * (int)(sizeof(Entry) / 16); i += kThreads)
       reinterpret_cast<int4*>(a.lists)[i] = reinterpret_cast<const int4*>(&l)[i];
+    __syncthreads();
   }
-  products<false, NT, kGroup, kZeros>(a, l, weight, smem);
+  make_lists(a, c, total, S::kColumns, l);
+  products<false, kGroup, kZeros>(a, l, weight, smem);
 }
 
 }  // namespace
 
 bool launch_layer_up(const LayerArgs& a, int group, int blocks, cudaStream_t st) {
-  if (a.T <= 8) {
-    EP_LAYER_GROUPS(layer_up_kernel, false, 1, a.up)
-  }
-  EP_LAYER_GROUPS(layer_up_kernel, false, 2, a.up)
+  EP_LAYER_INSTANCES(layer_up_kernel, false, a.up)
 }
 
 namespace {

@@ -46,15 +46,19 @@ constexpr int kMaxTokens = 16;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxSlots = kMaxTokens * EP_MAX_TOPK;
 
-// The experts that some token chose, in order, and who chose them.
+// A chosen expert with the tokens that chose it, or some of them where they are
+// more than the matrix instruction has columns for.
+struct Entry {
+  int expert;
+  int n;            // tokens
+  uint8_t tok[8];
+  uint16_t row[8];  // of h: token * K + slot
+};
 struct Lists {
   int count;
   int pad[3];
-  int mask[kMaxSlots];                      // a bit for each token
-  uint16_t expert[kMaxSlots];
-  uint8_t slot[kMaxSlots * kMaxTokens];     // the token's slot + 1, 0: not chosen
+  Entry entry[kMaxSlots];
 };
-static_assert(sizeof(Lists) % 16 == 0, "copied in vectors");
 
 struct Weights {
   const uint8_t* q;
@@ -72,22 +76,30 @@ struct LayerArgs {
   const uint8_t* x;
   int T, H, N;
   Weights up, down;
-  __nv_bfloat16 *hi, *lo;  // [T * K, N]
-  Lists* lists;
+  __nv_bfloat16 *hi, *lo;  // [T * K, N], every 8 channels in the order of the operand
+  Lists* lists;            // of the down projection
   __nv_bfloat16* out;
 };
 
-// Shared memory of a launch: the warps' stages, then the parts of tiles that
-// lie in several warps' runs, then the lists.
-template <bool kDown, int NT>
-struct Shared {
-  static constexpr int kMT = kDown ? 1 : 2;  // tiles of 16 weight rows
-  static constexpr int kRows = 16 * kMT;
-  static constexpr int kStages = kDown ? 6 : 4;
-  static constexpr int kCodes = kRows * 64;                // of a step
-  static constexpr int kStage = kCodes + kRows * (8 + 4);  // and scales and zero points
-  static constexpr int kParts = kMT * NT * 512;            // of a warp
-  static constexpr int kBytes = kWarps * (kStages * kStage + kParts) + (int)sizeof(Lists);
+// Sizes of a launch.  A step is 4096 codes: 128 channels of 32 rows (16 of the
+// gate, 16 of the up projection), or 256 channels of 16 rows.
+template <bool kDown, int kGroup, bool kZeros>
+struct Sizes {
+  static constexpr int kRows = kDown ? 16 : 32;
+  static constexpr int kChannels = kDown ? 256 : 128;
+  static constexpr int kColumns = kDown ? 4 : 8;           // tokens of an entry
+  static constexpr int kPer = 128 / kGroup;                // groups of 128 channels
+  static constexpr int kGroups = kChannels / kGroup;       // of a step
+  static constexpr int kScaleRow = kGroups < 2 ? 4 : 2 * kGroups;  // bytes: whole words
+  static constexpr int kZeroRow = kGroups < 4 ? 4 : kGroups;
+  static constexpr int kCodes = 2048;
+  static constexpr int kStage = kCodes + kRows * (kScaleRow + (kZeros ? kZeroRow : 0));
+  static constexpr int kStages = 4;
+  // a warp's part of a tile whose first step is another warp's; of the down
+  // projection also its current tile, both [token][channel]
+  static constexpr int kParts = kDown ? 2 * 1024 : 1024;
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kBytes = kRing + kWarps * kParts + (int)sizeof(Lists);
 };
 
 // Codes i and i + 4 (i = 0..3) of the 8 in w less their zero point, over 64:
@@ -116,329 +128,350 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 }
 template <int kBytes>
 __device__ __forceinline__ void copy_few(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)
-               : "memory");
+  if constexpr (kBytes == 16)
+    copy16(dst, src);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)
+                 : "memory");
 }
 
-// First channel, within a step, of word j of thread t of a quad.
+// First of the 8 channels of word j of thread t of a quad, within 128 channels.
 template <int kGroup>
 __device__ __forceinline__ int channel_of(int t, int j) {
   return kGroup == 128 ? t * 32 + j * 8 : word_channel<kGroup>(t, j);
 }
 
-// A warp's place in its run: tile `j` of the block, chosen expert `e`, step `s`.
-struct Cursor {
-  int j, e, s, n0;  // n0: the tile's first channel
-};
-
 // The products of one launch.
-template <bool kDown, int NT, int kGroup, bool kZeros>
+template <bool kDown, int kGroup, bool kZeros>
 __device__ __forceinline__ void products(const LayerArgs& a, const Lists& l, const float* weight,
                                          uint8_t* smem) {
-  using S = Shared<kDown, NT>;
-  constexpr int kMT = S::kMT, kStages = S::kStages, kPer = 128 / kGroup;
+  using S = Sizes<kDown, kGroup, kZeros>;
+  constexpr int kStages = S::kStages, kPer = S::kPer, kRowBytes = S::kChannels / 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const Weights& W = kDown ? a.down : a.up;
-  const int in = 2 * W.pitch, channels = kDown ? a.H : a.N, K = a.route.K;
-  // channels come in whole groups of at least 32, so tiles are whole
-  const int steps = (in + 127) / 128, tiles = channels / 16, count = l.count;
+  // channels come in whole groups of at least 32, so tiles of 16 are whole
+  const int in = 2 * W.pitch, channels = kDown ? a.H : a.N, tiles = channels / 16;
+  const int steps = (in + S::kChannels - 1) / S::kChannels, count = l.count;
   const int items = kDown ? tiles : tiles * count;
   const int item_steps = kDown ? steps * count : steps;
   const int mine = items > (int)blockIdx.x ? (items - (int)blockIdx.x - 1) / (int)gridDim.x + 1 : 0;
   const auto start = [&](int w) { return (int)((int64_t)mine * item_steps * w / kWarps); };
   const int p0 = start(warp), p1 = start(warp + 1);
-  const bool aligned = W.groups % 4 == 0;  // scales and zero points can be copied in words
+  // Scales and zero points of a step can be copied in words; the row is then
+  // a whole number of steps.  Else lanes load them one by one.
+  const bool words = W.groups % (S::kGroups < 4 ? 4 : S::kGroups) == 0;
+  const bool ragged = in % S::kChannels != 0;
 
   const uint32_t ring = smem_addr(smem) + warp * kStages * S::kStage;
-  float4* parts = reinterpret_cast<float4*>(smem + kWarps * kStages * S::kStage);
+  float* parts = reinterpret_cast<float*>(smem + S::kRing);
 
-  const auto enter = [&](Cursor& c) {
+  // --- copies: this lane's 16 bytes of each of four rows of a step ---
+  constexpr int kLanesRow = kRowBytes / 16;  // lanes a row
+  const int lrow = lane / kLanesRow, lcol = lane % kLanesRow * 16;
+  const uint8_t* codes = nullptr;
+  const uint16_t* scales = nullptr;
+  const uint8_t* zeros = nullptr;
+  uint32_t row_at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    row_at[i] = (uint32_t)(kDown ? 4 * i : 8 * (i & 1) + (i >> 1) * channels) * (uint32_t)W.pitch;
+  const auto swizzle = [](int r) {  // of the 16-byte pieces of row r: no bank twice
+    return kDown ? (r & 1) << 2 | (r & 2) | (r >> 2 & 1) : chunk_swizzle(r);
+  };
+  const auto write_at = [&](int i) {
+    const int r = kDown ? 4 * i + lrow : 8 * i + lrow;
+    return (uint32_t)(r * kRowBytes + ((lcol >> 4 ^ swizzle(r & 7)) << 4));
+  };
+
+  struct Cursor {
+    int j, e, s;  // tile of the block, entry, step
+  };
+  const auto tile_of = [&](Cursor& c) {  // the tile's first channel; up: sets its entry
     const int id = (int)blockIdx.x + c.j * (int)gridDim.x;
-    if (kDown) {
-      c.n0 = id * 16;
-    } else {
-      c.e = id / tiles;
-      c.n0 = (id - c.e * tiles) * 16;
-    }
+    if (kDown) return id * 16;
+    c.e = id / tiles;
+    return (id - c.e * tiles) * 16;
   };
-  const auto advance = [&](Cursor& c) {
-    if (++c.s < steps) return;
-    c.s = 0;
-    if (kDown) {
-      if (++c.e < count) return;
-      c.e = 0;
-    }
-    ++c.j;
-    enter(c);
-  };
-  Cursor load = {}, use;
+  Cursor load = {0, 0, 0};
   if (p0 < p1) {
     load.j = p0 / item_steps;
     const int rest = p0 - load.j * item_steps;
-    enter(load);
     if (kDown) load.e = rest / steps;
     load.s = kDown ? rest - load.e * steps : rest;
   }
-  use = load;
-  int to_load = p1 - p0;
+  Cursor use = load;
+  int to_load = p1 - p0, load_n0 = tile_of(load);
+  const auto point = [&]() {  // the pointers for `load`
+    const int64_t row0 = (int64_t)l.entry[load.e].expert * W.rows + load_n0;
+    codes = W.q + (row0 + lrow) * W.pitch + load.s * kRowBytes + lcol;
+    const int r = kDown ? lane & 15 : (lane & 15) + (lane >> 4) * channels;
+    scales = W.scales + (row0 + r) * W.groups;
+    if (kZeros) zeros = W.zeros + (row0 + r) * W.groups;
+  };
+  if (to_load > 0) point();
 
-  const auto issue = [&](int slot) {
+  const auto issue = [&](uint32_t stage) {
     if (to_load > 0) {
       --to_load;
-      const uint32_t stage = ring + slot * S::kStage;
-      const int64_t row0 = (int64_t)l.expert[load.e] * W.rows + load.n0;
       // beyond a row's last channel: any of its bytes, they meet zeros
-      const int col = load.s * 64 + t * 16;
-      const uint8_t* base = W.q + row0 * W.pitch + (col < W.pitch ? col : 0);
-      const uint32_t chunk = stage + g * 64 + ((t ^ chunk_swizzle(g)) << 4);
+      const uint8_t* p = codes;
+      if (ragged && load.s * kRowBytes + lcol >= W.pitch) p -= load.s * kRowBytes + lcol;
 #pragma unroll
-      for (int i = 0; i < 2 * kMT; ++i) {
-        const int r = g + 8 * (i & 1) + (i >> 1) * channels;
-        copy16(chunk + i * 512, base + (uint32_t)r * (uint32_t)W.pitch);
-      }
-      // scales (8 bytes a row) and zero points (4): of the step's groups, from the
-      // last multiple of 2 and of 4 on
-      const int half = lane >> 4, r = lane & 15;
-      const int sg = kGroup == 128 ? load.s & ~1 : load.s * kPer, zg = load.s * kPer & ~3;
-      if (!kDown || half == 0) {
-        const uint16_t* p = W.scales + (row0 + r + half * channels) * W.groups;
-        const uint32_t dst = stage + S::kCodes + lane * 8;
-        if (aligned) {
-          copy_few<kGroup == 32 ? 8 : 4>(dst, p + sg);
+      for (int i = 0; i < 4; ++i) copy16(stage + write_at(i), p + row_at[i]);
+      codes += kRowBytes;
+      // of the step's groups; with fewer than a word's, of the whole word
+      const int sg = S::kGroups < 2 ? load.s & ~1 : load.s * S::kGroups;
+      const int zg = load.s * S::kGroups & ~(S::kZeroRow - 1);
+      if (!kDown || lane < 16) {
+        const uint32_t dst = stage + S::kCodes + lane * S::kScaleRow;
+        if (words) {
+          copy_few<S::kScaleRow>(dst, scales + sg);
         } else {
-          uint32_t v[2] = {};
 #pragma unroll
-          for (int k = 0; k < (kGroup == 32 ? 4 : 2); ++k)
-            v[k >> 1] |= (uint32_t)__ldg(p + min(sg + k, W.groups - 1)) << (16 * (k & 1));
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(v[0]), "r"(v[1])
-                       : "memory");
+          for (int k = 0; k < S::kScaleRow / 2; ++k)
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 2 * k),
+                         "h"(__ldg(scales + min(sg + k, W.groups - 1)))
+                         : "memory");
         }
       }
-      if (kZeros && (!kDown || half == 1)) {
-        const uint8_t* p = W.zeros + (row0 + r + (kDown ? 0 : half * channels)) * W.groups;
-        const uint32_t dst = stage + S::kCodes + S::kRows * 8 + (kDown ? lane & 15 : lane) * 4;
-        if (aligned) {
-          copy_few<4>(dst, p + zg);
+      if (kZeros && (!kDown || lane >= 16)) {
+        const uint32_t dst = stage + S::kCodes + S::kRows * S::kScaleRow +
+                             (kDown ? lane & 15 : lane) * S::kZeroRow;
+        if (words) {
+          copy_few<S::kZeroRow>(dst, zeros + zg);
         } else {
-          uint32_t v = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            v |= (uint32_t)__ldg(p + min(zg + k, W.groups - 1)) << (8 * k);
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+          for (int k = 0; k < S::kZeroRow; ++k)
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst + k),
+                         "r"((uint32_t)__ldg(zeros + min(zg + k, W.groups - 1)))
+                         : "memory");
         }
       }
-      advance(load);
+      if (++load.s == steps) {
+        load.s = 0;
+        if (!kDown || ++load.e == count) {
+          load.e = 0;
+          ++load.j;
+          load_n0 = tile_of(load);
+        }
+        if (to_load > 0) point();
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(ring + i * S::kStage);
 
-  float acc[kMT][NT][4];
-  const auto clear = [&]() {
+  // --- products ---
+  constexpr int kM = kDown ? 1 : 2;  // tiles of sums: gate and up projection
+  float acc[kM][4] = {};
+  // every step has two tiles of operand A: rows (up) or halves of the channels (down)
+  const auto step = [&](const uint8_t* xp, int s, uint32_t stage) {
+    uint4 xv[kDown ? 2 : 1][4];
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt)
+    for (int h = 0; h < (kDown ? 2 : 1); ++h)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.0f;
-  };
-  // The tile's results; operands are 1/64 of the weights.
-  const auto finish = [&](const Cursor& c) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ch = c.n0 + g + 8 * (i >> 1);
-        if (kDown) {
-          float v = acc[0][nt][i];
-          v += __shfl_xor_sync(kFull, v, 2);  // what the rounding of h left
-          const int tok = nt * 4 + 2 * t + (i & 1);
-          if (t < 2 && tok < a.T)
-            a.out[(int64_t)tok * a.H + ch] = __float2bfloat16_rn(64.0f * v);
-        } else {
-          const int tok = nt * 8 + 2 * t + (i & 1);
-          const int k = tok < a.T ? l.slot[c.e * kMaxTokens + tok] : 0;
-          if (k) {
-            const int row = tok * K + k - 1;
-            const float v = weight[row] * silu_times(64.0f * acc[0][nt][i],
-                                                     64.0f * acc[kMT - 1][nt][i]);
-            const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-            const float rest = v - __bfloat162float(hi);
-            a.hi[(int64_t)row * a.N + ch] = hi;
-            // an infinite h leaves nothing
-            a.lo[(int64_t)row * a.N + ch] =
-                __float2bfloat16_rn(fabsf(v) < INFINITY && fabsf(rest) < INFINITY ? rest : 0.0f);
-          }
-        }
-      }
-  };
-
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
-  clear();
-  bool head = p0 < p1 && (use.s != 0 || (kDown && use.e != 0));
-  int slot = 0, expert = -1;
-  int mask = 0;
-  const uint8_t* xp[NT];
-
-  for (int p = p0; p < p1; ++p) {
-    if (use.e != expert || use.s == 0) {
-      expert = use.e;
-      mask = l.mask[expert];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int tok = kDown ? nt * 4 + (g & 3) : nt * 8 + g;
-        const bool in_it = mask >> tok & 1;
-        if (kDown) {
-          const __nv_bfloat16* base = g < 4 ? a.hi : a.lo;
-          const int row = tok * K + l.slot[expert * kMaxTokens + tok] - 1;
-          xp[nt] = in_it ? reinterpret_cast<const uint8_t*>(base + (int64_t)row * a.N) : nullptr;
-        } else {
-          xp[nt] = in_it ? a.x + (int64_t)tok * a.H * 2 : nullptr;
-        }
-      }
-    }
-    const auto column = [&](int nt, int j) {
-      const int ch = use.s * 128 + channel_of<kGroup>(t, j);
-      return xp[nt] && ch < in ? __ldg(reinterpret_cast<const uint4*>(xp[nt] + 2 * ch))
-                               : make_uint4(0, 0, 0, 0);
-    };
-    const auto busy = [&](int nt) {
-      return NT == 1 || (mask >> (kDown ? nt * 4 : nt * 8) & (kDown ? 15 : 255));
-    };
-    constexpr int kAhead = NT > 2 ? 2 : 4;  // words of the columns loaded at once
-    uint4 xv[NT][kAhead];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      if (busy(nt)) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) xv[nt][j] = column(nt, j);
+      for (int j = 0; j < 4; ++j) {
+        const int ch = h * 128 + channel_of<kGroup>(t, j);
+        xv[h][j] = make_uint4(0, 0, 0, 0);
+        if (!ragged || s * S::kChannels + ch < in)
+          xv[h][j] = __ldg(reinterpret_cast<const uint4*>(xp + 2 * ch));
       }
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     __syncwarp();
-
-    const uint32_t stage = ring + slot * S::kStage;
-    uint32_t w[kMT][2][4];
+    uint32_t w[2][2][4];  // [tile][row g, row g + 8][word]
 #pragma unroll
-    for (int i = 0; i < 2 * kMT; ++i) {
-      const uint32_t row = stage + i * 512 + g * 64;
-      uint32_t(&o)[4] = w[i >> 1][i & 1];
-      if (kGroup == 128) {
-        const uint4 v = lds128(row + ((t ^ chunk_swizzle(g)) << 4));
-        o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
-      } else {
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; j += kGroup == 32 ? 1 : 2) {
-          const int byte = word_channel<kGroup>(t, j) / 2;
-          const uint32_t at = row + ((byte >> 4 ^ chunk_swizzle(g)) << 4) + (byte & 15);
-          if (kGroup == 32) {
-            o[j] = lds32(at);
-          } else {
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t row = stage + (kDown ? r * 8 + g : m * 16 + r * 8 + g) * kRowBytes;
+        uint32_t(&o)[4] = w[m][r];
+#pragma unroll
+        for (int j = 0; j < 4; j += kGroup == 128 ? 4 : kGroup == 64 ? 2 : 1) {
+          const int byte = (kDown ? m * 64 : 0) + channel_of<kGroup>(t, j) / 2;
+          const uint32_t at = row + ((byte >> 4 ^ swizzle(g)) << 4) + (byte & 15);
+          if (kGroup == 128) {
+            const uint4 v = lds128(at);
+            o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+          } else if (kGroup == 64) {
             const uint2 v = lds64(at);
-            o[j] = v.x, o[j + 1 & 3] = v.y;
+            o[j] = v.x, o[(j + 1) & 3] = v.y;
+          } else {
+            o[j] = lds32(at);
           }
         }
       }
-    }
-    const uint32_t scales = stage + S::kCodes + g * 8 + (kGroup == 128 ? (use.s & 1) * 2 : 0);
-    const uint32_t zeros = stage + S::kCodes + S::kRows * 8 + g * 4 + (use.s * kPer & 3);
-    float part[kMT][NT][4] = {};
-    uint32_t nz[kMT][2];
+    const uint32_t sc = stage + S::kCodes + g * S::kScaleRow + (S::kGroups < 2 ? (s & 1) * 2 : 0);
+    const uint32_t zr = stage + S::kCodes + S::kRows * S::kScaleRow + g * S::kZeroRow +
+                        (s * S::kGroups & (S::kZeroRow - 1));
+    float part[2][4] = {};
+    uint32_t nz[2][2];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int q = j / (4 / kPer);  // the word's group
-      if (j == kAhead) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          if (busy(nt)) {
+      for (int m = 0; m < 2; ++m) {
+        const int group = kDown ? m * kPer + q : q, row = kDown ? 0 : m * 16;
+        if (j % (4 / kPer) == 0) {
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) xv[nt][k] = column(nt, (kAhead + k) & 3);
-          }
-      }
-      if (j % (4 / kPer) == 0) {
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            nz[mt][h] =
-                kZeros ? minus_zero(lds8(zeros + mt * 64 + h * 32 + q) & 15) : 0xBE00BE00u;
-      }
-      uint32_t lo[kMT][4], hi[kMT][4];
-#pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) {
-        codes_over_64(w[mt][0][j], nz[mt][0], lo[mt]);
-        codes_over_64(w[mt][1][j], nz[mt][1], hi[mt]);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        if (busy(nt)) {
-          uint32_t b[4];
-          pairs_bf16(xv[nt][j % kAhead], b);
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) {
-            mma_bf16(part[mt][nt], lo[mt][0], hi[mt][0], lo[mt][1], hi[mt][1], b[0], b[1]);
-            mma_bf16(part[mt][nt], lo[mt][2], hi[mt][2], lo[mt][3], hi[mt][3], b[2], b[3]);
-          }
+          for (int r = 0; r < 2; ++r)
+            nz[m][r] = kZeros ? minus_zero(lds8(zr + (row + r * 8) * S::kZeroRow + group) & 15)
+                              : 0xBE00BE00u;
         }
-      if ((j + 1) % (4 / kPer) == 0) {  // the end of a group
+        uint32_t lo[4], hi[4], b[4];
+        codes_over_64(w[m][0][j], nz[m][0], lo);
+        codes_over_64(w[m][1][j], nz[m][1], hi);
+        if (kDown) {
+          const uint4& v = xv[kDown ? m : 0][j];
+          b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+        } else {
+          pairs_bf16(xv[0][j], b);
+        }
+        mma_bf16(part[m], lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
+        mma_bf16(part[m], lo[2], hi[2], lo[3], hi[3], b[2], b[3]);
+        if ((j + 1) % (4 / kPer) == 0) {  // the end of a group
+          const float s0 = __uint_as_float(lds16(sc + row * S::kScaleRow + group * 2) << 16);
+          const float s1 = __uint_as_float(lds16(sc + (row + 8) * S::kScaleRow + group * 2) << 16);
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-          const float s0 = __uint_as_float(lds16(scales + mt * 128 + q * 2) << 16);
-          const float s1 = __uint_as_float(lds16(scales + mt * 128 + 64 + q * 2) << 16);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            if (busy(nt)) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                acc[mt][nt][i] = fmaf(part[mt][nt][i], i < 2 ? s0 : s1, acc[mt][nt][i]);
-                part[mt][nt][i] = 0.0f;
-              }
-            }
+          for (int i = 0; i < 4; ++i) {
+            float& v = acc[kDown ? 0 : m][i];
+            v = fmaf(part[m][i], i < 2 ? s0 : s1, v);
+            part[m][i] = 0.0f;
+          }
         }
       }
     }
-    const Cursor at = use;
-    advance(use);
-    if (use.j != at.j) {  // the tile's last step
-      if (head) {
+  };
+
+  // Up: the tile's h.  Operands are 1/64 of the weights.
+  const auto finish_up = [&](const Entry& e, int n0) {
 #pragma unroll
-        for (int i = 0; i < kMT * NT; ++i)
-          parts[(warp * kMT * NT + i) * 32 + lane] =
-              *reinterpret_cast<const float4*>(acc[i / NT][i % NT]);
-        head = false;
-      } else {
-        finish(at);
-      }
-      clear();
+    for (int i = 0; i < 4; ++i) {
+      const int c = 2 * t + (i & 1);
+      if (c >= e.n) continue;
+      const int row = e.row[c];
+      const float v = weight[row] * silu_times(64.0f * acc[0][i], 64.0f * acc[kM - 1][i]);
+      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+      const float rest = v - __bfloat162float(hi);
+      // channel g of 8 goes to the place that pairs it with g + 4 or g - 4
+      const int64_t at = (int64_t)row * a.N + n0 + (i >> 1) * 8 + (g & 3) * 2 + (g >> 2);
+      a.hi[at] = hi;
+      // an infinite h leaves nothing
+      a.lo[at] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);
+    }
+  };
+  // Down: adds the entry's sums to the tile's, and writes a tile.
+  const auto add_entry = [&](const Entry& e, float* tile) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = acc[0][i] + __shfl_xor_sync(kFull, acc[0][i], 2);  // h in two parts
+      const int c = 2 * t + (i & 1);
+      if (t < 2 && c < e.n) tile[e.tok[c] * 16 + (i >> 1) * 8 + g] += v;
     }
     __syncwarp();
-    issue(slot == 0 ? kStages - 1 : slot - 1);
-    slot = slot == kStages - 1 ? 0 : slot + 1;
+  };
+  const auto clear_tile = [&](float* tile) {
+    for (int i = lane; i < a.T * 16; i += 32) tile[i] = 0.0f;
+    __syncwarp();
+  };
+  const auto finish_down = [&](const float* tile, int n0) {
+    for (int i = lane; i < a.T * 16; i += 32)
+      a.out[(int64_t)(i >> 4) * a.H + n0 + (i & 15)] = __float2bfloat16_rn(64.0f * tile[i]);
+    __syncwarp();
+  };
+  const auto clear = [&]() {
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][i] = 0.0f;
+  };
+
+  // a run that begins inside a tile leaves that tile's sums in its first part
+  bool head = p0 < p1 && (use.s != 0 || (kDown && use.e != 0));
+  float* const first = parts + warp * (S::kParts / 4);
+  float* tile = kDown && !head ? first + 256 : first;
+  if (kDown) clear_tile(tile);
+  int slot = 0, n0 = tile_of(use);
+  for (int p = p0; p < p1;) {
+    const Entry& e = l.entry[use.e];
+    const int n = min(steps - use.s, p1 - p);
+    // columns without a token repeat the first: their sums are not used
+    const uint8_t* xp;
+    if (kDown) {
+      const int c = (g & 3) < e.n ? g & 3 : 0;
+      xp = reinterpret_cast<const uint8_t*>((g < 4 ? a.hi : a.lo) + (int64_t)e.row[c] * a.N);
+    } else {
+      xp = a.x + (int64_t)e.tok[g < e.n ? g : 0] * a.H * 2;
+    }
+    xp += use.s * S::kChannels * 2;
+    for (int i = 0; i < n; ++i) {
+      step(xp, use.s + i, ring + slot * S::kStage);
+      xp += S::kChannels * 2;
+      __syncwarp();
+      issue(ring + (slot == 0 ? kStages - 1 : slot - 1) * S::kStage);
+      slot = slot == kStages - 1 ? 0 : slot + 1;
+    }
+    p += n;
+    use.s += n;
+    if (kDown) {
+      add_entry(e, tile);
+      clear();
+    }
+    if (use.s < steps) break;  // the end of the run
+    use.s = 0;
+    if (kDown && ++use.e < count) continue;
+    if (head) {
+      if (!kDown) {
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+          reinterpret_cast<float4*>(first)[m * 32 + lane] =
+              make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+      }
+      tile = first + 256;
+      head = false;
+    } else if (kDown) {
+      finish_down(tile, n0);
+    } else {
+      finish_up(e, n0);
+    }
+    if (kDown) clear_tile(tile);
+    clear();
+    use.e = 0;
+    ++use.j;
+    n0 = tile_of(use);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 
-  // the end of the run, inside a tile: the warp that has the tile's first step
-  // adds the parts of those after it
+  // The end of the run, inside a tile: the warp that has the tile's first step
+  // adds the parts of those after it, in order.
   const bool open = p0 < p1 && (use.s != 0 || (kDown && use.e != 0));
-  if (open && head) {
+  if (!kDown && open && head) {
 #pragma unroll
-    for (int i = 0; i < kMT * NT; ++i)
-      parts[(warp * kMT * NT + i) * 32 + lane] =
-          *reinterpret_cast<const float4*>(acc[i / NT][i % NT]);
+    for (int m = 0; m < kM; ++m)
+      reinterpret_cast<float4*>(first)[m * 32 + lane] =
+          make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
   }
   __syncthreads();
-  if (open && !head) {
-    const int end = (use.j + 1) * item_steps;
-    for (int v = warp + 1; v < kWarps && start(v) < end; ++v) {
-      if (start(v) == start(v + 1)) continue;
+  if (!open || head) return;
+  const int end = (use.j + 1) * item_steps;
+  for (int v = warp + 1; v < kWarps && start(v) < end; ++v) {
+    if (start(v) == start(v + 1)) continue;
+    const float* other = parts + v * (S::kParts / 4);
+    if (kDown) {
+      for (int i = lane; i < a.T * 16; i += 32) tile[i] += other[i];
+      __syncwarp();
+    } else {
 #pragma unroll
-      for (int i = 0; i < kMT * NT; ++i) {
-        const float4 f = parts[(v * kMT * NT + i) * 32 + lane];
-        float(&c)[4] = acc[i / NT][i % NT];
-        c[0] += f.x, c[1] += f.y, c[2] += f.z, c[3] += f.w;
+      for (int m = 0; m < kM; ++m) {
+        const float4 f = reinterpret_cast<const float4*>(other)[m * 32 + lane];
+        acc[m][0] += f.x, acc[m][1] += f.y, acc[m][2] += f.z, acc[m][3] += f.w;
       }
     }
-    finish(use);
   }
+  if (kDown)
+    finish_down(tile, n0);
+  else
+    finish_up(l.entry[use.e], n0);
 }
 
 // Raises the kernel's shared memory, once per device, and launches it.
@@ -458,20 +491,21 @@ bool launch_layer(Kernel kernel, int bytes, bool (&done)[64], std::mutex& mu, co
 }
 
 // The instance for a group size, with zero points or without.
-#define EP_LAYER_INSTANCE(KERNEL, DOWN, NT, GROUP, ZEROS)                                          \
-  {                                                                                                \
-    static std::mutex mu;                                                                          \
-    static bool done[64] = {};                                                                     \
-    return launch_layer(KERNEL<NT, GROUP, ZEROS>, Shared<DOWN, NT>::kBytes, done, mu, a, blocks, st); \
+#define EP_LAYER_INSTANCE(KERNEL, DOWN, GROUP, ZEROS)                                            \
+  {                                                                                              \
+    static std::mutex mu;                                                                        \
+    static bool done[64] = {};                                                                   \
+    return launch_layer(KERNEL<GROUP, ZEROS>, Sizes<DOWN, GROUP, ZEROS>::kBytes, done, mu, a,    \
+                        blocks, st);                                                             \
   }
-#define EP_LAYER_GROUPS(KERNEL, DOWN, NT, WEIGHTS)                               \
-  if (WEIGHTS.zeros) {                                                           \
-    if (group == 32) EP_LAYER_INSTANCE(KERNEL, DOWN, NT, 32, true)               \
-    if (group == 64) EP_LAYER_INSTANCE(KERNEL, DOWN, NT, 64, true)               \
-    EP_LAYER_INSTANCE(KERNEL, DOWN, NT, 128, true)                               \
-  }                                                                              \
-  if (group == 32) EP_LAYER_INSTANCE(KERNEL, DOWN, NT, 32, false)                \
-  if (group == 64) EP_LAYER_INSTANCE(KERNEL, DOWN, NT, 64, false)                \
-  EP_LAYER_INSTANCE(KERNEL, DOWN, NT, 128, false)
+#define EP_LAYER_INSTANCES(KERNEL, DOWN, WEIGHTS)                     \
+  if (WEIGHTS.zeros) {                                                \
+    if (group == 32) EP_LAYER_INSTANCE(KERNEL, DOWN, 32, true)        \
+    if (group == 64) EP_LAYER_INSTANCE(KERNEL, DOWN, 64, true)        \
+    EP_LAYER_INSTANCE(KERNEL, DOWN, 128, true)                        \
+  }                                                                   \
+  if (group == 32) EP_LAYER_INSTANCE(KERNEL, DOWN, 32, false)         \
+  if (group == 64) EP_LAYER_INSTANCE(KERNEL, DOWN, 64, false)         \
+  EP_LAYER_INSTANCE(KERNEL, DOWN, 128, false)
 
 }  // namespace ep

@@ -5,34 +5,30 @@
 namespace ep {
 namespace {
 
-template <int NT, int kGroup, bool kZeros>
+template <int kGroup, bool kZeros>
 __global__ void __launch_bounds__(kThreads, 1) layer_down_kernel(LayerArgs a) {
-  using S = Shared<true, NT>;
+  using S = Sizes<true, kGroup, kZeros>;
   pdl_wait_then_release();
   extern __shared__ __align__(16) uint8_t smem[];
   Lists& l = *reinterpret_cast<Lists*>(smem + S::kBytes - sizeof(Lists));
-  for (int i = threadIdx.x; i < (int)(sizeof(Lists) / 16); i += kThreads)
-    reinterpret_cast<int4*>(&l)[i] = reinterpret_cast<const int4*>(a.lists)[i];
+  const int count = a.lists->count;
+  for (int i = threadIdx.x; i < count * (int)(sizeof(Entry) / 16); i += kThreads)
+    reinterpret_cast<int4*>(l.entry)[i] = reinterpret_cast<const int4*>(a.lists->entry)[i];
+  if (threadIdx.x == 0) l.count = count;
   __syncthreads();
-  if (l.count == 0) {  // no token chose any expert
+  if (count == 0) {  // no token chose any expert
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < (int64_t)a.T * a.H;
          i += (int64_t)gridDim.x * kThreads)
       a.out[i] = __float2bfloat16_rn(0.0f);
     return;
   }
-  products<true, NT, kGroup, kZeros>(a, l, nullptr, smem);
+  products<true, kGroup, kZeros>(a, l, nullptr, smem);
 }
 
 }  // namespace
 
 bool launch_layer_down(const LayerArgs& a, int group, int blocks, cudaStream_t st) {
-  if (a.T <= 4) {
-    EP_LAYER_GROUPS(layer_down_kernel, true, 1, a.down)
-  }
-  if (a.T <= 8) {
-    EP_LAYER_GROUPS(layer_down_kernel, true, 2, a.down)
-  }
-  EP_LAYER_GROUPS(layer_down_kernel, true, 4, a.down)
+  EP_LAYER_INSTANCES(layer_down_kernel, true, a.down)
 }
 
 }  // namespace ep
