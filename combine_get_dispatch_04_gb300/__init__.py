@@ -33,7 +33,7 @@ EP_MAX_RANKS = 64
 EP_MAX_TOPK = 32
 EP_MAX_EXPERTS = 4096
 EP_LAYER_MAX_TOKENS = 16
-EP_LAYER_MAX_EXPERTS = 1024
+EP_LAYER_MAX_EXPERTS = 512
 EP_NORM_MAX_HIDDEN = 16384
 
 # ep_layout_path_t

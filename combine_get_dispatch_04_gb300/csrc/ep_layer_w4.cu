@@ -5,97 +5,83 @@
 namespace ep {
 namespace {
 
-// What the lists are made of, in shared memory: the experts that some token
-// chose, in order, and who chose them.
-struct Chosen {
-  uint32_t words[kMaxExperts / 32];       // a bit for each expert
-  int mask[kMaxSlots];                    // a bit for each token
-  uint16_t expert[kMaxSlots];
-  uint8_t slot[kMaxSlots][kMaxTokens];    // the token's slot + 1, 0: not chosen
-  int sums[kWarps];
-};
-
-// The tokens' choices, a warp each; every block computes them alike.
-__device__ void route_all(const LayerArgs& a, uint8_t* scratch, int64_t* idx, float* w) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The tokens' choices, a warp each; every block computes them alike.  A launch
+// finds none of its instructions in the SM's caches and fetches each line of them from L2,
+// so up to the products the code is kept short: one float32 copy of the logits and the bias in
+// shared memory serves all types and strides, and loops are not unrolled.
+__device__ void route_all(const LayerArgs& a, float* scratch, int64_t* idx, float* w) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.route.E;
+  float* logits = scratch;
+  float* bias = logits + a.T * E;
+#pragma unroll 1
+  for (int i = tid; i < (a.route.bias ? a.T + 1 : a.T) * E; i += kThreads) {
+    const int t = i / E, e = i - t * E;
+    const int64_t at = t * a.route.stride + e;
+    float v;
+    if (t == a.T)
+      v = a.route.bias[e];
+    else if (a.logits_bf16)
+      v = load_logit<true>(a.route.logits, at);
+    else
+      v = load_logit<false>(a.route.logits, at);
+    logits[i] = v;
+  }
+  __syncthreads();
   if (warp >= a.T) return;
-  uint32_t* key = reinterpret_cast<uint32_t*>(scratch) +
-                  warp * (a.route.E + kMaxGroups + 2 * EP_MAX_TOPK);
-  float* gscore = reinterpret_cast<float*>(key + a.route.E);
+  uint32_t* key = reinterpret_cast<uint32_t*>(bias + E) + warp * (E + kMaxGroups + 2 * EP_MAX_TOPK);
+  float* gscore = reinterpret_cast<float*>(key + E);
   int* slot = reinterpret_cast<int*>(gscore + kMaxGroups);
   float* score = reinterpret_cast<float*>(slot + EP_MAX_TOPK);
   RouteArgs r = a.route;
+  r.logits = logits;
+  r.stride = E;
+  if (r.bias) r.bias = bias;
   r.idx = idx;
   r.w = w;
   float m, z;
-  if (a.logits_bf16) {
-    if (a.group_lanes)
-      choose_in_registers<32, 8, true>(r, warp, lane, a.group_lanes, a.vec, slot, m, z);
-    else
-      choose_in_shared<true>(r, warp, lane, key, gscore, slot, m, z);
-    __syncwarp();
-    write_slots<32, true>(r, warp, true, lane, slot, score, m, z);
-  } else {
-    if (a.group_lanes)
-      choose_in_registers<32, 8, false>(r, warp, lane, a.group_lanes, a.vec, slot, m, z);
-    else
-      choose_in_shared<false>(r, warp, lane, key, gscore, slot, m, z);
-    __syncwarp();
-    write_slots<32, false>(r, warp, true, lane, slot, score, m, z);
-  }
+  choose_in_shared<false, 1>(r, warp, lane, key, gscore, slot, m, z);
+  __syncwarp();
+  write_slots<32, false>(r, warp, true, lane, slot, score, m, z);
 }
 
-// Which experts the slots name, and for each the tokens; returns their number.
-__device__ int gather_chosen(const LayerArgs& a, const int64_t* idx, Chosen& c) {
-  const int tid = threadIdx.x, K = a.route.K, slots = a.T * K;
-  if (tid < kMaxExperts / 32) c.words[tid] = 0;
-  for (int i = tid; i < slots; i += kThreads) {
-    c.mask[i] = 0;
-    *reinterpret_cast<int4*>(c.slot[i]) = make_int4(0, 0, 0, 0);
+// The entries, each of at most `most` tokens, of the experts in the order of
+// their first slots.  A thread looks through all slots for those that name its slot's
+// expert; the code is short on purpose (below).
+__device__ void make_lists(const LayerArgs& a, const int* idx, int* sums, int most, Lists& l) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.route.K;
+  static_assert(kMaxSlots <= kThreads, "a thread for every slot");
+  const int expert = tid < a.T * K ? idx[tid] : -1;
+  int n = 0, before = 0;
+  if (expert >= 0) {
+#pragma unroll 1
+    for (int i = 0; i < a.T * K; ++i) {
+      const bool same = idx[i] == expert;
+      n += same;
+      before += same && i < tid;
+    }
   }
-  __syncthreads();
-  for (int i = tid; i < slots; i += kThreads)
-    if (idx[i] >= 0) atomicOr(&c.words[idx[i] >> 5], 1u << (idx[i] & 31));
-  __syncthreads();
-  int total = 0;
-  for (int j = 0; j < (a.route.E + 31) / 32; ++j) total += __popc(c.words[j]);
-  for (int i = tid; i < slots; i += kThreads) {
-    if (idx[i] < 0) continue;
-    const int e = (int)idx[i], t = i / K;
-    int at = __popc(c.words[e >> 5] & ((1u << (e & 31)) - 1u));
-    for (int j = 0; j < (e >> 5); ++j) at += __popc(c.words[j]);
-    c.expert[at] = (uint16_t)e;  // by every slot that names it, alike
-    c.slot[at][t] = (uint8_t)(i - t * K + 1);
-    atomicOr(&c.mask[at], 1 << t);
-  }
-  __syncthreads();
-  return total;
-}
-
-// The entries of `total` experts, each of at most `most` tokens.
-__device__ void make_lists(const LayerArgs& a, Chosen& c, int total, int most, Lists& l) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  static_assert(kMaxSlots <= kThreads, "a thread for every chosen expert");
-  const int mask = tid < total ? c.mask[tid] : 0;
-  const int own = (__popc(mask) + most - 1) / most;
+  const int own = before ? 0 : (n + most - 1) / most;
   int at = own;  // sums up to and with this thread
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(kFull, at, o);
     if (lane >= o) at += v;
   }
-  if (lane == 31) c.sums[warp] = at;
+  if (lane == 31) sums[warp] = at;
   __syncthreads();
-  for (int i = 0; i < warp; ++i) at += c.sums[i];
+  for (int i = 0; i < warp; ++i) at += sums[i];
   if (tid == kThreads - 1) l.count = at;
-  int k = (at - own) * most;  // entry and column of the next token
-  for (int rest = mask; rest; rest &= rest - 1, ++k) {
-    const int t = __ffs(rest) - 1;
-    Entry& e = l.entry[k / most];
-    e.expert = c.expert[tid];
-    e.n = min(__popc(rest) + k % most, most);
-    e.tok[k % most] = (uint8_t)t;
-    e.row[k % most] = (uint16_t)(t * a.route.K + c.slot[tid][t] - 1);
+  if (own) {
+    int k = 0;  // of its tokens
+    for (int i = tid; k < n; ++i) {
+      if (idx[i] != expert) continue;
+      Entry& e = l.entry[at - own + k / most];
+      e.expert = expert;
+      e.n = min(n - k / most * most, most);
+      e.tok[k % most] = (uint8_t)(i / K);
+      e.row[k % most] = (uint16_t)i;
+      ++k;
+    }
   }
   __syncthreads();
 }
@@ -105,28 +91,30 @@ __global__ void __launch_bounds__(kThreads, 1) layer_up_kernel(LayerArgs a) {
   using S = Sizes<false, kGroup, kZeros>;
   pdl_wait_then_release();
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int64_t idx[kMaxSlots];
+  __shared__ int64_t chosen[kMaxSlots];
   __shared__ float weight[kMaxSlots];
+  __shared__ int idx[kMaxSlots], sums[kWarps];
   // before the products the ring is free
-  static_assert(kWarps * (kMaxExperts + kMaxGroups + 2 * EP_MAX_TOPK) * 4 <= S::kRing &&
-                    sizeof(Chosen) <= S::kRing,
+  static_assert((kMaxExperts * (2 * kMaxTokens + 1) + kMaxTokens * (kMaxGroups + 2 * EP_MAX_TOPK)) *
+                        4 <= S::kRing,
                 "the choice fits into the ring");
-  Chosen& c = *reinterpret_cast<Chosen*>(smem);
   Lists& l = *reinterpret_cast<Lists*>(smem + S::kBytes - sizeof(Lists));
-  route_all(a, smem, idx, weight);
+  const int tid = threadIdx.x;
+  route_all(a, reinterpret_cast<float*>(smem), chosen, weight);
   __syncthreads();
-  const int total = gather_chosen(a, idx, c);
+  if (tid < a.T * a.route.K) idx[tid] = (int)chosen[tid];
+  __syncthreads();
   if (blockIdx.x == gridDim.x - 1) {  // the block with the fewest tiles
-    make_lists(a, c, total, Sizes<true, 128, false>::kColumns, l);
-    for (int i = threadIdx.x; i < a.T * a.route.K; i += kThreads) {
-      a.route.idx[i] = idx[i];
-      a.route.w[i] = weight[i];
+    make_lists(a, idx, sums, Sizes<true, 128, false>::kColumns, l);
+    if (tid < a.T * a.route.K) {
+      a.route.idx[tid] = chosen[tid];
+      a.route.w[tid] = weight[tid];
     }
-    for (int i = threadIdx.x; i < 1 + l.count * (int)(sizeof(Entry) / 16); i += kThreads)
+    for (int i = tid; i < 1 + l.count * (int)(sizeof(Entry) / 16); i += kThreads)
       reinterpret_cast<int4*>(a.lists)[i] = reinterpret_cast<const int4*>(&l)[i];
     __syncthreads();
   }
-  make_lists(a, c, total, S::kColumns, l);
+  make_lists(a, idx, sums, S::kColumns, l);
   products<false, kGroup, kZeros>(a, l, weight, smem);
 }
 
@@ -209,12 +197,6 @@ extern "C" ep_status_t ep_layer_w4(const void* x, int hidden, int inter, int64_t
              topk_weights};
   if (a.route.keep == a.route.G) a.route.G = a.route.keep = 1;  // every group is kept
   a.logits_bf16 = logits_bf16 != 0;
-  a.vec = num_experts % 8 == 0 && aligned16(logits) && row_stride * size % 16 == 0;
-  const int group = num_experts / a.route.G, lanes = group / 8;
-  // eight experts a lane, groups of a power of two of whole lanes: in registers
-  a.group_lanes = num_experts > 256 ? 0
-                  : a.route.G == 1  ? 32
-                  : group % 8 == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
   a.x = static_cast<const uint8_t*>(x);
   a.T = (int)num_tokens;
   a.H = hidden;

@@ -42,8 +42,8 @@ bool launch_layer_down(const LayerArgs& a, int group, int blocks, cudaStream_t s
 
 constexpr int kWarps = 16;  // of a block, one block an SM
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxTokens = 16;
-constexpr int kMaxExperts = 1024;
+constexpr int kMaxTokens = EP_LAYER_MAX_TOKENS;
+constexpr int kMaxExperts = EP_LAYER_MAX_EXPERTS;
 constexpr int kMaxSlots = kMaxTokens * EP_MAX_TOPK;
 
 // A chosen expert with the tokens that chose it, or some of them where they are
@@ -71,8 +71,7 @@ struct Weights {
 
 struct LayerArgs {
   RouteArgs route;
-  bool logits_bf16, vec;
-  int group_lanes;  // of the choice in registers; 0: in shared memory
+  bool logits_bf16;
   const uint8_t* x;
   int T, H, N;
   Weights up, down;
@@ -94,7 +93,7 @@ struct Sizes {
   static constexpr int kZeroRow = kGroups < 4 ? 4 : kGroups;
   static constexpr int kCodes = 2048;
   static constexpr int kStage = kCodes + kRows * (kScaleRow + (kZeros ? kZeroRow : 0));
-  static constexpr int kStages = 4;
+  static constexpr int kStages = 3;
   // a warp's part of a tile whose first step is another warp's; of the down
   // projection also its current tile, both [token][channel]
   static constexpr int kParts = kDown ? 2 * 1024 : 1024;
@@ -125,6 +124,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(addr));
   return v;
+}
+// The codes pass through L2 as the first to be replaced: otherwise they
+// displace what every launch needs again, the kernels' own instructions among it.
+__device__ __forceinline__ void copy16_first(uint32_t dst, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "l"(policy)
+               : "memory");
 }
 template <int kBytes>
 __device__ __forceinline__ void copy_few(uint32_t dst, const void* src) {
@@ -157,6 +163,7 @@ __device__ __forceinline__ void products(const LayerArgs& a, const Lists& l, con
   const int mine = items > (int)blockIdx.x ? (items - (int)blockIdx.x - 1) / (int)gridDim.x + 1 : 0;
   const auto start = [&](int w) { return (int)((int64_t)mine * item_steps * w / kWarps); };
   const int p0 = start(warp), p1 = start(warp + 1);
+  const uint64_t policy = l2_policy_evict_first();
   // Scales and zero points of a step can be copied in words; the row is then
   // a whole number of steps.  Else lanes load them one by one.
   const bool words = W.groups % (S::kGroups < 4 ? 4 : S::kGroups) == 0;
@@ -217,7 +224,7 @@ __device__ __forceinline__ void products(const LayerArgs& a, const Lists& l, con
       const uint8_t* p = codes;
       if (ragged && load.s * kRowBytes + lcol >= W.pitch) p -= load.s * kRowBytes + lcol;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) copy16(stage + write_at(i), p + row_at[i]);
+      for (int i = 0; i < 4; ++i) copy16_first(stage + write_at(i), p + row_at[i], policy);
       codes += kRowBytes;
       // of the step's groups; with fewer than a word's, of the whole word
       const int sg = S::kGroups < 2 ? load.s & ~1 : load.s * S::kGroups;
@@ -259,7 +266,7 @@ __device__ __forceinline__ void products(const LayerArgs& a, const Lists& l, con
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) issue(ring + i * S::kStage);
 
   // --- products ---

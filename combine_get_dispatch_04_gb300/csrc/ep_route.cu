@@ -205,7 +205,7 @@ __global__ void route_any_kernel(RouteArgs a) {
   int* slots = reinterpret_cast<int*>(gscore + kMaxGroups);
   float* score = reinterpret_cast<float*>(slots + EP_MAX_TOPK);
   float m, z;
-  choose_in_shared<kBF16>(a, t, lane, key, gscore, slots, m, z);
+  choose_in_shared<kBF16, 4>(a, t, lane, key, gscore, slots, m, z);
   write_slots<32, kBF16>(a, t, true, lane, slots, score, m, z);
 }
 

@@ -216,23 +216,28 @@ __device__ __forceinline__ void choose_in_registers(const RouteArgs& a, int64_t 
 }
 
 // The same for any E and any groups, by a warp: the keys in shared memory, lanes
-// over experts and over groups.  key: E words, gscore: kMaxGroups.
-template <bool kBF16>
+// over experts and over groups.  key: E words, gscore: kMaxGroups.  kUnroll: of its
+// loops (1 where the code's size counts more than its speed).
+template <bool kBF16, int kUnroll>
 __device__ __forceinline__ void choose_in_shared(const RouteArgs& a, int64_t t, int lane,
                                                  uint32_t* key, float* gscore, int* slots,
                                                  float& m, float& z) {
   m = -INFINITY, z = 1.0f;
   if (!a.sigmoid && (a.bias || !a.renorm)) {
+#pragma unroll kUnroll
     for (int e = lane; e < a.E; e += 32)
       m = fmaxf(m, load_logit<kBF16>(a.logits, t * a.stride + e));
     m = warp_max(m);
     z = 0.0f;
-    for (int e = lane; e < a.E; e += 32) {
+#pragma unroll kUnroll
+  #pragma unroll kUnroll
+  for (int e = lane; e < a.E; e += 32) {
       const float l = load_logit<kBF16>(a.logits, t * a.stride + e);
       z += l > -INFINITY ? exp_from(l, m) : 0.0f;
     }
     z = warp_sum(z);
   }
+#pragma unroll kUnroll
   for (int e = lane; e < a.E; e += 32) {
     const float l = load_logit<kBF16>(a.logits, t * a.stride + e);
     float c = l;
@@ -249,6 +254,7 @@ __device__ __forceinline__ void choose_in_shared(const RouteArgs& a, int64_t t, 
     const int size = a.E / a.G;
     for (int g = lane; g < a.G; g += 32) {
       uint32_t m1 = 0, m2 = 0;
+#pragma unroll kUnroll
       for (int i = 0; i < size; ++i) {
         const uint32_t c = key[g * size + i];
         m2 = max(m2, min(m1, c));
@@ -265,6 +271,7 @@ __device__ __forceinline__ void choose_in_shared(const RouteArgs& a, int64_t t, 
       const int g = lane + 32 * i;
       if (g >= a.G) continue;
       int better = 0;
+#pragma unroll kUnroll
       for (int j = 0; j < a.G; ++j)
         better += gscore[j] > gscore[g] || (gscore[j] == gscore[g] && j < g);
       drop[i] = better >= a.keep;
@@ -273,6 +280,7 @@ __device__ __forceinline__ void choose_in_shared(const RouteArgs& a, int64_t t, 
     for (int i = 0; i < kMaxGroups / 32; ++i) {
       const int g = lane + 32 * i;
       if (g < a.G && drop[i])
+#pragma unroll kUnroll
         for (int j = 0; j < size; ++j) key[g * size + j] = 0;
     }
     __syncwarp();
@@ -281,7 +289,9 @@ __device__ __forceinline__ void choose_in_shared(const RouteArgs& a, int64_t t, 
   for (int k = 0; k < a.K; ++k) {
     uint32_t best = 0;
     int at = 0x7FFFFFFF;
-    for (int e = lane; e < a.E; e += 32) {
+#pragma unroll kUnroll
+  #pragma unroll kUnroll
+  for (int e = lane; e < a.E; e += 32) {
       if (key[e] > best) {
         best = key[e];
         at = e;

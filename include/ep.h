@@ -741,7 +741,7 @@ void ep_debug_set_experts_stall(int step);
  *   the GPU need workspaces of their own.
  * ------------------------------------------------------------------------ */
 #define EP_LAYER_MAX_TOKENS 16
-#define EP_LAYER_MAX_EXPERTS 1024
+#define EP_LAYER_MAX_EXPERTS 512
 
 /* Bytes of device scratch for ep_layer_w4 (0 for invalid sizes). */
 size_t ep_layer_w4_workspace_bytes(int64_t num_tokens, int inter, int num_topk);

@@ -34,7 +34,7 @@ def test_layer_arguments(eplib):
                                  group, q2, s2, z2, group2, idx, w, out, ws, n, None)
     for kw in (dict(x=None), dict(x=ODD), dict(H=0), dict(H=192), dict(H=130), dict(N=0), dict(N=96),
                dict(T=-1), dict(T=17), dict(lg=None), dict(lg=ODD), dict(stride=15), dict(bias=ODD),
-               dict(E=0, stride=0), dict(E=1025, stride=2000), dict(K=0), dict(K=17), dict(E=64, stride=64, K=33),
+               dict(E=0, stride=0), dict(E=513, stride=2000), dict(K=0), dict(K=17), dict(E=64, stride=64, K=33),
                dict(score=2), dict(G=3), dict(G=0), dict(G=4, keep=0), dict(G=4, keep=5), dict(q=None),
                dict(q=ODD), dict(s=None), dict(s=ODD), dict(z=ODD), dict(group=16), dict(group=0),
                dict(q2=None), dict(q2=ODD), dict(s2=None), dict(z2=ODD), dict(group2=48), dict(idx=None),

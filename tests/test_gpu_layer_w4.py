@@ -33,8 +33,8 @@ def check(ep, got, x, logits, gate_up, down, K, **kind):
     out, idx, w = got
     want_idx, want_w = ep.route(logits, K, **kind)
     assert torch.equal(idx, want_idx)
-    # the same float32 formula, its sums (of at most 1024 exponentials: 32 in a lane, then 5
-    # joins, so 37 roundings on either side) in another order
+    # the same float32 formula, its sums (of at most 512 exponentials: 16 in a lane, then 5
+    # joins, so 21 roundings on either side, and a few) in another order
     assert torch.allclose(w, want_w, rtol=96 * 2.0 ** -24, atol=0.0)
     want, off = ref.layer(x, idx, w, gate_up, down)
     bound = off + ref.half_step(BF16) * (want.abs() + off) + 1e-38
@@ -65,7 +65,7 @@ def test_shapes(ep, H, N, groups, zeros, T):
                                   dict(score="sigmoid", renormalize=False),
                                   dict(score="softmax", renormalize=False, scale=0.5),
                                   dict(score="softmax", num_groups=8, topk_groups=3)])
-@pytest.mark.parametrize("E", [64, 96, 256, 320, 1024])
+@pytest.mark.parametrize("E", [64, 96, 256, 320, 512])
 @pytest.mark.parametrize("dtype", [torch.float32, BF16])
 def test_router_options(ep, kind, E, dtype):
     x, logits, a, b = case(ep, 6, 128, 64, E, (128, 64), seed=E)
