@@ -139,88 +139,15 @@ __device__ __forceinline__ void block_sums(float (&v)[kN], float (*part)[kN]) {
   }
 }
 
-// The token's live rows and their weights; run by one warp.
-__device__ __forceinline__ int live_rows(const NormArgs& a, int64_t t, int lane, int32_t* row,
-                                         float* weight) {
-  int32_t r = lane < a.K ? a.slot[t * a.K + lane] : -1;
-  const bool over = r >= a.rows;
-  if (over && a.err) atomicOr(a.err, EP_ERRBIT_CAPACITY);
-  const bool live = r >= 0 && !over;
-  const unsigned all = __ballot_sync(kFull, live);
-  if (live) {
-    const int at = __popc(all & ((1u << lane) - 1u));
-    row[at] = r;
-    weight[at] = a.w ? a.w[t * a.K + lane] : 1.0f;
-  }
-  return __popc(all);
-}
-
-// NV vectors of 8 channels a thread.
-template <int NV, bool kF32, bool kRows>
-__global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
-  pdl_wait_then_release();
-  __shared__ float part[2][kMaxWarps][1];
-  __shared__ int32_t row[EP_MAX_TOPK];
-  __shared__ float weight[EP_MAX_TOPK];
-  __shared__ int live;
+// z and h of token t from its block output y (in 32 bits; of every thread NV
+// vectors) and its stream.
+template <int NV, bool kF32>
+__device__ __forceinline__ void finish_row(const NormArgs& a, int64_t t, float (&y)[NV][8],
+                                           const Stream8<kF32> (&xv)[NV],
+                                           float (*part)[kMaxWarps][1]) {
   const int tid = threadIdx.x, threads = blockDim.x;
-  const int64_t t = blockIdx.x, base = t * a.nvec;
-
-  Stream8<kF32> xv[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = tid + i * threads;
-    if (v < a.nvec) xv[i].load(a.x, base + v);
-    else xv[i].zero();
-  }
-  float y[NV][8];
-  if (kRows) {
-    if (tid < 32) {
-      const int n = live_rows(a, t, tid, row, weight);
-      if (tid == 0) live = n;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) y[i][c] = 0.0f;
-    const int n = live;
-    const int4* src = reinterpret_cast<const int4*>(a.y);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const int4* p = src + (int64_t)row[k] * a.nvec;
-      const float w = weight[k];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = tid + i * threads;
-        if (v < a.nvec) {
-          float f[8];
-          unpack_bf16x8(ld_stream_v4(p + v), f);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) y[i][c] = fmaf(w, f[c], y[i][c]);
-        }
-      }
-    }
-    if (a.comb) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = tid + i * threads;
-        if (v < a.nvec) st_stream_v4(reinterpret_cast<int4*>(a.comb) + base + v, pack8(y[i]));
-      }
-    }
-  } else if (a.y) {
-    int4 yv[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = tid + i * threads;
-      yv[i] = make_int4(0, 0, 0, 0);
-      if (v < a.nvec) yv[i] = ld_stream_v4(reinterpret_cast<const int4*>(a.y) + base + v);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) unpack_bf16x8(yv[i], y[i]);
-  }
-
-  if (kRows || a.y) {
+  const int64_t base = t * a.nvec;
+  if (a.z) {
     float f = a.scale;
     if (a.gate_kind == kGateToken) f *= weight1(a.gate, a.bf16, t);
     if (a.post) {
@@ -278,9 +205,463 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
   }
 }
 
+// The block's output given per token: a block a token, NV vectors of 8 channels a thread.
+template <int NV, bool kF32>
+__global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
+  pdl_wait_then_release();
+  __shared__ float part[2][kMaxWarps][1];
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int64_t base = (int64_t)blockIdx.x * a.nvec;
+  Stream8<kF32> xv[NV];
+  int4 yv[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = tid + i * threads;
+    xv[i].zero();
+    yv[i] = make_int4(0, 0, 0, 0);
+    if (v < a.nvec) {
+      xv[i].load(a.x, base + v);
+      if (a.y) yv[i] = ld_stream_v4(reinterpret_cast<const int4*>(a.y) + base + v);
+    }
+  }
+  float y[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) unpack_bf16x8(yv[i], y[i]);
+  finish_row<NV, kF32>(a, blockIdx.x, y, xv, part);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ int4 lds128(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+// The experts' rows combined first.  A block stays and takes every
+// gridDim-th token; what it reads is one sequence of rows (a token's live rows, then its
+// row of the stream), of which several are on their way with asynchronous
+// copies, each thread's vectors into a place of its own.  The rows of
+// the tokens ahead come from lists that the first warp makes before they are read.
+template <int NV>
+constexpr int kRowsAhead = 4;  // two blocks' rows of 7168 channels on an SM
+constexpr int kLists = 8;
+
+struct RowList {
+  int n;
+  int32_t row[EP_MAX_TOPK];
+  float weight[EP_MAX_TOPK];
+};
+
+// Slot `lane` of token t: its row and weight (-1: none).
+__device__ __forceinline__ void load_slot(const NormArgs& a, int64_t t, int lane, int32_t& row,
+                                          float& weight) {
+  row = -1;
+  weight = 1.0f;
+  if (t < a.T && lane < a.K) {
+    row = __ldg(a.slot + t * a.K + lane);
+    if (a.w) weight = __ldg(a.w + t * a.K + lane);
+  }
+}
+// The live rows of a token, by one warp that holds its slots.
+__device__ __forceinline__ void make_list(const NormArgs& a, int lane, int32_t row, float weight,
+                                          RowList& l) {
+  const bool over = row >= a.rows;
+  if (over && a.err) atomicOr(a.err, EP_ERRBIT_CAPACITY);
+  const bool live = row >= 0 && !over;
+  const unsigned all = __ballot_sync(kFull, live);
+  if (live) {
+    const int at = __popc(all & ((1u << lane) - 1u));
+    l.row[at] = row;
+    l.weight[at] = weight;
+  }
+  if (lane == 0) l.n = __popc(all);
+}
+
+template <int NV, bool kF32>
+__global__ void __launch_bounds__(512) norm_rows_kernel(NormArgs a) {
+  // every token has a row of the sequence at least, so while a token's rows are taken
+  // those of at most kAhead tokens after it are on their way
+  constexpr int kAhead = kRowsAhead<NV>, kS = kF32 ? 2 : 1;
+  static_assert(kAhead + 2 <= kLists, "a list is written while kAhead + 1 others are read");
+  pdl_wait_then_release();
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float part[2][kMaxWarps][1];
+  __shared__ RowList lists[kLists];
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
+  const int64_t stride = gridDim.x;
+  const auto token = [&](int j) { return blockIdx.x + j * stride; };  // of this block
+
+  for (int j = tid >> 5; j < kAhead + 1; j += threads >> 5) {
+    int32_t row;
+    float weight;
+    load_slot(a, token(j), lane, row, weight);
+    make_list(a, lane, row, weight, lists[j]);
+  }
+  int32_t next_row = -1;
+  float next_weight = 1.0f;
+  if (tid < 32) load_slot(a, token(kAhead + 1), lane, next_row, next_weight);
+  __syncthreads();
+
+  const uint32_t place = smem_addr(ring) + tid * 16;
+  const auto at = [&](int slot, int i) { return place + (uint32_t)((slot * NV + i) * threads) * 16; };
+  int load_j = 0, load_k = 0, load_at = 0;
+  const auto issue = [&]() {
+    const int64_t t = token(load_j);
+    if (t < a.T) {
+      const RowList& l = lists[load_j % kLists];
+      const int n = l.n;
+      const bool own = load_k >= n;  // the stream's row
+      const int4* p = own ? static_cast<const int4*>(a.x) + t * a.nvec * kS + (load_k - n)
+                          : reinterpret_cast<const int4*>(a.y) + (int64_t)l.row[load_k] * a.nvec;
+      const int step = own ? kS : 1;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = tid + i * threads;
+        if (v < a.nvec) copy16(at(load_at, i), p + (int64_t)v * step);
+      }
+      if (++load_k == n + kS) {
+        load_k = 0;
+        ++load_j;
+      }
+    }
+    load_at = load_at == kAhead ? 0 : load_at + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < kAhead; ++i) issue();
+
+  int slot = 0;
+  const auto take = [&](int4 (&v)[NV]) {  // the next row of the sequence
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      v[i] = tid + i * threads < a.nvec ? lds128(at(slot, i)) : make_int4(0, 0, 0, 0);
+    slot = slot == kAhead ? 0 : slot + 1;
+    issue();  // into the place that the row before left
+  };
+  for (int j = 0; token(j) < a.T; ++j) {
+    __syncthreads();  // the lists and `part` of the token before are no longer read
+    if (tid < 32) {
+      make_list(a, lane, next_row, next_weight, lists[(j + kAhead + 1) % kLists]);
+      load_slot(a, token(j + kAhead + 2), lane, next_row, next_weight);
+    }
+    float y[NV][8] = {};
+    const RowList& l = lists[j % kLists];
+    const int n = l.n;
+    for (int k = 0; k < n; ++k) {
+      const float w = l.weight[k];
+      int4 v[NV];
+      take(v);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float f[8];
+        unpack_bf16x8(v[i], f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) y[i][c] = fmaf(w, f[c], y[i][c]);
+      }
+    }
+    Stream8<kF32> xv[NV];
+#pragma unroll
+    for (int k = 0; k < kS; ++k) {
+      int4 v[NV];
+      take(v);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) xv[i].v[k] = v[i];
+    }
+    if (a.comb) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = tid + i * threads;
+        if (v < a.nvec)
+          st_stream_v4(reinterpret_cast<int4*>(a.comb) + token(j) * a.nvec + v, pack8(y[i]));
+      }
+    }
+    finish_row<NV, kF32>(a, token(j), y, xv, part);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
+// Rows of at most 8 * kRowThreads channels: a thread has one vector of 8, whose weights
+// and sums over the tokens stay in registers.  A block takes every gridDim-th
+// token and keeps the next ones' vectors on their way with asynchronous copies
+// into places of the thread's own.  A row has two halves, the sums and what is
+// made of them, with a barrier between; where three rows fit into shared memory, the
+// barrier of one row is hidden behind the second half of the row before.
+constexpr int kRowThreads = 896;
+
+// The six sums of a row: z z, y y, z d, q dz, q d, q z.
+constexpr int kSums = 6;
+
+// Two channels.
+using Pair = float2;
+__device__ __forceinline__ Pair make_pair(float lo, float hi) { return make_float2(lo, hi); }
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) { return make_float2(a.x * b.x, a.y * b.y); }
+__device__ __forceinline__ Pair mul2(Pair a, float b) { return make_float2(a.x * b, a.y * b); }
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+}
+__device__ __forceinline__ Pair fma2(Pair a, float b, Pair c) {
+  return make_float2(fmaf(a.x, b, c.x), fmaf(a.y, b, c.y));
+}
+__device__ __forceinline__ float dot2(Pair a, Pair b, float c) {
+  return fmaf(a.x, b.x, fmaf(a.y, b.y, c));
+}
+// Channels 2 i and 2 i + 1 of a vector.
+__device__ __forceinline__ Pair pair_of(const int4& v, int i) {
+  const uint32_t w = (uint32_t)(&v.x)[i];
+  return make_pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <bool kF32>
+__device__ __forceinline__ Pair pair_of(const Stream8<kF32>& v, int i) {
+  if constexpr (kF32)
+    return make_pair(__int_as_float((&v.v[i >> 1].x)[2 * (i & 1)]),
+                     __int_as_float((&v.v[i >> 1].x)[2 * (i & 1) + 1]));
+  else
+    return pair_of(v.v[0], i);
+}
+__device__ __forceinline__ uint32_t pack2(Pair p) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(p.x, p.y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+constexpr int kMaxRing = 220 << 10;  // bytes of a block's rows in shared memory
+template <bool kF32>
+constexpr int kGradPieces = kF32 ? 6 : 4;  // 16-byte pieces of a thread's vectors of a row
+
+// kStages: rows in shared memory, 3 (one row's second half with the next one's first) or 2.
+template <bool kF32, bool kFullGate, int kStages>
+__global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs a) {
+  constexpr int kPieces = kGradPieces<kF32>, kS = kF32 ? 2 : 1;
+  constexpr bool kOverlap = kStages == 3;
+  pdl_wait_then_release();
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float part[2][32][8];
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int warps = threads >> 5;
+  const bool in = tid < a.nvec;
+  const int v = in ? tid : a.nvec - 1;
+  const bool need_y = a.post || a.gate_kind != kGateNone;
+  const bool has_h = a.dh != nullptr;
+
+  Pair pre[4], q[4];  // the channels' weights; q: post * gate
+  {
+    float p[8], w[8], g[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) p[c] = 0.0f, w[c] = g[c] = 1.0f;
+    if (has_h) weight8(a.pre, a.bf16, v, p);
+    if (a.post) weight8(a.post, a.bf16, v, w);
+    if (a.gate_kind == kGateChannel) weight8(a.gate, a.bf16, v, g);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      pre[k] = make_pair(p[2 * k], p[2 * k + 1]);
+      q[k] = make_pair(w[2 * k] * g[2 * k], w[2 * k + 1] * g[2 * k + 1]);
+    }
+  }
+  Pair cpre[4] = {}, cpost[4] = {};  // sums over this block's tokens
+
+  const uint32_t place = smem_addr(ring) + tid * 16, piece = threads * 16;
+  // what is never copied (no such input, no such channel) is 0 throughout
+#pragma unroll 1
+  for (int i = 0; i < kStages * kPieces; ++i) {
+    const int k = i % kPieces;  // z, dz, y, dh
+    const bool copied = k < kS ? has_h : k < 2 * kS ? a.dz != nullptr : k == 2 * kS ? need_y : has_h;
+    if (!in || !copied)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(place + i * piece), "r"(0)
+                   : "memory");
+  }
+  const auto copy = [&](int stage, int64_t t) {
+    if (t < a.T && in) {
+      const int64_t i = t * a.nvec + tid;
+      const uint32_t to = place + stage * kPieces * piece;
+#pragma unroll
+      for (int k = 0; k < kS; ++k) {
+        if (has_h) copy16(to + k * piece, static_cast<const int4*>(a.x) + i * kS + k);
+        if (a.dz) copy16(to + (kS + k) * piece, static_cast<const int4*>(a.dz) + i * kS + k);
+      }
+      if (need_y) copy16(to + 2 * kS * piece, reinterpret_cast<const int4*>(a.y) + i);
+      if (has_h) copy16(to + (2 * kS + 1) * piece, reinterpret_cast<const int4*>(a.dh) + i);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  struct Vectors {
+    Stream8<kF32> z, dz;
+    int4 y, dh;
+  };
+  const auto take = [&](int stage, Vectors& r) {
+    const uint32_t from = place + stage * kPieces * piece;
+#pragma unroll
+    for (int k = 0; k < kS; ++k) {
+      r.z.v[k] = lds128(from + k * piece);
+      r.dz.v[k] = lds128(from + (kS + k) * piece);
+    }
+    r.y = lds128(from + 2 * kS * piece);
+    r.dh = lds128(from + (2 * kS + 1) * piece);
+  };
+  const auto full_gate = [&](int64_t t, Pair (&g)[4]) {
+    float f[8];
+    weight8(a.gate, a.bf16, t * a.nvec + v, f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) g[k] = make_pair(f[2 * k], f[2 * k + 1]);
+  };
+
+  // The row's sums, this warp's part.  A warp folds the six values into each other:
+  // after the steps over 16, 8 and 4 lanes a lane holds one of eight (the last two are nothing).
+  const auto first_half = [&](int64_t t, int stage, int turn) {
+    Vectors r;
+    take(stage, r);
+    Pair g[4];
+    if (kFullGate) full_gate(t, g);
+    float s[8] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const Pair z = pair_of(r.z, k), y = pair_of(r.y, k), d = mul2(pair_of(r.dh, k), pre[k]);
+      Pair p = mul2(y, q[k]);
+      if (kFullGate) p = mul2(p, g[k]);
+      s[0] = dot2(z, z, s[0]);
+      s[1] = dot2(y, y, s[1]);
+      s[2] = dot2(z, d, s[2]);
+      s[3] = dot2(p, pair_of(r.dz, k), s[3]);
+      s[4] = dot2(p, d, s[4]);
+      s[5] = dot2(p, z, s[5]);
+    }
+#pragma unroll
+    for (int h = 4; h; h >>= 1) {
+      const bool upper = lane & (4 * h);
+#pragma unroll
+      for (int k = 0; k < h; ++k) {
+        const float give = upper ? s[k] : s[k + h], keep = upper ? s[k + h] : s[k];
+        s[k] = keep + __shfl_xor_sync(kFull, give, 4 * h);
+      }
+    }
+    s[0] += __shfl_xor_sync(kFull, s[0], 2);
+    s[0] += __shfl_xor_sync(kFull, s[0], 1);
+    if ((lane & 3) == 0) part[turn][warp][lane >> 2] = s[0];
+  };
+  // After the barrier: lane l adds up value l % 8 of the warps.
+  float rz, cz, fr, cy;
+  const auto join = [&](int64_t t, int turn) {
+    float u = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRowThreads / 32; i += 4)
+      if (i + (lane >> 3) < warps) u += part[turn][i + (lane >> 3)][lane & 7];
+    u += __shfl_xor_sync(kFull, u, 8);
+    u += __shfl_xor_sync(kFull, u, 16);
+    float s[kSums];
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) s[i] = __shfl_sync(kFull, u, i);
+    const float inv_h = 1.0f / (float)a.H;
+    rz = has_h ? rsqrtf(s[0] * inv_h + a.eps) : 0.0f;
+    cz = rz * rz * rz * (s[2] * inv_h);
+    const float ry = a.post ? rsqrtf(s[1] * inv_h + a.eps) : 1.0f;
+    const float qt = s[3] + rz * s[4] - cz * s[5];  // sum of q t
+    const float f = a.scale * (a.gate_kind == kGateToken ? weight1(a.gate, a.bf16, t) : 1.0f);
+    fr = f * ry;
+    cy = a.post ? f * ry * ry * ry * (qt * inv_h) : 0.0f;
+    if (a.gate_kind == kGateToken && tid == 0 && a.dgate)
+      static_cast<float*>(a.dgate)[t] = a.scale * ry * qt;
+  };
+  // The row's outputs and its share of the sums over the tokens.
+  const auto second_half = [&](int64_t t, int stage) {
+    if (!in) return;
+    Vectors r;
+    take(stage, r);
+    const int64_t i = t * a.nvec + tid;
+    Pair g[4], tt[kF32 ? 4 : 1], dg[kFullGate ? 4 : 1];
+    if (kFullGate) full_gate(t, g);
+    int4 dx4, dy4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const Pair z = pair_of(r.z, k), y = pair_of(r.y, k), hr = mul2(pair_of(r.dh, k), rz);
+      const Pair tk = fma2(hr, pre[k], fma2(z, -cz, pair_of(r.dz, k)));  // the gradient of x
+      cpre[k] = fma2(hr, z, cpre[k]);
+      Pair u = mul2(tk, fr);
+      if constexpr (kFullGate) {
+        dg[k] = mul2(mul2(u, y), q[k]);
+        u = mul2(u, g[k]);
+      }
+      cpost[k] = fma2(u, y, cpost[k]);  // without the channel's gate, which the second kernel knows
+      (&dy4.x)[k] = (int)pack2(fma2(u, q[k], mul2(y, -cy)));
+      if (kF32)
+        tt[kF32 ? k : 0] = tk;
+      else
+        (&dx4.x)[k] = (int)pack2(tk);
+    }
+    const auto store8 = [&](void* p, const Pair* w) {
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[2 * k] = w[k].x, f[2 * k + 1] = w[k].y;
+      Stream8<true>::store(p, i, f);
+    };
+    if constexpr (kF32)
+      store8(a.dx, tt);
+    else
+      st_stream_v4(static_cast<int4*>(a.dx) + i, dx4);
+    if (a.dy) st_stream_v4(reinterpret_cast<int4*>(a.dy) + i, dy4);
+    if constexpr (kFullGate) {
+      if (a.dgate && a.bf16)
+        st_stream_v4(static_cast<int4*>(a.dgate) + i,
+                     make_int4((int)pack2(dg[0]), (int)pack2(dg[1]), (int)pack2(dg[2]),
+                               (int)pack2(dg[3])));
+      else if (a.dgate)
+        store8(a.dgate, dg);
+    }
+  };
+
+  const int64_t step = gridDim.x;
+  int64_t t = blockIdx.x;
+  copy(0, t);
+  copy(1, t + step);
+  if (kOverlap) {
+    copy(2, t + 2 * step);
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    first_half(t, 0, 0);
+    __syncthreads();
+    join(t, 0);
+    int turn = 1, stage = 0;  // of row t
+    while (true) {
+      const int next = stage == 2 ? 0 : stage + 1;
+      const bool more = t + step < a.T;
+      if (more) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        first_half(t + step, next, turn);
+      }
+      second_half(t, stage);
+      if (!more) break;
+      copy(stage, t + 3 * step);
+      t += step;
+      stage = next;
+      __syncthreads();
+      join(t, turn);
+      turn ^= 1;
+    }
+  } else {
+    for (int turn = 0; t < a.T; t += step, turn ^= 1) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      first_half(t, turn, turn);
+      __syncthreads();
+      join(t, turn);
+      second_half(t, turn);
+      copy(turn, t + 2 * step);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!a.part || !in) return;
+  float4* p = reinterpret_cast<float4*>(a.part + (int64_t)blockIdx.x * 2 * a.H) + 2 * tid;
+  p[0] = make_float4(cpre[0].x, cpre[0].y, cpre[1].x, cpre[1].y);
+  p[1] = make_float4(cpre[2].x, cpre[2].y, cpre[3].x, cpre[3].y);
+  p += a.H / 4;
+  p[0] = make_float4(cpost[0].x, cpost[0].y, cpost[1].x, cpost[1].y);
+  p[1] = make_float4(cpost[2].x, cpost[2].y, cpost[3].x, cpost[3].y);
+}
+
+// Longer rows: NV vectors a thread, loaded when their token's turn comes.
 template <int NV, bool kF32>
 __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
   pdl_wait_then_release();
@@ -431,29 +812,25 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
   }
 }
 
-// The blocks' sums, added up channel by channel: 32 channels a block, 8
-// warps over the blocks of the first kernel.
-__global__ void __launch_bounds__(256) norm_columns_kernel(NormArgs a, int blocks) {
+// The blocks' sums, added up channel by channel: 32 channels of one of the two a
+// block, 16 warps over the blocks of the first kernel.
+__global__ void __launch_bounds__(512) norm_columns_kernel(NormArgs a, int blocks) {
   pdl_wait_then_release();
-  __shared__ float sum[8][2][32];
+  __shared__ float sum[16][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x * 32 + lane;
-  float s0 = 0.0f, s1 = 0.0f;
-  if (h < a.H) {
-#pragma unroll 4
-    for (int b = warp; b < blocks; b += 8) {
-      s0 += a.part[(int64_t)b * 2 * a.H + h];
-      s1 += a.part[(int64_t)b * 2 * a.H + a.H + h];
-    }
-  }
-  sum[warp][0][lane] = s0;
-  sum[warp][1][lane] = s1;
-  __syncthreads();
-  if (warp >= 2 || h >= a.H) return;
+  const int h = blockIdx.x * 32 + lane, which = blockIdx.y;
   float s = 0.0f;
+  if (h < a.H) {
+    const float* p = a.part + which * a.H + h;
+#pragma unroll 8
+    for (int b = warp; b < blocks; b += 16) s += p[(int64_t)b * 2 * a.H];
+  }
+  sum[warp][lane] = s;
+  __syncthreads();
+  if (warp || h >= a.H) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s += sum[i][warp][lane];
-  if (warp == 0) {
+  for (int i = 1; i < 16; ++i) s += sum[i][lane];
+  if (which == 0) {
     if (a.dpre) a.dpre[h] = s;
     return;
   }
@@ -471,21 +848,78 @@ Shape forward_shape(int nvec) {
   const int nv = nvec <= 64 ? 1 : nvec <= 256 ? 2 : 4;
   return {nv, ((nvec + nv - 1) / nv + 31) / 32 * 32};
 }
-Shape backward_shape(int nvec) {
+Shape rows_shape(int nvec) {
   const int nv = nvec <= 128 ? 1 : nvec <= 1024 ? 2 : 4;
   return {nv, ((nvec + nv - 1) / nv + 31) / 32 * 32};
 }
+// One vector a thread, or four for rows beyond that.
+Shape backward_shape(int nvec) {
+  const int nv = nvec <= kRowThreads ? 1 : 4;
+  return {nv, ((nvec + nv - 1) / nv + 31) / 32 * 32};
+}
+// Blocks that stay for the whole of the work: as many threads on an SM as
+// registers allow.
 int backward_blocks(int64_t T, int threads, int sm_count) {
-  const int64_t most = (int64_t)sm_count * (1024 / threads > 8 ? 8 : 1024 / threads < 1 ? 1 : 1024 / threads);
+  const int per = threads >= kRowThreads ? 1 : kRowThreads / threads < 16 ? kRowThreads / threads : 16;
+  const int64_t most = (int64_t)sm_count * per;
   return (int)(T < most ? T : most);
 }
 
+template <bool kF32, bool kFullGate, int kStages>
+bool launch_backward_stages(const NormArgs& a, int blocks, int threads, cudaStream_t st) {
+  constexpr int kThreadBytes = kStages * kGradPieces<kF32> * 16;
+  const auto kernel = norm_grad_row_kernel<kF32, kFullGate, kStages>;
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev] &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxRing) != cudaSuccess)
+      return false;
+    done[dev] = true;
+  }
+  return launch_pdl(kernel, (unsigned)blocks, threads, (size_t)threads * kThreadBytes, st, a) ==
+         cudaSuccess;
+}
+template <bool kF32, bool kFullGate>
+bool launch_backward_rows(const NormArgs& a, int blocks, int threads, cudaStream_t st) {
+  if constexpr (3 * kGradPieces<kF32> * 16 * kRowThreads > kMaxRing) {
+    if (3 * kGradPieces<kF32> * 16 * threads > kMaxRing)
+      return launch_backward_stages<kF32, kFullGate, 2>(a, blocks, threads, st);
+  }
+  return launch_backward_stages<kF32, kFullGate, 3>(a, blocks, threads, st);
+}
+
 template <int NV, bool kF32>
-void launch_forward(const NormArgs& a, int threads, cudaStream_t st) {
-  if (a.slot)
-    launch_pdl(norm_kernel<NV, kF32, true>, (unsigned)a.T, threads, 0, st, a);
-  else
-    launch_pdl(norm_kernel<NV, kF32, false>, (unsigned)a.T, threads, 0, st, a);
+bool launch_rows(const NormArgs& a, int threads, const DeviceProps& props, cudaStream_t st) {
+  const auto kernel = norm_rows_kernel<NV, kF32>;
+  const size_t smem = (size_t)(kRowsAhead<NV> + 1) * NV * threads * 16;
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev] && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (kRowsAhead<NV> + 1) * NV * 512 * 16) != cudaSuccess)
+      return false;
+    done[dev] = true;
+  }
+  // blocks that fit an SM by shared memory (and 8 KB for each block's own) and threads
+  int per = (int)(props.smem_per_sm / (smem + 8192));
+  per = per < 1024 / threads ? per : 1024 / threads;
+  per = per < 1 ? 1 : per > 16 ? 16 : per;
+  const int64_t blocks = (int64_t)per * props.sm_count;
+  return launch_pdl(kernel, (unsigned)(a.T < blocks ? a.T : blocks), threads, smem, st, a) ==
+         cudaSuccess;
+}
+template <int NV, bool kF32>
+bool launch_forward(const NormArgs& a, int threads, const DeviceProps& props, cudaStream_t st) {
+  if (a.slot) return launch_rows<NV, kF32>(a, threads, props, st);
+  return launch_pdl(norm_kernel<NV, kF32>, (unsigned)a.T, threads, 0, st, a) == cudaSuccess;
 }
 
 bool common_ok(const NormArgs& a, int64_t T, int H, int gate_kind, float eps) {
@@ -555,17 +989,22 @@ extern "C" ep_status_t ep_block_norm(const void* x, int stream_f32, const void* 
       overlap(combined, 2 * n, h, 2 * n) || overlap(z, xs, gate, gs) || overlap(h, 2 * n, gate, gs) ||
       overlap(combined, 2 * n, gate, gs))
     return EP_ERR_INVALID_ARG;
-  const Shape s = forward_shape(a.nvec);
+  const Shape s = ll_slot ? rows_shape(a.nvec) : forward_shape(a.nvec);
+  DeviceProps props;
+  if (!device_props(&props)) return EP_ERR_CUDA;
   cudaStream_t st = to_cuda(stream);
-  if (stream_f32)
-    s.nv == 1   ? launch_forward<1, true>(a, s.threads, st)
-    : s.nv == 2 ? launch_forward<2, true>(a, s.threads, st)
-                : launch_forward<4, true>(a, s.threads, st);
-  else
-    s.nv == 1   ? launch_forward<1, false>(a, s.threads, st)
-    : s.nv == 2 ? launch_forward<2, false>(a, s.threads, st)
-                : launch_forward<4, false>(a, s.threads, st);
-  return launch_status();
+  const bool ok =
+      stream_f32 ? (s.nv == 1   ? launch_forward<1, true>(a, s.threads, props, st)
+                    : s.nv == 2 ? launch_forward<2, true>(a, s.threads, props, st)
+                                : launch_forward<4, true>(a, s.threads, props, st))
+                 : (s.nv == 1   ? launch_forward<1, false>(a, s.threads, props, st)
+                    : s.nv == 2 ? launch_forward<2, false>(a, s.threads, props, st)
+                                : launch_forward<4, false>(a, s.threads, props, st));
+  if (!ok) {
+    cudaGetLastError();
+    return EP_ERR_CUDA;
+  }
+  return EP_OK;
 }
 
 extern "C" size_t ep_block_norm_backward_workspace_bytes(int64_t num_tokens, int hidden) {
@@ -643,16 +1082,24 @@ extern "C" ep_status_t ep_block_norm_backward(
       return EP_ERR_CAPACITY;
     a.part = static_cast<float*>(workspace);
   }
-  const auto go = [&](auto kernel) {
-    launch_pdl(kernel, (unsigned)blocks, s.threads, 0, st, a);
-  };
-  if (stream_f32)
-    s.nv == 1 ? go(norm_grad_kernel<1, true>) : s.nv == 2 ? go(norm_grad_kernel<2, true>)
-                                                          : go(norm_grad_kernel<4, true>);
-  else
-    s.nv == 1 ? go(norm_grad_kernel<1, false>) : s.nv == 2 ? go(norm_grad_kernel<2, false>)
-                                                           : go(norm_grad_kernel<4, false>);
-  if (columns)
-    launch_pdl(norm_columns_kernel, (unsigned)((hidden + 31) / 32), 256, 0, st, a, blocks);
-  return launch_status();
+  bool ok;
+  if (s.nv == 1) {
+    const bool full = gate_kind == kGateFull;
+    ok = stream_f32 ? (full ? launch_backward_rows<true, true>(a, blocks, s.threads, st)
+                            : launch_backward_rows<true, false>(a, blocks, s.threads, st))
+                    : (full ? launch_backward_rows<false, true>(a, blocks, s.threads, st)
+                            : launch_backward_rows<false, false>(a, blocks, s.threads, st));
+  } else {
+    ok = (stream_f32 ? launch_pdl(norm_grad_kernel<4, true>, (unsigned)blocks, s.threads, 0, st, a)
+                     : launch_pdl(norm_grad_kernel<4, false>, (unsigned)blocks, s.threads, 0, st,
+                                  a)) == cudaSuccess;
+  }
+  if (ok && columns)
+    ok = launch_pdl(norm_columns_kernel, dim3((unsigned)((hidden + 31) / 32), 2), 512, 0, st, a,
+                    blocks) == cudaSuccess;
+  if (!ok) {
+    cudaGetLastError();
+    return EP_ERR_CUDA;
+  }
+  return EP_OK;
 }
