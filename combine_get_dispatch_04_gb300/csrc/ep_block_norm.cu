@@ -18,6 +18,8 @@
 // block and are joined by a second kernel in a fixed order.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "ep_common.cuh"
 
 namespace ep {
@@ -81,11 +83,32 @@ __device__ __forceinline__ float weight1(const void* p, bool bf16, int64_t i) {
               : static_cast<const float*>(p)[i];
 }
 
-// Eight values of the stream, read once.
+// 32 bytes at once, on a 32-byte boundary.
+__device__ __forceinline__ void ld_stream_32(const void* p, int4 (&v)[2]) {
+  asm("ld.global.nc.L1::no_allocate.L2::256B.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y),
+        "=r"(v[1].z), "=r"(v[1].w)
+      : "l"(p));
+}
+__device__ __forceinline__ void st_stream_32(void* p, const float (&f)[8]) {
+  asm volatile("st.global.cs.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]),
+               "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+               : "memory");
+}
+
+// Eight values of the stream, read once.  Float32 ones are two 16-byte pieces, or one of 32 where
+// the buffer allows it: L2 sees every sector twice otherwise.
 template <bool kF32>
 struct Stream8 {
   int4 v[kF32 ? 2 : 1];
   __device__ __forceinline__ void load(const void* p, int64_t at) {
+    if constexpr (kF32) {
+      const int4* q = static_cast<const int4*>(p) + 2 * at;
+      if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {  // the same for all threads
+        ld_stream_32(q, v);
+        return;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < (kF32 ? 2 : 1); ++i)
       v[i] = ld_stream_v4(static_cast<const int4*>(p) + at * (kF32 ? 2 : 1) + i);
@@ -105,6 +128,10 @@ struct Stream8 {
   static __device__ __forceinline__ void store(void* p, int64_t at, const float (&f)[8]) {
     if constexpr (kF32) {
       int4* q = static_cast<int4*>(p) + 2 * at;
+      if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        st_stream_32(q, f);
+        return;
+      }
       st_stream_v4(q, make_int4(__float_as_int(f[0]), __float_as_int(f[1]), __float_as_int(f[2]),
                                 __float_as_int(f[3])));
       st_stream_v4(q + 1, make_int4(__float_as_int(f[4]), __float_as_int(f[5]),
@@ -466,27 +493,41 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
   }
   Pair cpre[4] = {}, cpost[4] = {};  // sums over this block's tokens
 
-  const uint32_t place = smem_addr(ring) + tid * 16, piece = threads * 16;
+  // A row in shared memory: z, dz, y and dh, each in the threads' order.  Of float32 inputs
+  // a warp's 32 lanes copy neighbouring 16-byte pieces, not each its own two (L2
+  // would see every sector twice).
+  const uint32_t base = smem_addr(ring), piece = threads * 16;
+  const auto place = [&](int stage, int array) {  // array 0..3, of this thread
+    const uint32_t from = base + stage * kPieces * piece;
+    return array < 2 ? from + (array * piece + tid * 16) * kS
+                     : from + (2 * kS + array - 2) * piece + tid * 16;
+  };
   // what is never copied (no such input, no such channel) is 0 throughout
 #pragma unroll 1
-  for (int i = 0; i < kStages * kPieces; ++i) {
-    const int k = i % kPieces;  // z, dz, y, dh
-    const bool copied = k < kS ? has_h : k < 2 * kS ? a.dz != nullptr : k == 2 * kS ? need_y : has_h;
-    if (!in || !copied)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(place + i * piece), "r"(0)
+  for (int i = 0; i < kStages * 4; ++i) {
+    const int k = i & 3;
+    if (in && (k == 1 ? a.dz != nullptr : k == 2 ? need_y : has_h)) continue;
+    for (int j = 0; j < (k < 2 ? kS : 1); ++j)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(place(i >> 2, k) + j * 16),
+                   "r"(0)
                    : "memory");
   }
   const auto copy = [&](int stage, int64_t t) {
-    if (t < a.T && in) {
+    if (t < a.T) {
       const int64_t i = t * a.nvec + tid;
-      const uint32_t to = place + stage * kPieces * piece;
 #pragma unroll
       for (int k = 0; k < kS; ++k) {
-        if (has_h) copy16(to + k * piece, static_cast<const int4*>(a.x) + i * kS + k);
-        if (a.dz) copy16(to + (kS + k) * piece, static_cast<const int4*>(a.dz) + i * kS + k);
+        // piece k * 32 + lane of the warp's
+        const int at = kS == 1 ? tid : warp * 64 + k * 32 + lane;
+        if (at < a.nvec * kS) {
+          const int64_t from = t * a.nvec * kS + at;
+          const uint32_t to = (at - tid * kS) * 16;
+          if (has_h) copy16(place(stage, 0) + to, static_cast<const int4*>(a.x) + from);
+          if (a.dz) copy16(place(stage, 1) + to, static_cast<const int4*>(a.dz) + from);
+        }
       }
-      if (need_y) copy16(to + 2 * kS * piece, reinterpret_cast<const int4*>(a.y) + i);
-      if (has_h) copy16(to + (2 * kS + 1) * piece, reinterpret_cast<const int4*>(a.dh) + i);
+      if (in && need_y) copy16(place(stage, 2), reinterpret_cast<const int4*>(a.y) + i);
+      if (in && has_h) copy16(place(stage, 3), reinterpret_cast<const int4*>(a.dh) + i);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -495,14 +536,21 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
     int4 y, dh;
   };
   const auto take = [&](int stage, Vectors& r) {
-    const uint32_t from = place + stage * kPieces * piece;
 #pragma unroll
     for (int k = 0; k < kS; ++k) {
-      r.z.v[k] = lds128(from + k * piece);
-      r.dz.v[k] = lds128(from + (kS + k) * piece);
+      r.z.v[k] = lds128(place(stage, 0) + k * 16);
+      r.dz.v[k] = lds128(place(stage, 1) + k * 16);
     }
-    r.y = lds128(from + 2 * kS * piece);
-    r.dh = lds128(from + (2 * kS + 1) * piece);
+    r.y = lds128(place(stage, 2));
+    r.dh = lds128(place(stage, 3));
+  };
+  const auto arrived = [&](auto pending) {  // all but the last `pending` rows
+    asm volatile("cp.async.wait_group %0;" ::"n"(decltype(pending)::value) : "memory");
+    if (kF32) __syncwarp();  // other lanes' copies too
+  };
+  const auto again = [&](int stage, int64_t t) {  // a row into the place of one that was read
+    if (kF32) __syncwarp();
+    copy(stage, t);
   };
   const auto full_gate = [&](int64_t t, Pair (&g)[4]) {
     float f[8];
@@ -620,7 +668,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
   copy(1, t + step);
   if (kOverlap) {
     copy(2, t + 2 * step);
-    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    arrived(std::integral_constant<int, 2>());
     first_half(t, 0, 0);
     __syncthreads();
     join(t, 0);
@@ -629,12 +677,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
       const int next = stage == 2 ? 0 : stage + 1;
       const bool more = t + step < a.T;
       if (more) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        arrived(std::integral_constant<int, 1>());
         first_half(t + step, next, turn);
       }
       second_half(t, stage);
       if (!more) break;
-      copy(stage, t + 3 * step);
+      again(stage, t + 3 * step);
       t += step;
       stage = next;
       __syncthreads();
@@ -643,12 +691,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
     }
   } else {
     for (int turn = 0; t < a.T; t += step, turn ^= 1) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      arrived(std::integral_constant<int, 1>());
       first_half(t, turn, turn);
       __syncthreads();
       join(t, turn);
       second_half(t, turn);
-      copy(turn, t + 2 * step);
+      again(turn, t + 2 * step);
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -857,12 +905,14 @@ Shape backward_shape(int nvec) {
   const int nv = nvec <= kRowThreads ? 1 : 4;
   return {nv, ((nvec + nv - 1) / nv + 31) / 32 * 32};
 }
-// Blocks that stay for the whole of the work: as many threads on an SM as
-// registers allow.
+// Blocks that stay for the whole of the work, the same number on every SM: as many
+// threads as registers allow, and three tokens a block at least (997 tokens of 2056 channels: 20.4 us with
+// two on an SM, 23.6 with one, 25.9 with three).
 int backward_blocks(int64_t T, int threads, int sm_count) {
-  const int per = threads >= kRowThreads ? 1 : kRowThreads / threads < 16 ? kRowThreads / threads : 16;
-  const int64_t most = (int64_t)sm_count * per;
-  return (int)(T < most ? T : most);
+  const int most = kRowThreads / threads < 1 ? 1 : kRowThreads / threads < 16 ? kRowThreads / threads : 16;
+  const int64_t want = T / (3 * sm_count);
+  const int64_t blocks = (int64_t)sm_count * (want < 1 ? 1 : want < most ? want : most);
+  return (int)(T < blocks ? T : blocks);
 }
 
 template <bool kF32, bool kFullGate, int kStages>

@@ -9,7 +9,6 @@
 // and rows that no slot names are neither read nor written.
 #include <cuda_bf16.h>
 
-#include "ep_experts_w4.cuh"
 #include "ep_scatter.cuh"
 
 namespace ep {
@@ -44,6 +43,15 @@ __device__ __forceinline__ int4 pack8(const float (&f)[8]) {
   return v;
 }
 
+// exp(-|g|), which cannot overflow, and 1 / (1 + exp(-|g|)).  __expf is off by 2 + 1.173 |g|
+// units in the last place, and the reciprocal by one: of a sigmoid that is
+// at most a few units of 2^-24 for positive g, and 4 + 1.2 |g| for negative.  (expf and a
+// division took 36 instructions a channel of the gradient instead of 25, and those bound it.)
+__device__ __forceinline__ void decay(float g, float& e, float& r) {
+  e = __expf(-fabsf(g));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+}
+
 // The row of slot i (-1: none, or one beyond the buffer, which is reported).
 __device__ __forceinline__ int slot_row(const SwigluArgs& a, int64_t i, bool tell) {
   const int r = a.slot[i];
@@ -54,57 +62,53 @@ __device__ __forceinline__ int slot_row(const SwigluArgs& a, int64_t i, bool tel
   return r;
 }
 
-// Codes and scale of the 16 channels in v, whose block of 128 is held by 8
-// neighbouring lanes.  Every step is rounded as the FP8 dispatch rounds it.  A block
-// with an infinity or a NaN has codes that read back as NaN throughout.
-__device__ __forceinline__ uint4 quantise16(const int4 (&v)[2], float* scale) {
-  uint32_t m = 0;
+// The largest magnitude of a block of 128 channels, 8 in each of 16 neighbouring lanes.
+__device__ __forceinline__ float block_top(const int4& v) {
+  // |x| of finite bf16 is ordered as the low 15 bits, and NaN is above all
+  uint32_t m = __vmaxu2(__vmaxu2((uint32_t)v.x & 0x7FFF7FFFu, (uint32_t)v.y & 0x7FFF7FFFu),
+                        __vmaxu2((uint32_t)v.z & 0x7FFF7FFFu, (uint32_t)v.w & 0x7FFF7FFFu));
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    // |x| of finite bf16 is ordered as the low 15 bits, and NaN is above all
-    m = __vmaxu2(m, __vmaxu2(__vmaxu2((uint32_t)v[i].x & 0x7FFF7FFFu, (uint32_t)v[i].y & 0x7FFF7FFFu),
-                             __vmaxu2((uint32_t)v[i].z & 0x7FFF7FFFu, (uint32_t)v[i].w & 0x7FFF7FFFu)));
-  }
-  m = max(m & 0xFFFFu, m >> 16);
-#pragma unroll
-  for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-  const float top = __uint_as_float(m << 16);
-  const float am = top < 1e-4f ? 1e-4f : top;  // keeps NaN
-  const float inv = __fdiv_rn(448.0f, am);
-  *scale = __fdiv_rn(am, 448.0f);
-  uint32_t q[4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float f[8];
-    unpack_bf16x8(v[i], f);
-    q[2 * i] = cvt_e4m3x4(__fmul_rn(f[0], inv), __fmul_rn(f[1], inv), __fmul_rn(f[2], inv),
-                          __fmul_rn(f[3], inv));
-    q[2 * i + 1] = cvt_e4m3x4(__fmul_rn(f[4], inv), __fmul_rn(f[5], inv), __fmul_rn(f[6], inv),
-                              __fmul_rn(f[7], inv));
-  }
-  return make_uint4(q[0], q[1], q[2], q[3]);
+  for (int o = 8; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kFull, m, o));
+  const float top = __uint_as_float(max(m & 0xFFFFu, m >> 16) << 16);
+  return top < 1e-4f ? 1e-4f : top;  // keeps NaN
 }
-
-__device__ __forceinline__ void dequantise16(const int4& codes, float scale, float (&f)[16]) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&codes);
+// Codes of 8 channels; inv = 448 / the block's largest magnitude.  Every step is
+// rounded as the FP8 dispatch rounds it.  A block with an infinity or a NaN has
+// codes that read back as NaN throughout.
+__device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
+  return make_uint2(cvt_e4m3x4(__fmul_rn(f[0], inv), __fmul_rn(f[1], inv), __fmul_rn(f[2], inv),
+                               __fmul_rn(f[3], inv)),
+                    cvt_e4m3x4(__fmul_rn(f[4], inv), __fmul_rn(f[5], inv), __fmul_rn(f[6], inv),
+                               __fmul_rn(f[7], inv)));
+}
+__device__ __forceinline__ void dequantise8(const uint2& codes, float scale, float (&f)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-        (__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1)) & 0xFFFFu), __NV_E4M3);
-    const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    f[2 * i] = two.x * scale;
-    f[2 * i + 1] = two.y * scale;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t two = (i < 2 ? codes.x : codes.y) >> (16 * (i & 1)) & 0xFFFFu;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    f[2 * i] = v.x * scale;
+    f[2 * i + 1] = v.y * scale;
   }
 }
+__device__ __forceinline__ uint2 ld_stream_v2(const uint2* p) {
+  uint2 v;
+  asm("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];"
+      : "=r"(v.x), "=r"(v.y)
+      : "l"(p));
+  return v;
+}
 
+// Neighbouring lanes take neighbouring vectors of 8 channels, so that every
+// access of a warp fills whole sectors.  (With 16 channels a lane, in two 16-byte
+// accesses 32 bytes apart, L2 saw every sector twice: 795 against 663 us for the
+// gradient of 262144 rows of 2 x 2048.)
 constexpr int kThreads = 128;
-constexpr int kUnroll = 2;  // pieces a lane holds at once
+constexpr int kUnroll = 4;  // vectors a lane holds at once
 
-// A warp takes 32 * kUnroll pieces of one slot's row, a piece being kV vectors
-// of 8 channels of g and the same of u.
+// A warp takes 32 * kUnroll vectors of g, and the same of u, of one slot's row.
 template <bool kKeep>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(SwigluArgs a, int parts) {
-  constexpr int kV = kKeep ? 2 : 1;
   pdl_wait_then_release();
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -114,121 +118,127 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(SwigluArgs a, int part
   const int64_t row = slot_row(a, i, lane == 0 && part == 0);
   if (row < 0) return;
   const float w = a.w ? a.w[i] : 1.0f;
-  const int nvec = a.N / 8, p0 = part * 32 * kUnroll + lane;
+  const int nvec = a.N / 8, v0 = part * 32 * kUnroll + lane;
   const int4* g = reinterpret_cast<const int4*>(a.gate_up) + row * 2 * nvec;
   int4* out = reinterpret_cast<int4*>(a.out) + row * nvec;
 
-  int4 gv[kUnroll][kV], uv[kUnroll][kV];
+  int4 gv[kUnroll], uv[kUnroll];
 #pragma unroll
   for (int j = 0; j < kUnroll; ++j) {
-    const int v = (p0 + 32 * j) * kV;
-#pragma unroll
-    for (int k = 0; k < kV; ++k) {
-      gv[j][k] = uv[j][k] = make_int4(0, 0, 0, 0);
-      if (v < nvec) {
-        gv[j][k] = ld_stream_v4(g + v + k);
-        uv[j][k] = ld_stream_v4(g + nvec + v + k);
-      }
+    const int v = v0 + 32 * j;
+    gv[j] = uv[j] = make_int4(0, 0, 0, 0);
+    if (v < nvec) {
+      gv[j] = ld_stream_v4(g + v);
+      uv[j] = ld_stream_v4(g + nvec + v);
     }
   }
 #pragma unroll
   for (int j = 0; j < kUnroll; ++j) {
-    const int v = (p0 + 32 * j) * kV;
+    const int v = v0 + 32 * j;
+    if (v - lane >= nvec) break;  // the whole warp
+    float f[8], u[8];
+    unpack_bf16x8(gv[j], f);
+    unpack_bf16x8(uv[j], u);
     if (kKeep) {
-      float gs, us;
-      const uint4 gq = quantise16(reinterpret_cast<const int4(&)[2]>(gv[j]), &gs);
-      const uint4 uq = quantise16(reinterpret_cast<const int4(&)[2]>(uv[j]), &us);
+      // the two blocks' quotients both ways, one division a lane
+      const float gt = block_top(gv[j]), ut = block_top(uv[j]);
+      const float t = lane & 1 ? ut : gt;
+      const bool back = lane & 2;
+      const float quotient = __fdiv_rn(back ? t : 448.0f, back ? 448.0f : t);
+      const int lane0 = lane & ~3;
+      const uint2 gq = quantise8(f, __shfl_sync(kFull, quotient, lane0));
+      const uint2 uq = quantise8(u, __shfl_sync(kFull, quotient, lane0 + 1));
       if (v < nvec) {
-        int4* q = reinterpret_cast<int4*>(a.out_codes + row * 2 * a.N) + v / 2;
-        st_stream_v4(q, *reinterpret_cast<const int4*>(&gq));
-        st_stream_v4(q + nvec / 2, *reinterpret_cast<const int4*>(&uq));
-        if ((lane & 7) == 0) {
+        uint2* q = reinterpret_cast<uint2*>(a.out_codes + row * 2 * a.N) + v;
+        st_stream_v2(q, gq);
+        st_stream_v2(q + nvec, uq);
+        if ((lane & 14) == 2) {  // lanes 2 and 3 of 16 have the scales of g and u
           float* s = a.out_scales + row * (2 * a.N / 128) + v / 16;
-          s[0] = gs;
-          s[a.N / 128] = us;
+          s[lane & 1 ? a.N / 128 : 0] = quotient;
         }
       }
     }
     if (v < nvec) {
 #pragma unroll
-      for (int k = 0; k < kV; ++k) {
-        float f[8], u[8];
-        unpack_bf16x8(gv[j][k], f);
-        unpack_bf16x8(uv[j][k], u);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) f[c] = w * silu_times(f[c], u[c]);
-        st_stream_v4(out + v + k, pack8(f));
+      for (int c = 0; c < 8; ++c) {
+        float e, r;
+        decay(f[c], e, r);
+        f[c] = w * (f[c] < 0.0f ? f[c] * e : f[c]) * r * u[c];
       }
+      st_stream_v4(out + v, pack8(f));
     }
   }
 }
 
-// A block takes one slot's row, so that dw is summed in a fixed order.
-template <bool kCodes>
+// A warp (kWarpRow) or a block takes one slot's row, so that dw is summed in a
+// fixed order.
+template <bool kCodes, bool kWarpRow>
 __global__ void __launch_bounds__(256) swiglu_grad_kernel(SwigluArgs a) {
-  constexpr int kV = kCodes ? 2 : 1;
   pdl_wait_then_release();
   __shared__ float sums[8];
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t i = blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  const int tid = kWarpRow ? lane : threadIdx.x, threads = kWarpRow ? 32 : blockDim.x;
+  const int64_t i = kWarpRow ? (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  if (kWarpRow && i >= a.slots) return;
   const int64_t row = slot_row(a, i, tid == 0);
   if (row < 0) {
     if (a.dw && tid == 0) a.dw[i] = 0.0f;
     return;
   }
   const float w = a.w ? a.w[i] : 1.0f;
-  const int nvec = a.N / 8, pieces = nvec / kV;
+  const int nvec = a.N / 8;
   const int4* dh = reinterpret_cast<const int4*>(a.dh) + row * nvec;
-  const int4* src = reinterpret_cast<const int4*>(kCodes ? a.codes + row * 2 * a.N
-                                                         : a.gate_up + row * 4 * a.N);
+  const uint2* codes = reinterpret_cast<const uint2*>(a.codes) + row * 2 * nvec;
+  const int4* gu = reinterpret_cast<const int4*>(a.gate_up) + row * 2 * nvec;
   const float* scale = kCodes ? a.scales + row * (2 * a.N / 128) : nullptr;
   int4* out = reinterpret_cast<int4*>(a.out) + row * 2 * nvec;
   float dot = 0.0f;
-  for (int p = tid; p < pieces; p += blockDim.x) {
-    int4 dv[kV];
-#pragma unroll
-    for (int k = 0; k < kV; ++k) dv[k] = ld_stream_v4(dh + p * kV + k);
-    const int4 gv = ld_stream_v4(src + p), uv = ld_stream_v4(src + pieces + p);
-    float g[8 * kV], u[8 * kV];
+#pragma unroll kWarpRow ? 4 : 1
+  for (int v = tid; v < nvec; v += threads) {
+    const int4 dv = ld_stream_v4(dh + v);
+    float g[8], u[8], d[8], dg[8], du[8];
     if constexpr (kCodes) {
-      dequantise16(gv, scale[p >> 3], g);
-      dequantise16(uv, scale[a.N / 128 + (p >> 3)], u);
+      const uint2 gv = ld_stream_v2(codes + v), uv = ld_stream_v2(codes + nvec + v);
+      dequantise8(gv, scale[v >> 4], g);
+      dequantise8(uv, scale[a.N / 128 + (v >> 4)], u);
     } else {
+      const int4 gv = ld_stream_v4(gu + v), uv = ld_stream_v4(gu + nvec + v);
       unpack_bf16x8(gv, g);
       unpack_bf16x8(uv, u);
     }
+    unpack_bf16x8(dv, d);
 #pragma unroll
-    for (int k = 0; k < kV; ++k) {
-      float d[8], dg[8], du[8];
-      unpack_bf16x8(dv[k], d);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float x = g[8 * k + c], y = u[8 * k + c];
-        // e = exp(-|g|) cannot overflow: s = 1 / (1 + e) or e / (1 + e), and
-        // 1 - s is the other of the two, without cancellation
-        const float e = expf(-fabsf(x));
-        const float r = __fdividef(1.0f, 1.0f + e);
-        const float s = x < 0.0f ? e * r : r, o = x < 0.0f ? r : e * r;
-        const float silu = x * s;
-        dot = fmaf(d[c], silu * y, dot);
-        const float wd = w * d[c];
-        dg[c] = wd * y * fmaf(silu, o, s);
-        du[c] = wd * silu;
-      }
-      st_stream_v4(out + p * kV + k, pack8(dg));
-      st_stream_v4(out + nvec + p * kV + k, pack8(du));
+    for (int c = 0; c < 8; ++c) {
+      // s = 1 / (1 + e) or e / (1 + e), and 1 - s is the other of the two,
+      // without cancellation
+      float e, r;
+      decay(g[c], e, r);
+      const float s = g[c] < 0.0f ? e * r : r, o = g[c] < 0.0f ? r : e * r;
+      const float silu = g[c] * s;
+      dot = fmaf(d[c], silu * u[c], dot);
+      const float wd = w * d[c];
+      dg[c] = wd * u[c] * fmaf(silu, o, s);
+      du[c] = wd * silu;
     }
+    st_stream_v4(out + v, pack8(dg));
+    st_stream_v4(out + nvec + v, pack8(du));
   }
   if (!a.dw) return;
 #pragma unroll
   for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-  if (lane == 0) sums[tid >> 5] = dot;
-  __syncthreads();
-  if (tid == 0) {
-    for (int j = 1; j < (int)blockDim.x / 32; ++j) dot += sums[j];
-    a.dw[i] = dot;
+  if (!kWarpRow) {
+    if (lane == 0) sums[tid >> 5] = dot;
+    __syncthreads();
+    if (tid == 0)
+      for (int j = 1; j < threads / 32; ++j) dot += sums[j];
   }
+  if (tid == 0) a.dw[i] = dot;
 }
+
+// The gradient gives a row a warp where there are this many slots an SM, or where a row
+// has at most this many vectors, else a block.  Warp against block: 4864 rows of 2 x 2048
+// channels 16.5 and 18.7 us, 1216 rows 8.6 and 5.7; 1216 rows of 2 x 256, 2.2 and 2.4.
+constexpr int kManyRows = 32, kShortRow = 64;
 
 // What both directions ask of their sizes and slots.
 bool sizes_ok(int inter, int64_t rows, int64_t T, int K, bool codes) {
@@ -269,7 +279,7 @@ extern "C" ep_status_t ep_ll_swiglu(const void* gate_up, int inter, int64_t num_
   a.out_codes = codes;
   a.out_scales = scales;
   a.err = err_word;
-  const int per = 32 * kUnroll * 8 * (codes ? 2 : 1);  // channels of a warp
+  const int per = 32 * kUnroll * 8;  // channels of a warp
   const int parts = (inter + per - 1) / per;
   const int64_t blocks = (a.slots * parts + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks >= (int64_t(1) << 31)) return EP_ERR_INVALID_ARG;
@@ -313,12 +323,22 @@ extern "C" ep_status_t ep_ll_swiglu_backward(const void* dh, const void* gate_up
   a.out = static_cast<uint8_t*>(dgate_up);
   a.dw = dweights;
   a.err = err_word;
-  // a thread for each piece of the row, at least a warp and at most 256
-  const int pieces = inter / (codes ? 16 : 8);
-  const unsigned threads = (unsigned)min(256, (pieces + 31) / 32 * 32);
-  if (codes)
-    launch_pdl(swiglu_grad_kernel<true>, (unsigned)a.slots, threads, 0, to_cuda(stream), a);
-  else
-    launch_pdl(swiglu_grad_kernel<false>, (unsigned)a.slots, threads, 0, to_cuda(stream), a);
+  DeviceProps props;
+  if (!device_props(&props)) return EP_ERR_CUDA;
+  cudaStream_t st = to_cuda(stream);
+  if (a.slots >= kManyRows * (int64_t)props.sm_count || inter / 8 <= kShortRow) {
+    const unsigned blocks = (unsigned)((a.slots + kThreads / 32 - 1) / (kThreads / 32));
+    if (codes)
+      launch_pdl(swiglu_grad_kernel<true, true>, blocks, kThreads, 0, st, a);
+    else
+      launch_pdl(swiglu_grad_kernel<false, true>, blocks, kThreads, 0, st, a);
+  } else {
+    // a thread for each vector of the row, at least a warp and at most 256
+    const unsigned threads = (unsigned)min(256, (inter / 8 + 31) / 32 * 32);
+    if (codes)
+      launch_pdl(swiglu_grad_kernel<true, false>, (unsigned)a.slots, threads, 0, st, a);
+    else
+      launch_pdl(swiglu_grad_kernel<false, false>, (unsigned)a.slots, threads, 0, st, a);
+  }
   return launch_status();
 }
