@@ -942,17 +942,22 @@ def ll_experts_w4(x: torch.Tensor, weights: W4Weights, layout: LLLayout, *,
 # --------------------------------------------------------------------------
 # a whole layer for a few tokens
 # --------------------------------------------------------------------------
+# The current device's index without torch's check that CUDA is initialised (which
+# a CUDA tensor shows), where torch offers it.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _same_device(first: torch.Tensor, *others: torch.Tensor | None) -> torch.device:
     """The tensors' device, which has to be the current one: a kernel launched on another
     device's stream would run where its buffers are not."""
-    dev = first.device
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise EPError(f"tensors are on different devices ({dev} and {t.device})")
-    if dev.type == "cuda" and torch.cuda.current_device() != dev.index:
-        raise EPError(f"tensors are on {dev}, but the current device is "
-                      f"cuda:{torch.cuda.current_device()}")
-    return dev
+        if t is not None and t.get_device() != index:
+            raise EPError(f"tensors are on different devices ({first.device} and {t.device})")
+    if index >= 0 and _current_device() != index:
+        raise EPError(f"tensors are on {first.device}, but the current device is "
+                      f"cuda:{_current_device()}")
+    return first.device
 
 
 def _w4_shape(w: W4Weights, name: str, experts: int) -> tuple[int, int, int]:
@@ -1053,15 +1058,16 @@ def _norm_arguments(x, gate, post_weight, pre_weight):
     if H % 8 or not 8 <= H <= EP_NORM_MAX_HIDDEN:
         raise EPError(f"hidden must be a multiple of 8 and at most {EP_NORM_MAX_HIDDEN}, got {H}")
     kind, dtype = GATE_NONE, None
-    for name, v in (("post_weight", post_weight), ("pre_weight", pre_weight), ("gate", gate)):
-        if v is None:
-            continue
-        dtype = dtype or v.dtype
-        if dtype not in _STREAMS:
-            raise EPError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
-        _need(v, name, dtype, None if name == "gate" else (H,))
+    if post_weight is not None:
+        dtype = post_weight.dtype
+        _need(post_weight, "post_weight", dtype, (H,))
+    if pre_weight is not None:
+        dtype = dtype or pre_weight.dtype
+        _need(pre_weight, "pre_weight", dtype, (H,))
     if gate is not None:
-        shape = tuple(gate.shape)
+        dtype = dtype or gate.dtype
+        _need(gate, "gate", dtype)
+        shape = gate.shape
         if shape == (H,):
             kind = GATE_CHANNEL
         elif shape == (T, 1):
@@ -1070,6 +1076,9 @@ def _norm_arguments(x, gate, post_weight, pre_weight):
             kind = GATE_FULL
         else:
             raise EPError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}], got {list(shape)}")
+    if dtype is not None and dtype not in _STREAMS:
+        raise EPError("gate and weights must be torch.bfloat16 or torch.float32, got "
+                      f"{dtype}")
     return T, H, kind, int(dtype == torch.bfloat16)
 
 

@@ -126,6 +126,8 @@ bool launch_layer_up(const LayerArgs& a, int group, int blocks, cudaStream_t st)
 
 namespace {
 
+constexpr uint64_t kCodesFirst = 400 << 20;  // bytes of codes of a call
+
 bool sizes_ok(int64_t T, int H, int N, int E, int K) {
   return T >= 0 && T <= kMaxTokens && H >= 32 && N >= 32 && E >= 1 &&
          E <= kMaxExperts && K >= 1 && K <= EP_MAX_TOPK && K <= E && H <= (1 << 20) &&
@@ -145,7 +147,7 @@ extern "C" size_t ep_layer_w4_workspace_bytes(int64_t num_tokens, int inter, int
   if (num_tokens < 1 || num_tokens > kMaxTokens || inter < 1 || num_topk < 1 ||
       num_topk > EP_MAX_TOPK)
     return 0;
-  return sizeof(Lists) + 2 * align_up((size_t)num_tokens * num_topk * inter * 2, 16);
+  return sizeof(Lists) + (size_t)num_tokens * num_topk * align_up(inter, 128) * 4;
 }
 
 extern "C" ep_status_t ep_layer_w4(const void* x, int hidden, int inter, int64_t num_tokens,
@@ -207,8 +209,10 @@ extern "C" ep_status_t ep_layer_w4(const void* x, int hidden, int inter, int64_t
             inter / down_group};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.lists = reinterpret_cast<Lists*>(ws);
-  a.hi = reinterpret_cast<__nv_bfloat16*>(ws + sizeof(Lists));
-  a.lo = reinterpret_cast<__nv_bfloat16*>(ws + sizeof(Lists) + align_up(slots * inter * 2, 16));
+  a.h = reinterpret_cast<__nv_bfloat16*>(ws + sizeof(Lists));
+  a.h_pitch = (int)align_up(inter, 128);
+  a.down_group = down_group;
+  a.codes_first = slots * 3 * hidden * inter / 2 < kCodesFirst;
   a.out = static_cast<__nv_bfloat16*>(out);
   DeviceProps props;
   if (!device_props(&props)) return EP_ERR_CUDA;

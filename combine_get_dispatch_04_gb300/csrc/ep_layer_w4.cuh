@@ -75,7 +75,11 @@ struct LayerArgs {
   const uint8_t* x;
   int T, H, N;
   Weights up, down;
-  __nv_bfloat16 *hi, *lo;  // [T * K, N], every 8 channels in the order of the operand
+  // h [T * K, 2 * pitch]: of every 128 channels the operand's words (place_of), each
+  // 32 channels' upper parts before their lower ones; pitch: N in whole blocks of 128
+  __nv_bfloat16* h;
+  int h_pitch, down_group;
+  bool codes_first;  // out of L2, see copy16_first
   Lists* lists;            // of the down projection
   __nv_bfloat16* out;
 };
@@ -112,10 +116,13 @@ __device__ __forceinline__ void codes_over_64(uint32_t w, uint32_t nz, uint32_t 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o[2 * i + 1]) : "r"(b), "r"(0x7D007D00u), "r"(nz));
   }
 }
-// A pair of -z / 64, z < 16.
-__device__ __forceinline__ uint32_t minus_zero(uint32_t z) {
-  const uint32_t f = __float_as_uint((float)z * -0.015625f);
-  return __byte_perm(f, f, 0x3232);
+// A pair of -z / 64 from byte k of the zero points in w: z 2^-133 times -2^127.
+__device__ __forceinline__ uint32_t minus_zero(uint32_t w, int k) {
+  uint32_t o;
+  asm("mul.rn.bf16x2 %0, %1, %2;"
+      : "=r"(o)
+      : "r"(__byte_perm(w, 0, k | 4 << 4 | k << 8 | 4 << 12)), "r"(0xFF00FF00u));
+  return o;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -125,12 +132,24 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "r"(addr));
   return v;
 }
+// The first product of a sum.
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1,
+                                               uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 // The codes pass through L2 as the first to be replaced: otherwise they
 // displace what every launch needs again, the kernels' own instructions among it.
 __device__ __forceinline__ void copy16_first(uint32_t dst, const void* src, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "l"(policy)
                : "memory");
+}
+__device__ __forceinline__ void copy16_ahead(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 template <int kBytes>
 __device__ __forceinline__ void copy_few(uint32_t dst, const void* src) {
@@ -145,6 +164,15 @@ __device__ __forceinline__ void copy_few(uint32_t dst, const void* src) {
 template <int kGroup>
 __device__ __forceinline__ int channel_of(int t, int j) {
   return kGroup == 128 ? t * 32 + j * 8 : word_channel<kGroup>(t, j);
+}
+
+// Where channel c of h is kept within its row: the 8 channels of word j of thread t lie beside
+// those of the quad's other threads, so that a warp loads them from one line, and
+// within the 8 channel i pairs with i + 4.
+__device__ __forceinline__ int place_of(int c, int group) {
+  const int t = group == 128 ? c >> 5 & 3 : group == 64 ? c >> 4 & 3 : c >> 3 & 3;
+  const int j = group == 128 ? c >> 3 & 3 : group == 64 ? (c >> 5 & 2) | (c >> 3 & 1) : c >> 5 & 3;
+  return (c & ~127) * 2 + j * 64 + t * 8 + (c & 3) * 2 + (c >> 2 & 1);
 }
 
 // The products of one launch.
@@ -223,8 +251,13 @@ __device__ __forceinline__ void products(const LayerArgs& a, const Lists& l, con
       // beyond a row's last channel: any of its bytes, they meet zeros
       const uint8_t* p = codes;
       if (ragged && load.s * kRowBytes + lcol >= W.pitch) p -= load.s * kRowBytes + lcol;
+      if (a.codes_first) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) copy16_first(stage + write_at(i), p + row_at[i], policy);
+        for (int i = 0; i < 4; ++i) copy16_first(stage + write_at(i), p + row_at[i], policy);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) copy16_ahead(stage + write_at(i), p + row_at[i]);
+      }
       codes += kRowBytes;
       // of the step's groups; with fewer than a word's, of the whole word
       const int sg = S::kGroups < 2 ? load.s & ~1 : load.s * S::kGroups;
@@ -273,17 +306,19 @@ __device__ __forceinline__ void products(const LayerArgs& a, const Lists& l, con
   constexpr int kM = kDown ? 1 : 2;  // tiles of sums: gate and up projection
   float acc[kM][4] = {};
   // every step has two tiles of operand A: rows (up) or halves of the channels (down)
-  const auto step = [&](const uint8_t* xp, int s, uint32_t stage) {
-    uint4 xv[kDown ? 2 : 1][4];
-#pragma unroll
-    for (int h = 0; h < (kDown ? 2 : 1); ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int ch = h * 128 + channel_of<kGroup>(t, j);
-        xv[h][j] = make_uint4(0, 0, 0, 0);
-        if (!ragged || s * S::kChannels + ch < in)
-          xv[h][j] = __ldg(reinterpret_cast<const uint4*>(xp + 2 * ch));
-      }
+  // The columns' words of a step; each is loaded for the next step as soon as it has been
+  // multiplied, so that its latency passes behind the products of the others.
+  uint4 xv[kDown ? 2 : 1][4];
+  const auto column = [&](const uint8_t* xp, int s, int h, int j) {
+    const int ch = h * 128 + channel_of<kGroup>(0, j);  // and this thread's, which xp has
+    const int at = kDown ? h * 256 + j * 64 : ch;
+    if (!ragged || s + 1 < steps || s * S::kChannels + channel_of<kGroup>(t, 0) + ch < in)
+      xv[h][j] = __ldg(reinterpret_cast<const uint4*>(xp + 2 * at));
+    else
+      xv[h][j] = make_uint4(0, 0, 0, 0);
+  };
+  constexpr int kColumnBytes = S::kChannels * (kDown ? 4 : 2);  // of a step
+  const auto step = [&](const uint8_t* xp, int s, uint32_t stage, bool more) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     __syncwarp();
     uint32_t w[2][2][4];  // [tile][row g, row g + 8][word]
@@ -308,22 +343,52 @@ __device__ __forceinline__ void products(const LayerArgs& a, const Lists& l, con
           }
         }
       }
-    const uint32_t sc = stage + S::kCodes + g * S::kScaleRow + (S::kGroups < 2 ? (s & 1) * 2 : 0);
-    const uint32_t zr = stage + S::kCodes + S::kRows * S::kScaleRow + g * S::kZeroRow +
-                        (s * S::kGroups & (S::kZeroRow - 1));
-    float part[2][4] = {};
+    // scales and zero points of rows g and g + 8 (of both tiles: up), packed
+    constexpr int kRowSets = kDown ? 1 : 2, kWords = (S::kGroups + 1) / 2;
+    uint32_t sw[kRowSets][2][kWords], zw[kRowSets][2][S::kGroups > 4 ? 2 : 1];
+#pragma unroll
+    for (int m = 0; m < kRowSets; ++m)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = m * 16 + r * 8 + g;
+        const uint32_t sc = stage + S::kCodes + row * S::kScaleRow;
+        uint32_t(&o)[kWords] = sw[m][r];
+        if constexpr (S::kGroups == 1) {
+          o[0] = lds16(sc + (s & 1) * 2);
+        } else if constexpr (kWords == 1) {
+          o[0] = lds32(sc);
+        } else if constexpr (kWords == 2) {
+          const uint2 v = lds64(sc);
+          o[0] = v.x, o[1] = v.y;
+        } else {
+          const uint4 v = lds128(sc);
+          o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+        }
+        if constexpr (kZeros) {
+          const uint32_t zr = stage + S::kCodes + S::kRows * S::kScaleRow + row * S::kZeroRow +
+                              (s * S::kGroups & (S::kZeroRow - 1));
+          if constexpr (S::kGroups > 4) {
+            const uint2 v = lds64(zr);
+            zw[m][r][0] = v.x & 0x0F0F0F0Fu, zw[m][r][1] = v.y & 0x0F0F0F0Fu;
+          } else {
+            zw[m][r][0] = (S::kGroups == 4   ? lds32(zr)
+                           : S::kGroups == 2 ? lds16(zr)
+                                             : lds8(zr)) & 0x0F0F0F0Fu;
+          }
+        }
+      }
+    float part[2][4];
     uint32_t nz[2][2];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int q = j / (4 / kPer);  // the word's group
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const int group = kDown ? m * kPer + q : q, row = kDown ? 0 : m * 16;
+        const int group = kDown ? m * kPer + q : q, set = kDown ? 0 : m;
         if (j % (4 / kPer) == 0) {
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            nz[m][r] = kZeros ? minus_zero(lds8(zr + (row + r * 8) * S::kZeroRow + group) & 15)
-                              : 0xBE00BE00u;
+            nz[m][r] = kZeros ? minus_zero(zw[set][r][group >> 2], group & 3) : 0xBE00BE00u;
         }
         uint32_t lo[4], hi[4], b[4];
         codes_over_64(w[m][0][j], nz[m][0], lo);
@@ -334,16 +399,23 @@ __device__ __forceinline__ void products(const LayerArgs& a, const Lists& l, con
         } else {
           pairs_bf16(xv[0][j], b);
         }
-        mma_bf16(part[m], lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
+        if (j % (4 / kPer) == 0)
+          mma_bf16_first(part[m], lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
+        else
+          mma_bf16(part[m], lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
         mma_bf16(part[m], lo[2], hi[2], lo[3], hi[3], b[2], b[3]);
+        if (more && (kDown || m == 1)) column(xp + kColumnBytes, s + 1, kDown ? m : 0, j);
         if ((j + 1) % (4 / kPer) == 0) {  // the end of a group
-          const float s0 = __uint_as_float(lds16(sc + row * S::kScaleRow + group * 2) << 16);
-          const float s1 = __uint_as_float(lds16(sc + (row + 8) * S::kScaleRow + group * 2) << 16);
+          float sf[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t word = sw[set][r][group >> 1];
+            sf[r] = __uint_as_float(group & 1 ? word & 0xFFFF0000u : word << 16);
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float& v = acc[kDown ? 0 : m][i];
-            v = fmaf(part[m][i], i < 2 ? s0 : s1, v);
-            part[m][i] = 0.0f;
+            v = fmaf(part[m][i], sf[i >> 1], v);
           }
         }
       }
@@ -360,11 +432,11 @@ __device__ __forceinline__ void products(const LayerArgs& a, const Lists& l, con
       const float v = weight[row] * silu_times(64.0f * acc[0][i], 64.0f * acc[kM - 1][i]);
       const __nv_bfloat16 hi = __float2bfloat16_rn(v);
       const float rest = v - __bfloat162float(hi);
-      // channel g of 8 goes to the place that pairs it with g + 4 or g - 4
-      const int64_t at = (int64_t)row * a.N + n0 + (i >> 1) * 8 + (g & 3) * 2 + (g >> 2);
-      a.hi[at] = hi;
+      __nv_bfloat16* to = a.h + (int64_t)row * 2 * a.h_pitch +
+                          place_of(n0 + (i >> 1) * 8 + g, a.down_group);
+      to[0] = hi;
       // an infinite h leaves nothing
-      a.lo[at] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);
+      to[32] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);
     }
   };
   // Down: adds the entry's sums to the tile's, and writes a tile.
@@ -406,14 +478,19 @@ __device__ __forceinline__ void products(const LayerArgs& a, const Lists& l, con
     const uint8_t* xp;
     if (kDown) {
       const int c = (g & 3) < e.n ? g & 3 : 0;
-      xp = reinterpret_cast<const uint8_t*>((g < 4 ? a.hi : a.lo) + (int64_t)e.row[c] * a.N);
+      xp = reinterpret_cast<const uint8_t*>(a.h + (int64_t)e.row[c] * 2 * a.h_pitch +
+                                            (g < 4 ? 0 : 32) + t * 8);
     } else {
-      xp = a.x + (int64_t)e.tok[g < e.n ? g : 0] * a.H * 2;
+      xp = a.x + ((int64_t)e.tok[g < e.n ? g : 0] * a.H + channel_of<kGroup>(t, 0)) * 2;
     }
-    xp += use.s * S::kChannels * 2;
+    xp += use.s * kColumnBytes;
+#pragma unroll
+    for (int h = 0; h < (kDown ? 2 : 1); ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) column(xp, use.s, h, j);
     for (int i = 0; i < n; ++i) {
-      step(xp, use.s + i, ring + slot * S::kStage);
-      xp += S::kChannels * 2;
+      step(xp, use.s + i, ring + slot * S::kStage, i + 1 < n);
+      xp += kColumnBytes;
       __syncwarp();
       issue(ring + (slot == 0 ? kStages - 1 : slot - 1) * S::kStage);
       slot = slot == kStages - 1 ? 0 : slot + 1;
