@@ -972,6 +972,22 @@ bool launch_forward(const NormArgs& a, int threads, const DeviceProps& props, cu
   return launch_pdl(norm_kernel<NV, kF32>, (unsigned)a.T, threads, 0, st, a) == cudaSuccess;
 }
 
+struct Buffer {
+  const void* p;
+  uint64_t n;
+};
+// Whether an output overlaps an input or another output.
+template <int kIn, int kOut>
+bool any_overlap(const Buffer (&in)[kIn], const Buffer (&out)[kOut]) {
+  for (int i = 0; i < kOut; ++i) {
+    for (const Buffer& b : in)
+      if (overlap(out[i].p, out[i].n, b.p, b.n)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
+
 bool common_ok(const NormArgs& a, int64_t T, int H, int gate_kind, float eps) {
   if (T < 0 || T >= (int64_t(1) << 31) || H < 8 || H % 8 || H > kMaxHidden) return false;
   if (gate_kind < kGateNone || gate_kind > kGateFull) return false;
@@ -1031,13 +1047,20 @@ extern "C" ep_status_t ep_block_norm(const void* x, int stream_f32, const void* 
   // a token's outputs are written while others still read: nothing may overlap,
   // but z may be x itself, which each token reads before it writes
   const uint64_t n = (uint64_t)num_tokens * hidden, xs = n * (stream_f32 ? 4 : 2);
-  const uint64_t ys = (uint64_t)a.rows * hidden * 2;
-  const uint64_t gs = gate_kind == kGateFull ? n * (a.bf16 ? 2 : 4) : 0;
-  if ((z != x && overlap(z, xs, x, xs)) || overlap(z, xs, y, ys) || overlap(h, 2 * n, x, xs) ||
-      overlap(h, 2 * n, y, ys) || overlap(h, 2 * n, z, xs) || overlap(combined, 2 * n, x, xs) ||
-      overlap(combined, 2 * n, y, ys) || overlap(combined, 2 * n, z, xs) ||
-      overlap(combined, 2 * n, h, 2 * n) || overlap(z, xs, gate, gs) || overlap(h, 2 * n, gate, gs) ||
-      overlap(combined, 2 * n, gate, gs))
+  const uint64_t each = weights_bf16 ? 2 : 4;
+  const uint64_t gate_size = gate_kind == kGateFull      ? n
+                             : gate_kind == kGateChannel ? hidden
+                             : gate_kind == kGateToken   ? num_tokens
+                                                         : 0;
+  const Buffer in[] = {{z == x ? nullptr : x, xs},
+                       {y, (uint64_t)a.rows * hidden * 2},
+                       {gate, gate_size * each},
+                       {post_weight, hidden * each},
+                       {pre_weight, hidden * each},
+                       {topk_weights, ll_slot ? (uint64_t)num_tokens * num_topk * 4 : 0},
+                       {ll_slot, ll_slot ? (uint64_t)num_tokens * num_topk * 4 : 0}};
+  const Buffer out[] = {{z, xs}, {h, 2 * n}, {combined, 2 * n}};
+  if (any_overlap(in, out) || overlap(h, 2 * n, x, xs) || overlap(combined, 2 * n, x, xs))
     return EP_ERR_INVALID_ARG;
   const Shape s = ll_slot ? rows_shape(a.nvec) : forward_shape(a.nvec);
   DeviceProps props;
@@ -1111,18 +1134,25 @@ extern "C" ep_status_t ep_block_norm_backward(
   if (!gate != (gate_kind == kGateNone) || !dh != !pre_weight) return EP_ERR_INVALID_ARG;
   if (!dx || (!dz && !dh) || (dh && !z) || (need_y && !y)) return EP_ERR_INVALID_ARG;
   const uint64_t n = (uint64_t)num_tokens * hidden, ss = n * (stream_f32 ? 4 : 2);
-  const uint64_t gs = gate_kind == kGateFull ? n * (a.bf16 ? 2 : 4) : 0;
-  const struct {
-    const void* p;
-    uint64_t n;
-  } in[] = {{dz, ss}, {dh, 2 * n}, {z, ss}, {y, 2 * n}, {gate, gs}},
-    out[] = {{dx, ss}, {dy, 2 * n}, {dgate, gs}};
-  for (const auto& o : out)
-    for (const auto& i : in)
-      if (overlap(o.p, o.n, i.p, i.n)) return EP_ERR_INVALID_ARG;
-  for (int i = 0; i < 3; ++i)
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return EP_ERR_INVALID_ARG;
+  const uint64_t each = weights_bf16 ? 2 : 4;
+  const uint64_t gate_size = gate_kind == kGateFull      ? n
+                             : gate_kind == kGateChannel ? hidden
+                             : gate_kind == kGateToken   ? num_tokens
+                                                         : 0;
+  const Buffer in[] = {{dz, ss},
+                       {dh, 2 * n},
+                       {z, ss},
+                       {y, 2 * n},
+                       {gate, gate_size * each},
+                       {post_weight, hidden * each},
+                       {pre_weight, hidden * each}};
+  const Buffer out[] = {{dx, ss},
+                        {dy, 2 * n},
+                        {dgate, gate_size * (gate_kind == kGateFull ? each : 4)},
+                        {dpost_weight, hidden * 4ull},
+                        {dpre_weight, hidden * 4ull},
+                        {columns ? workspace : nullptr, workspace_bytes}};
+  if (any_overlap(in, out)) return EP_ERR_INVALID_ARG;
   DeviceProps props;
   if (!device_props(&props)) return EP_ERR_CUDA;
   const Shape s = backward_shape(a.nvec);

@@ -125,6 +125,52 @@ def test_combine_norm(ep, T, H, E, K, weighted, stream):
     assert int(err) == 0
 
 
+def test_float32_streams_on_16_byte_boundaries(ep):
+    """Buffers that are 16-byte but not 32-byte aligned give what aligned ones give."""
+    T, H = 7, 1032
+    s = inputs(T, H, "full", F32, F32, seed=4)
+    dz, dh = rand(s["gen"], T, H), rand(s["gen"], T, H, dtype=BF16)
+    kind = dict(post_weight=s["post"], pre_weight=s["pre"])
+
+    def off(t):
+        flat = torch.empty(t.numel() + 4, dtype=t.dtype, device="cuda")[4:]
+        assert flat.data_ptr() % 32 == 16
+        return flat.view(t.shape).copy_(t)
+
+    want = ep.block_norm(s["x"], s["y"], gate=s["gate"], **kind)
+    got = ep.block_norm(off(s["x"]), s["y"], gate=off(s["gate"]), out=off(s["x"]), **kind)
+    assert torch.equal(want.z, got.z) and torch.equal(want.h, got.h)
+    want = ep.block_norm_backward(dz, dh, s["x"], s["y"], gate=s["gate"], **kind)
+    got = ep.block_norm_backward(off(dz), dh, off(s["x"]), s["y"], gate=off(s["gate"]), **kind)
+    for name in GRADS:
+        assert torch.equal(getattr(want, name), getattr(got, name)), name
+
+
+def test_offsets_beyond_32_bits(ep):
+    """More than 2^31 elements: the last tokens and rows are those of a small call."""
+    H, T = 7168, 300_100
+    x = torch.zeros((T, H), dtype=BF16, device="cuda")
+    y = torch.zeros((T, H), dtype=BF16, device="cuda")
+    s = inputs(5, H, "channel", BF16, F32, seed=5)
+    x[-5:], y[-5:] = s["x"], s["y"]
+    kind = dict(gate=s["gate"], post_weight=s["post"], pre_weight=s["pre"])
+    want, got = ep.block_norm(s["x"], s["y"], **kind), ep.block_norm(x, y, **kind)
+    assert torch.equal(want.z, got.z[-5:]) and torch.equal(want.h, got.h[-5:])
+    assert not got.z[:100].any() and not got.h[:100].any()
+    dz, dh = torch.zeros_like(x), torch.zeros_like(x)
+    dz[-5:], dh[-5:] = rand(s["gen"], 5, H, dtype=BF16), rand(s["gen"], 5, H, dtype=BF16)
+    want = ep.block_norm_backward(dz[-5:].clone(), dh[-5:].clone(), s["x"], s["y"], **kind)
+    got = ep.block_norm_backward(dz, dh, x, y, **kind)
+    assert torch.equal(want.dx, got.dx[-5:]) and torch.equal(want.dy, got.dy[-5:])
+    del dz, dh, got
+    slot = torch.tensor([[T - 5, T - 1], [T - 2, -1]], dtype=torch.int32, device="cuda")
+    L = ep.LLLayout(slot, None, None, T, 1, 1)
+    got = ep.ll_combine_norm(y, None, L, s["x"][:2].contiguous(), save=True, **kind)
+    small = ep.LLLayout(slot - torch.where(slot < 0, 0, T - 5).to(torch.int32), None, None, 5, 1, 1)
+    want = ep.ll_combine_norm(s["y"], None, small, s["x"][:2].contiguous(), save=True, **kind)
+    assert torch.equal(want.y, got.y) and torch.equal(want.z, got.z) and torch.equal(want.h, got.h)
+
+
 def test_combine_norm_rows_beyond_the_buffer_are_left_out(ep):
     T, H = 4, 64
     x = torch.zeros((T, H), device="cuda")
@@ -153,8 +199,11 @@ def check_backward(r, dz, dh, z, y, gate, post, pre, scale, eps):
         check(got, want[name], bound + ref.half_step(got.dtype) * want[name].abs() + 1e-38, name)
 
 
+# rows of a few vectors; as long as one vector a thread allows (7168) and longer; float32 rows
+# of which three (4688) or two (4696) are kept at once; one, three and many tokens a block
 @pytest.mark.parametrize("T,H", [(1, 8), (3, 256), (5, 520), (700, 264), (37, 2056), (5, 7168),
-                                 (2, 16384), (400, 1024)])
+                                 (2, 16384), (400, 1024), (640, 4688), (310, 4696), (3, 7176),
+                                 (1300, 8192), (20000, 32)])
 @pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
 @pytest.mark.parametrize("stream", [BF16, F32])
 def test_backward(ep, T, H, gate, stream):

@@ -178,6 +178,17 @@ def test_many_replays_see_new_inputs(ep):
         check(ep, (out, idx, w), x, logits, a, b, 2)
 
 
+def test_experts_beyond_32_bits(ep):
+    """Weights of more than 2^31 bytes: the last experts' are read at their place."""
+    E, H, N = 512, 4096, 1152  # 4.8 and 2.4 GB
+    gen = torch.Generator("cuda").manual_seed(3)
+    x = torch.randn((3, H), generator=gen, device="cuda").to(BF16)
+    logits = torch.zeros((3, E), device="cuda")
+    logits[:, -4:] = torch.randn((3, 4), generator=gen, device="cuda") + 10
+    a, b = weights(ep, gen, E, 2 * N, H, 128, True), weights(ep, gen, E, H, N, 128, True)
+    check(ep, ep.layer_w4(x, logits, a, b, 3), x, logits, a, b, 3)
+
+
 def test_no_tokens_and_arguments(ep):
     x, logits, a, b = case(ep, 4, 256, 128, 8)
     out, idx, w = ep.layer_w4(x[:0], logits[:0], a, b, 2)
