@@ -78,6 +78,10 @@ __device__ __forceinline__ void weight8(const void* p, bool bf16, int64_t v, flo
     f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
 }
+// Asks for 8 values that will be read once, later, and passes them on to L2.
+__device__ __forceinline__ void prefetch8(const void* p, bool bf16, int64_t v) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p) + v * (bf16 ? 16 : 32)));
+}
 __device__ __forceinline__ float weight1(const void* p, bool bf16, int64_t i) {
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
               : static_cast<const float*>(p)[i];
@@ -145,8 +149,8 @@ struct Stream8 {
 // Sums of kN values over the block; every thread gets them.  `part` is not
 // written again before the caller's next barrier.
 template <int kN>
-__device__ __forceinline__ void block_sums(float (&v)[kN], float (*part)[kN]) {
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+__device__ __forceinline__ void block_sums(float (&v)[kN], float (*part)[kN], int warps) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < kN; ++i)
 #pragma unroll
@@ -166,13 +170,12 @@ __device__ __forceinline__ void block_sums(float (&v)[kN], float (*part)[kN]) {
   }
 }
 
-// z and h of token t from its block output y (in 32 bits; of every thread NV
-// vectors) and its stream.
+// z and h of token t from its block output y (in 32 bits; of each of `threads` threads
+// NV vectors) and its stream.
 template <int NV, bool kF32>
-__device__ __forceinline__ void finish_row(const NormArgs& a, int64_t t, float (&y)[NV][8],
-                                           const Stream8<kF32> (&xv)[NV],
+__device__ __forceinline__ void finish_row(const NormArgs& a, int64_t t, int tid, int threads,
+                                           float (&y)[NV][8], const Stream8<kF32> (&xv)[NV],
                                            float (*part)[kMaxWarps][1]) {
-  const int tid = threadIdx.x, threads = blockDim.x;
   const int64_t base = t * a.nvec;
   if (a.z) {
     float f = a.scale;
@@ -183,7 +186,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, int64_t t, float (
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int c = 0; c < 8; ++c) s[0] = fmaf(y[i][c], y[i][c], s[0]);
-      block_sums<1>(s, part[0]);
+      block_sums<1>(s, part[0], threads >> 5);
       f *= rsqrtf(s[0] / (float)a.H + a.eps);
     }
 #pragma unroll
@@ -217,7 +220,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, int64_t t, float (
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int c = 0; c < 8; ++c) s[0] = fmaf(y[i][c], y[i][c], s[0]);
-  block_sums<1>(s, part[1]);
+  block_sums<1>(s, part[1], threads >> 5);
   const float r = rsqrtf(s[0] / (float)a.H + a.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -232,13 +235,18 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, int64_t t, float (
   }
 }
 
-// The block's output given per token: a block a token, NV vectors of 8 channels a thread.
-template <int NV, bool kF32>
-__global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
+// The block's output given per token: a block a token, or (kWarpRow) a warp,
+// NV vectors of 8 channels a thread.
+constexpr int kRowWarps = 4;  // of a block whose warps have a token each
+template <int NV, bool kF32, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? kRowWarps * 32 : 512) norm_kernel(NormArgs a) {
   pdl_wait_then_release();
   __shared__ float part[2][kMaxWarps][1];
-  const int tid = threadIdx.x, threads = blockDim.x;
-  const int64_t base = (int64_t)blockIdx.x * a.nvec;
+  const int tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x, threads = kWarpRow ? 32 : blockDim.x;
+  const int64_t t =
+      kWarpRow ? (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  if (kWarpRow && t >= a.T) return;
+  const int64_t base = t * a.nvec;
   Stream8<kF32> xv[NV];
   int4 yv[NV];
 #pragma unroll
@@ -251,10 +259,13 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
       if (a.y) yv[i] = ld_stream_v4(reinterpret_cast<const int4*>(a.y) + base + v);
     }
   }
+  if (a.gate_kind == kGateFull) {
+    for (int v = tid; v < a.nvec; v += threads) prefetch8(a.gate, a.bf16, base + v);
+  }
   float y[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) unpack_bf16x8(yv[i], y[i]);
-  finish_row<NV, kF32>(a, blockIdx.x, y, xv, part);
+  finish_row<NV, kF32>(a, t, tid, threads, y, xv, part);
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -273,14 +284,14 @@ __device__ __forceinline__ int4 lds128(uint32_t addr) {
 // row of the stream), of which several are on their way with asynchronous
 // copies, each thread's vectors into a place of its own.  The rows of
 // the tokens ahead come from lists that the first warp makes before they are read.
-template <int NV>
-constexpr int kRowsAhead = 4;  // two blocks' rows of 7168 channels on an SM
+constexpr int kRowsAhead = 3;
 constexpr int kLists = 8;
 
 struct RowList {
-  int n;
-  int32_t row[EP_MAX_TOPK];
+  int n;                            // live rows
   float weight[EP_MAX_TOPK];
+  const int4* row[EP_MAX_TOPK + 2]; // and the stream's: its row, or (float32) the two
+                                    // 16-byte halves of its vectors
 };
 
 // Slot `lane` of token t: its row and weight (-1: none).
@@ -293,26 +304,29 @@ __device__ __forceinline__ void load_slot(const NormArgs& a, int64_t t, int lane
     if (a.w) weight = __ldg(a.w + t * a.K + lane);
   }
 }
-// The live rows of a token, by one warp that holds its slots.
-__device__ __forceinline__ void make_list(const NormArgs& a, int lane, int32_t row, float weight,
-                                          RowList& l) {
+// What token t reads, by one warp that holds its slots.
+template <int kS>
+__device__ __forceinline__ void make_list(const NormArgs& a, int64_t t, int lane, int32_t row,
+                                          float weight, RowList& l) {
   const bool over = row >= a.rows;
   if (over && a.err) atomicOr(a.err, EP_ERRBIT_CAPACITY);
   const bool live = row >= 0 && !over;
   const unsigned all = __ballot_sync(kFull, live);
+  const int n = __popc(all);
   if (live) {
     const int at = __popc(all & ((1u << lane) - 1u));
-    l.row[at] = row;
+    l.row[at] = reinterpret_cast<const int4*>(a.y) + (int64_t)row * a.nvec;
     l.weight[at] = weight;
   }
-  if (lane == 0) l.n = __popc(all);
+  if (lane < kS) l.row[n + lane] = static_cast<const int4*>(a.x) + t * a.nvec * kS + lane;
+  if (lane == 0) l.n = n;
 }
 
 template <int NV, bool kF32>
 __global__ void __launch_bounds__(512) norm_rows_kernel(NormArgs a) {
   // every token has a row of the sequence at least, so while a token's rows are taken
   // those of at most kAhead tokens after it are on their way
-  constexpr int kAhead = kRowsAhead<NV>, kS = kF32 ? 2 : 1;
+  constexpr int kAhead = kRowsAhead, kS = kF32 ? 2 : 1;
   static_assert(kAhead + 2 <= kLists, "a list is written while kAhead + 1 others are read");
   pdl_wait_then_release();
   extern __shared__ __align__(16) uint8_t ring[];
@@ -321,59 +335,61 @@ __global__ void __launch_bounds__(512) norm_rows_kernel(NormArgs a) {
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
   const int64_t stride = gridDim.x;
   const auto token = [&](int j) { return blockIdx.x + j * stride; };  // of this block
+  const int mine = (int)((a.T - blockIdx.x + stride - 1) / stride);
 
   for (int j = tid >> 5; j < kAhead + 1; j += threads >> 5) {
     int32_t row;
     float weight;
     load_slot(a, token(j), lane, row, weight);
-    make_list(a, lane, row, weight, lists[j]);
+    make_list<kS>(a, token(j), lane, row, weight, lists[j]);
   }
   int32_t next_row = -1;
   float next_weight = 1.0f;
   if (tid < 32) load_slot(a, token(kAhead + 1), lane, next_row, next_weight);
   __syncthreads();
 
-  const uint32_t place = smem_addr(ring) + tid * 16;
-  const auto at = [&](int slot, int i) { return place + (uint32_t)((slot * NV + i) * threads) * 16; };
-  int load_j = 0, load_k = 0, load_at = 0;
+  bool in[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) in[i] = tid + i * threads < a.nvec;
+  const uint32_t piece = threads * 16, first = smem_addr(ring) + tid * 16;
+  const uint32_t end = first + (kAhead + 1) * NV * piece;  // of this thread's places
+  int load_j = 0, load_k = 0;
+  uint32_t load_at = first, take_at = first;
   const auto issue = [&]() {
-    const int64_t t = token(load_j);
-    if (t < a.T) {
+    if (load_j < mine) {
       const RowList& l = lists[load_j % kLists];
       const int n = l.n;
-      const bool own = load_k >= n;  // the stream's row
-      const int4* p = own ? static_cast<const int4*>(a.x) + t * a.nvec * kS + (load_k - n)
-                          : reinterpret_cast<const int4*>(a.y) + (int64_t)l.row[load_k] * a.nvec;
-      const int step = own ? kS : 1;
+      const int4* p = l.row[load_k];
+      const int64_t step = load_k < n ? 1 : kS;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = tid + i * threads;
-        if (v < a.nvec) copy16(at(load_at, i), p + (int64_t)v * step);
-      }
+      for (int i = 0; i < NV; ++i)
+        if (in[i]) copy16(load_at + i * piece, p + (tid + i * threads) * step);
       if (++load_k == n + kS) {
         load_k = 0;
         ++load_j;
       }
     }
-    load_at = load_at == kAhead ? 0 : load_at + 1;
+    load_at += NV * piece;
+    if (load_at == end) load_at = first;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll 1
   for (int i = 0; i < kAhead; ++i) issue();
 
-  int slot = 0;
   const auto take = [&](int4 (&v)[NV]) {  // the next row of the sequence
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      v[i] = tid + i * threads < a.nvec ? lds128(at(slot, i)) : make_int4(0, 0, 0, 0);
-    slot = slot == kAhead ? 0 : slot + 1;
+      v[i] = in[i] ? lds128(take_at + i * piece) : make_int4(0, 0, 0, 0);
+    take_at += NV * piece;
+    if (take_at == end) take_at = first;
     issue();  // into the place that the row before left
   };
-  for (int j = 0; token(j) < a.T; ++j) {
+  for (int j = 0; j < mine; ++j) {
     __syncthreads();  // the lists and `part` of the token before are no longer read
     if (tid < 32) {
-      make_list(a, lane, next_row, next_weight, lists[(j + kAhead + 1) % kLists]);
+      make_list<kS>(a, token(j + kAhead + 1), lane, next_row, next_weight,
+                    lists[(j + kAhead + 1) % kLists]);
       load_slot(a, token(j + kAhead + 2), lane, next_row, next_weight);
     }
     float y[NV][8] = {};
@@ -407,7 +423,7 @@ __global__ void __launch_bounds__(512) norm_rows_kernel(NormArgs a) {
           st_stream_v4(reinterpret_cast<int4*>(a.comb) + token(j) * a.nvec + v, pack8(y[i]));
       }
     }
-    finish_row<NV, kF32>(a, token(j), y, xv, part);
+    finish_row<NV, kF32>(a, token(j), tid, threads, y, xv, part);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -463,7 +479,8 @@ template <bool kF32>
 constexpr int kGradPieces = kF32 ? 6 : 4;  // 16-byte pieces of a thread's vectors of a row
 
 // kStages: rows in shared memory, 3 (one row's second half with the next one's first) or 2.
-template <bool kF32, bool kFullGate, int kStages>
+// kH: with dh (the norm before the next block), kY: with y (the norm after the block or a gate).
+template <bool kF32, bool kFullGate, int kStages, bool kH, bool kY>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs a) {
   constexpr int kPieces = kGradPieces<kF32>, kS = kF32 ? 2 : 1;
   constexpr bool kOverlap = kStages == 3;
@@ -474,15 +491,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
   const int warps = threads >> 5;
   const bool in = tid < a.nvec;
   const int v = in ? tid : a.nvec - 1;
-  const bool need_y = a.post || a.gate_kind != kGateNone;
-  const bool has_h = a.dh != nullptr;
-
   Pair pre[4], q[4];  // the channels' weights; q: post * gate
   {
     float p[8], w[8], g[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) p[c] = 0.0f, w[c] = g[c] = 1.0f;
-    if (has_h) weight8(a.pre, a.bf16, v, p);
+    if (kH) weight8(a.pre, a.bf16, v, p);
     if (a.post) weight8(a.post, a.bf16, v, w);
     if (a.gate_kind == kGateChannel) weight8(a.gate, a.bf16, v, g);
 #pragma unroll
@@ -506,7 +520,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
 #pragma unroll 1
   for (int i = 0; i < kStages * 4; ++i) {
     const int k = i & 3;
-    if (in && (k == 1 ? a.dz != nullptr : k == 2 ? need_y : has_h)) continue;
+    if (in && (k == 1 ? a.dz != nullptr : k == 2 ? kY && a.y : kH)) continue;
     for (int j = 0; j < (k < 2 ? kS : 1); ++j)
       asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(place(i >> 2, k) + j * 16),
                    "r"(0)
@@ -522,12 +536,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
         if (at < a.nvec * kS) {
           const int64_t from = t * a.nvec * kS + at;
           const uint32_t to = (at - tid * kS) * 16;
-          if (has_h) copy16(place(stage, 0) + to, static_cast<const int4*>(a.x) + from);
+          if (kH) copy16(place(stage, 0) + to, static_cast<const int4*>(a.x) + from);
           if (a.dz) copy16(place(stage, 1) + to, static_cast<const int4*>(a.dz) + from);
         }
       }
-      if (in && need_y) copy16(place(stage, 2), reinterpret_cast<const int4*>(a.y) + i);
-      if (in && has_h) copy16(place(stage, 3), reinterpret_cast<const int4*>(a.dh) + i);
+      if (kY && in && a.y) copy16(place(stage, 2), reinterpret_cast<const int4*>(a.y) + i);
+      if (kFullGate && in) prefetch8(a.gate, a.bf16, i);
+      if (kH && in) copy16(place(stage, 3), reinterpret_cast<const int4*>(a.dh) + i);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -562,22 +577,28 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
   // The row's sums, this warp's part.  A warp folds the six values into each other:
   // after the steps over 16, 8 and 4 lanes a lane holds one of eight (the last two are nothing).
   const auto first_half = [&](int64_t t, int stage, int turn) {
+    float s[8] = {};
     Vectors r;
     take(stage, r);
     Pair g[4];
     if (kFullGate) full_gate(t, g);
-    float s[8] = {};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const Pair z = pair_of(r.z, k), y = pair_of(r.y, k), d = mul2(pair_of(r.dh, k), pre[k]);
-      Pair p = mul2(y, q[k]);
-      if (kFullGate) p = mul2(p, g[k]);
-      s[0] = dot2(z, z, s[0]);
-      s[1] = dot2(y, y, s[1]);
-      s[2] = dot2(z, d, s[2]);
-      s[3] = dot2(p, pair_of(r.dz, k), s[3]);
-      s[4] = dot2(p, d, s[4]);
-      s[5] = dot2(p, z, s[5]);
+      if (kH) {
+        s[0] = dot2(z, z, s[0]);
+        s[2] = dot2(z, d, s[2]);
+      }
+      if (kY) {
+        Pair p = mul2(y, q[k]);
+        if (kFullGate) p = mul2(p, g[k]);
+        s[1] = dot2(y, y, s[1]);
+        s[3] = dot2(p, pair_of(r.dz, k), s[3]);
+        if (kH) {
+          s[4] = dot2(p, d, s[4]);
+          s[5] = dot2(p, z, s[5]);
+        }
+      }
     }
 #pragma unroll
     for (int h = 4; h; h >>= 1) {
@@ -605,7 +626,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
 #pragma unroll
     for (int i = 0; i < kSums; ++i) s[i] = __shfl_sync(kFull, u, i);
     const float inv_h = 1.0f / (float)a.H;
-    rz = has_h ? rsqrtf(s[0] * inv_h + a.eps) : 0.0f;
+    rz = kH ? rsqrtf(s[0] * inv_h + a.eps) : 0.0f;
     cz = rz * rz * rz * (s[2] * inv_h);
     const float ry = a.post ? rsqrtf(s[1] * inv_h + a.eps) : 1.0f;
     const float qt = s[3] + rz * s[4] - cz * s[5];  // sum of q t
@@ -626,16 +647,23 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
     int4 dx4, dy4;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const Pair z = pair_of(r.z, k), y = pair_of(r.y, k), hr = mul2(pair_of(r.dh, k), rz);
-      const Pair tk = fma2(hr, pre[k], fma2(z, -cz, pair_of(r.dz, k)));  // the gradient of x
-      cpre[k] = fma2(hr, z, cpre[k]);
-      Pair u = mul2(tk, fr);
-      if constexpr (kFullGate) {
-        dg[k] = mul2(mul2(u, y), q[k]);
-        u = mul2(u, g[k]);
+      Pair tk = pair_of(r.dz, k);  // the gradient of x
+      if (kH) {
+        const Pair z = pair_of(r.z, k), hr = mul2(pair_of(r.dh, k), rz);
+        tk = fma2(hr, pre[k], fma2(z, -cz, tk));
+        cpre[k] = fma2(hr, z, cpre[k]);
       }
-      cpost[k] = fma2(u, y, cpost[k]);  // without the channel's gate, which the second kernel knows
-      (&dy4.x)[k] = (int)pack2(fma2(u, q[k], mul2(y, -cy)));
+      Pair u = mul2(tk, fr);
+      if (kY) {
+        const Pair y = pair_of(r.y, k);
+        if constexpr (kFullGate) {
+          dg[k] = mul2(mul2(u, y), q[k]);
+          u = mul2(u, g[k]);
+        }
+        cpost[k] = fma2(u, y, cpost[k]);  // without the channel's gate, which the second kernel knows
+        u = fma2(u, q[k], mul2(y, -cy));
+      }
+      (&dy4.x)[k] = (int)pack2(u);
       if (kF32)
         tt[kF32 ? k : 0] = tk;
       else
@@ -661,7 +689,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
         store8(a.dgate, dg);
     }
   };
-
   const int64_t step = gridDim.x;
   int64_t t = blockIdx.x;
   copy(0, t);
@@ -782,7 +809,7 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
         }
       }
     }
-    block_sums<6>(s, part[turn]);
+    block_sums<6>(s, part[turn], threads >> 5);
     const float rz = a.dh ? rsqrtf(s[0] * inv_h + a.eps) : 0.0f;
     const float cz = rz * rz * rz * (s[2] * inv_h);
     const float ry = a.post ? rsqrtf(s[1] * inv_h + a.eps) : 1.0f;
@@ -861,23 +888,32 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
 }
 
 // The blocks' sums, added up channel by channel: 32 channels of one of the two a
-// block, 16 warps over the blocks of the first kernel.
-__global__ void __launch_bounds__(512) norm_columns_kernel(NormArgs a, int blocks) {
+// block, its warps over the blocks of the first kernel, a batch of loads at once.
+constexpr int kColumnWarps = 16, kColumnBatch = 16;
+__global__ void __launch_bounds__(kColumnWarps * 32) norm_columns_kernel(NormArgs a, int blocks) {
   pdl_wait_then_release();
-  __shared__ float sum[16][32];
+  __shared__ float sum[kColumnWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.x * 32 + lane, which = blockIdx.y;
   float s = 0.0f;
   if (h < a.H) {
     const float* p = a.part + which * a.H + h;
-#pragma unroll 8
-    for (int b = warp; b < blocks; b += 16) s += p[(int64_t)b * 2 * a.H];
+    for (int b0 = warp; b0 < blocks; b0 += kColumnWarps * kColumnBatch) {
+      float v[kColumnBatch];
+#pragma unroll
+      for (int i = 0; i < kColumnBatch; ++i) {
+        const int b = b0 + i * kColumnWarps;
+        v[i] = b < blocks ? p[(int64_t)b * 2 * a.H] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kColumnBatch; ++i) s += v[i];
+    }
   }
   sum[warp][lane] = s;
   __syncthreads();
   if (warp || h >= a.H) return;
 #pragma unroll
-  for (int i = 1; i < 16; ++i) s += sum[i][lane];
+  for (int i = 1; i < kColumnWarps; ++i) s += sum[i][lane];
   if (which == 0) {
     if (a.dpre) a.dpre[h] = s;
     return;
@@ -888,12 +924,14 @@ __global__ void __launch_bounds__(512) norm_columns_kernel(NormArgs a, int block
     static_cast<float*>(a.dgate)[h] = a.post ? s * weight1(a.post, a.bf16, h) : s;
 }
 
-// Vectors a thread and threads a block for rows of nvec vectors.
+// Vectors a thread and threads a row for rows of nvec vectors.
 struct Shape {
   int nv, threads;
 };
+// A warp for rows of up to 128 vectors, else a block.
 Shape forward_shape(int nvec) {
-  const int nv = nvec <= 64 ? 1 : nvec <= 256 ? 2 : 4;
+  if (nvec <= 128) return {nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, 32};
+  const int nv = nvec <= 256 ? 2 : 4;
   return {nv, ((nvec + nv - 1) / nv + 31) / 32 * 32};
 }
 Shape rows_shape(int nvec) {
@@ -915,10 +953,10 @@ int backward_blocks(int64_t T, int threads, int sm_count) {
   return (int)(T < blocks ? T : blocks);
 }
 
-template <bool kF32, bool kFullGate, int kStages>
-bool launch_backward_stages(const NormArgs& a, int blocks, int threads, cudaStream_t st) {
+template <bool kF32, bool kFullGate, int kStages, bool kH, bool kY>
+bool launch_backward_parts(const NormArgs& a, int blocks, int threads, cudaStream_t st) {
   constexpr int kThreadBytes = kStages * kGradPieces<kF32> * 16;
-  const auto kernel = norm_grad_row_kernel<kF32, kFullGate, kStages>;
+  const auto kernel = norm_grad_row_kernel<kF32, kFullGate, kStages, kH, kY>;
   static std::mutex mu;
   static bool done[64] = {};
   int dev = -1;
@@ -934,6 +972,17 @@ bool launch_backward_stages(const NormArgs& a, int blocks, int threads, cudaStre
   return launch_pdl(kernel, (unsigned)blocks, threads, (size_t)threads * kThreadBytes, st, a) ==
          cudaSuccess;
 }
+// A full gate comes with y.  Without dh and without y (which then counts as 0) the
+// gradient of the block's output is a product.
+template <bool kF32, bool kFullGate, int kStages>
+bool launch_backward_stages(const NormArgs& a, int blocks, int threads, cudaStream_t st) {
+  if (!a.dh) return launch_backward_parts<kF32, kFullGate, kStages, false, true>(a, blocks, threads, st);
+  if constexpr (!kFullGate) {
+    if (!a.post && a.gate_kind == kGateNone)
+      return launch_backward_parts<kF32, false, kStages, true, false>(a, blocks, threads, st);
+  }
+  return launch_backward_parts<kF32, kFullGate, kStages, true, true>(a, blocks, threads, st);
+}
 template <bool kF32, bool kFullGate>
 bool launch_backward_rows(const NormArgs& a, int blocks, int threads, cudaStream_t st) {
   if constexpr (3 * kGradPieces<kF32> * 16 * kRowThreads > kMaxRing) {
@@ -946,7 +995,7 @@ bool launch_backward_rows(const NormArgs& a, int blocks, int threads, cudaStream
 template <int NV, bool kF32>
 bool launch_rows(const NormArgs& a, int threads, const DeviceProps& props, cudaStream_t st) {
   const auto kernel = norm_rows_kernel<NV, kF32>;
-  const size_t smem = (size_t)(kRowsAhead<NV> + 1) * NV * threads * 16;
+  const size_t smem = (size_t)(kRowsAhead + 1) * NV * threads * 16;
   static std::mutex mu;
   static bool done[64] = {};
   int dev = -1;
@@ -954,14 +1003,14 @@ bool launch_rows(const NormArgs& a, int threads, const DeviceProps& props, cudaS
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev] && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (kRowsAhead<NV> + 1) * NV * 512 * 16) != cudaSuccess)
+                                           (kRowsAhead + 1) * NV * 512 * 16) != cudaSuccess)
       return false;
     done[dev] = true;
   }
-  // blocks that fit an SM by shared memory (and 8 KB for each block's own) and threads
-  int per = (int)(props.smem_per_sm / (smem + 8192));
+  // blocks that fit an SM by shared memory (and 6 KB for each block's own) and threads
+  int per = (int)(props.smem_per_sm / (smem + 6144));
   per = per < 1024 / threads ? per : 1024 / threads;
-  per = per < 1 ? 1 : per > 16 ? 16 : per;
+  per = per < 1 ? 1 : per > 32 ? 32 : per;
   const int64_t blocks = (int64_t)per * props.sm_count;
   return launch_pdl(kernel, (unsigned)(a.T < blocks ? a.T : blocks), threads, smem, st, a) ==
          cudaSuccess;
@@ -969,7 +1018,12 @@ bool launch_rows(const NormArgs& a, int threads, const DeviceProps& props, cudaS
 template <int NV, bool kF32>
 bool launch_forward(const NormArgs& a, int threads, const DeviceProps& props, cudaStream_t st) {
   if (a.slot) return launch_rows<NV, kF32>(a, threads, props, st);
-  return launch_pdl(norm_kernel<NV, kF32>, (unsigned)a.T, threads, 0, st, a) == cudaSuccess;
+  if (threads == 32)
+    return launch_pdl(norm_kernel<NV, kF32, true>, (unsigned)((a.T + kRowWarps - 1) / kRowWarps),
+                      kRowWarps * 32, 0, st, a) == cudaSuccess;
+  if constexpr (NV > 1)
+    return launch_pdl(norm_kernel<NV, kF32, false>, (unsigned)a.T, threads, 0, st, a) == cudaSuccess;
+  return false;
 }
 
 struct Buffer {
@@ -1175,8 +1229,8 @@ extern "C" ep_status_t ep_block_norm_backward(
                                   a)) == cudaSuccess;
   }
   if (ok && columns)
-    ok = launch_pdl(norm_columns_kernel, dim3((unsigned)((hidden + 31) / 32), 2), 512, 0, st, a,
-                    blocks) == cudaSuccess;
+    ok = launch_pdl(norm_columns_kernel, dim3((unsigned)((hidden + 31) / 32), 2), kColumnWarps * 32,
+                    0, st, a, blocks) == cudaSuccess;
   if (!ok) {
     cudaGetLastError();
     return EP_ERR_CUDA;
