@@ -960,6 +960,12 @@ def _same_device(first: torch.Tensor, *others: torch.Tensor | None) -> torch.dev
     return first.device
 
 
+def _need_rows(t: torch.Tensor, name: str, layout: LLLayout):
+    if t.shape[0] < layout.num_rows:
+        raise EPError(f"{name} must have the layout's {layout.num_rows} rows (E * capacity), "
+                      f"got {t.shape[0]}")
+
+
 def _w4_shape(w: W4Weights, name: str, experts: int) -> tuple[int, int, int]:
     """Checks 4-bit weights; returns their rows, input channels and group size."""
     _need(w.q, f"{name}.q", torch.uint8)
@@ -1143,6 +1149,7 @@ def ll_combine_norm(y: torch.Tensor, topk_weights: torch.Tensor | None, layout: 
     _need(layout.ll_slot, "ll_slot", torch.int32, (T, K))
     if x.dim() != 2 or y.dim() != 2 or x.shape[0] != T or x.shape[1] != y.shape[1]:
         raise EPError(f"x must be [{T}, hidden] and y [rows, hidden]")
+    _need_rows(y, "y", layout)
     if topk_weights is not None:
         _need(topk_weights, "topk_weights", torch.float32, (T, K))
     r = _block_norm(x, y, y.shape[0], topk_weights, layout.ll_slot, gate, post_weight, pre_weight,
@@ -1235,6 +1242,7 @@ def ll_swiglu(gate_up: torch.Tensor, layout: LLLayout, topk_weights: torch.Tenso
     _need(layout.ll_slot, "ll_slot", torch.int32, (T, K))
     if gate_up.dim() != 2 or gate_up.shape[1] % 16 or gate_up.shape[1] == 0:
         raise EPError("gate_up must be [rows, 2 N] with N a multiple of 8")
+    _need_rows(gate_up, "gate_up", layout)
     rows, N = gate_up.shape[0], gate_up.shape[1] // 2
     if topk_weights is not None:
         _need(topk_weights, "topk_weights", torch.float32, (T, K))
@@ -1269,6 +1277,7 @@ def ll_swiglu_backward(dh: torch.Tensor, kept: Checkpoint8 | torch.Tensor, layou
     _need(layout.ll_slot, "ll_slot", torch.int32, (T, K))
     if dh.dim() != 2 or dh.shape[1] % 8 or dh.shape[1] == 0:
         raise EPError("dh must be [rows, N] with N a multiple of 8")
+    _need_rows(dh, "dh", layout)
     rows, N = dh.shape
     gate_up = codes = scales = None
     if isinstance(kept, Checkpoint8):

@@ -5,8 +5,10 @@
 //
 //   n = y / rms(y) * post,  z = x + scale * gate * n,  h = z / rms(z) * pre
 //
-// Forward: a block takes one token and keeps its row in registers, in 32
-// bits, between the two sums of squares.
+// Forward: a block (for short rows a warp) takes one token and keeps its row in
+// registers, in 32 bits, between the two sums of squares.  Bound by DRAM: 32768 tokens of
+// 7168 channels, bf16, 281 us (its bytes take 281); out of eight expert rows each, 4096
+// tokens, 110 us (96); one token 4.8 us, the launch and three passes through the block.
 //
 // Backward: with d = dh * pre, q = y * post * gate, r = 1 / rms and c = r_z^3
 // mean(z d),
@@ -15,7 +17,10 @@
 // The sum of q t needs t, and so the sum of z d first; but it is sum(q dz) + r_z sum(q d)
 // - c sum(q z), so one reduction of six sums serves both norms.  The sums over
 // the tokens (of dh z r_z and of t y r_y) stay in the registers of a persistent
-// block and are joined by a second kernel in a fixed order.
+// block and are joined by a second kernel in a fixed order.  Bound by DRAM and the
+// instructions (some 340 for a vector of 8 channels): 32768 tokens of 7168 channels 478 us
+// (421); 997 tokens of 2056, float32, a gate for every channel and token, 18.6 us (8), of which the
+// second kernel takes 2 to 4.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -284,6 +289,7 @@ __device__ __forceinline__ int4 lds128(uint32_t addr) {
 // row of the stream), of which several are on their way with asynchronous
 // copies, each thread's vectors into a place of its own.  The rows of
 // the tokens ahead come from lists that the first warp makes before they are read.
+// (4096 tokens of 7168 channels, eight rows each: 110 us with 3 or 4 ahead, 116 with 2, 113 with 5.)
 constexpr int kRowsAhead = 3;
 constexpr int kLists = 8;
 
@@ -928,7 +934,8 @@ __global__ void __launch_bounds__(kColumnWarps * 32) norm_columns_kernel(NormArg
 struct Shape {
   int nv, threads;
 };
-// A warp for rows of up to 128 vectors, else a block.
+// A warp for rows of up to 128 vectors, else a block (16266 tokens of 360 channels: 8.9 and
+// 17.2 us).
 Shape forward_shape(int nvec) {
   if (nvec <= 128) return {nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, 32};
   const int nv = nvec <= 256 ? 2 : 4;

@@ -126,7 +126,8 @@ bool launch_layer_up(const LayerArgs& a, int group, int blocks, cudaStream_t st)
 
 namespace {
 
-constexpr uint64_t kCodesFirst = 400 << 20;  // bytes of codes of a call
+// Bytes of codes of a call, at most, below which they leave L2 first (copy16_first).
+constexpr uint64_t kCodesFirst = 400 << 20;
 
 bool sizes_ok(int64_t T, int H, int N, int E, int K) {
   return T >= 0 && T <= kMaxTokens && H >= 32 && N >= 32 && E >= 1 &&
@@ -177,18 +178,28 @@ extern "C" ep_status_t ep_layer_w4(const void* x, int hidden, int inter, int64_t
     return EP_ERR_INVALID_ARG;
   if (workspace_bytes < ep_layer_w4_workspace_bytes(num_tokens, inter, num_topk))
     return EP_ERR_CAPACITY;
-  // The first launch still reads x and the logits while it writes, and the
-  // second writes `out` only after it: out may be x.
+  // Nothing that is written may overlap anything, but for out and x: the second launch,
+  // which writes out, does not read x.
   const uint64_t slots = (uint64_t)num_tokens * num_topk, size = logits_bf16 ? 2 : 4;
-  const uint64_t lbytes = ((num_tokens - 1) * row_stride + num_experts) * size;
   const uint64_t xbytes = (uint64_t)num_tokens * hidden * 2;
-  const struct {
+  const uint64_t all = (uint64_t)num_experts * hidden * inter;  // weights of the down projection
+  struct Buffer {
     const void* p;
     uint64_t n;
-  } outs[] = {{topk_idx, slots * 8}, {topk_weights, slots * 4}, {workspace, workspace_bytes},
-              {out, xbytes}};
+  };
+  const Buffer outs[] = {{topk_idx, slots * 8}, {topk_weights, slots * 4},
+                         {workspace, workspace_bytes}, {out, xbytes}};
+  const Buffer ins[] = {{logits, ((num_tokens - 1) * row_stride + num_experts) * size},
+                        {bias, (uint64_t)num_experts * 4},
+                        {gate_up_q, all},
+                        {gate_up_scales, 4 * all / gate_up_group},
+                        {gate_up_zeros, 2 * all / gate_up_group},
+                        {down_q, all / 2},
+                        {down_scales, 2 * all / down_group},
+                        {down_zeros, all / down_group}};
   for (int i = 0; i < 4; ++i) {
-    if (overlap(outs[i].p, outs[i].n, logits, lbytes)) return EP_ERR_INVALID_ARG;
+    for (const Buffer& b : ins)
+      if (overlap(outs[i].p, outs[i].n, b.p, b.n)) return EP_ERR_INVALID_ARG;
     if (i < 3 && overlap(outs[i].p, outs[i].n, x, xbytes)) return EP_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return EP_ERR_INVALID_ARG;

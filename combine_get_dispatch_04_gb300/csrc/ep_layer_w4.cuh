@@ -4,26 +4,35 @@
 //
 //   h[t,k] = w[t,k] * silu(G_e x[t]) * U_e x[t],  out[t] = sum_k D_e h[t,k],  e = e_k
 //
-// First launch: every block routes all tokens (a warp each) and makes the list
-// of the experts that were chosen; its warps then multiply tiles of 16 gate and
-// 16 up channels by the tokens.  Second launch: tiles of 16 output channels,
-// each summed over all chosen experts in registers, so that no expert's
-// output is ever stored.  The columns of the matrix instruction are the
-// tokens themselves: a token that did not choose an expert has zeros there.
+// First launch: every block routes all tokens (a warp each) and lists the experts
+// that were chosen, each with the tokens that chose it; its warps then multiply
+// tiles of 16 gate and 16 up channels by an entry's tokens (columns of the matrix
+// instruction; an expert with more than 8 tokens has several entries).  Second
+// launch: tiles of 16 output channels, each summed over all chosen experts in
+// shared memory, so that no expert's output is ever stored; an entry is 4 tokens, as h
+// comes in two bf16 (its rounding, and what that leaves), in columns of their own, and
+// only the layer's result is rounded noticeably.
 //
-// What bounds it is the stream of the codes.  A block takes whole tiles, and
-// its 16 warps share the tiles' steps (128 channels) evenly: each takes one
-// run of consecutive steps, keeps several steps on their way with asynchronous
-// copies, and where a tile lies in several warps' runs, its parts are added in the
-// order of the channels through shared memory.  The order of every sum depends on the sizes
-// and the choice alone, so results repeat bit for bit.
+// A block takes whole tiles, the same number on every SM but for one, and its 16
+// warps share the tiles' steps (4096 codes) evenly: each takes one run of
+// consecutive steps, keeps two steps on their way with asynchronous copies, and where a
+// tile lies in several warps' runs, its parts are added in the order of the channels
+// through shared memory.  The order of every sum depends on the sizes and the choice
+// alone, so results repeat bit for bit.
 //
 // Codes become operands with few instructions: the four bits of a code,
 // placed in the low bits of a bf16, are the number q 2^-133 (a subnormal, or
 // in the next four bits the first normal numbers, which continue the same
-// scale), and one fused multiply-add makes (q - zero) / 64 of it, exactly.  h
-// is kept as two bf16 (its rounding, and what that leaves), in columns of
-// their own, so the layer's result is rounded once.
+// scale), and one fused multiply-add makes (q - zero) / 64 of it, exactly.
+//
+// What bounds it: with many experts the stream of the codes and, nearly as long, the
+// instructions that turn them into operands, some 300 for a step; with one token also
+// what comes before and between (routing and lists 4.5 us, a launch and the way to the first
+// product 5 us).  Measured on 256 experts of 7168 -> 2 x 2048 -> 7168, 8 chosen: 16
+// tokens 353 us (the bytes take 346 if all chosen experts differ), 4 tokens 142
+// (104), 1 token 53 (27); 5 tokens on 64 experts of 4096 -> 2 x 1024, groups of 64 and zero
+// points, 56 us (26).  More stages (4: 55 us for one token) or more warps (20:
+// 58 us, registers) did not help.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -38,7 +47,6 @@ struct LayerArgs;
 // The launches (false: CUDA refused one).
 bool launch_layer_up(const LayerArgs& a, int group, int blocks, cudaStream_t st);
 bool launch_layer_down(const LayerArgs& a, int group, int blocks, cudaStream_t st);
-
 
 constexpr int kWarps = 16;  // of a block, one block an SM
 constexpr int kThreads = kWarps * 32;
@@ -142,7 +150,10 @@ __device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // The codes pass through L2 as the first to be replaced: otherwise they
-// displace what every launch needs again, the kernels' own instructions among it.
+// displace what every launch needs again, the kernels' own instructions among it.  That
+// pays for calls of few codes (one token 53.1 against 55.2 us, 5 tokens of 4096 x 1024 56.3
+// against 59.5); with many, reading ahead is faster (4 tokens 155 against 150 us, 16: 395
+// against 372).
 __device__ __forceinline__ void copy16_first(uint32_t dst, const void* src, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "l"(policy)

@@ -40,7 +40,9 @@ def test_layer_arguments(eplib):
                dict(q2=None), dict(q2=ODD), dict(s2=None), dict(z2=ODD), dict(group2=48), dict(idx=None),
                dict(idx=ODD), dict(w=None), dict(w=ODD), dict(out=None), dict(out=ODD), dict(ws=None),
                dict(ws=ODD), dict(H=1 << 16, N=1 << 16), dict(idx=at(1)), dict(w=at(2)),
-               dict(out=at(2)), dict(out=at(10)), dict(ws=at(1)), dict(w=at(7)), dict(out=at(7, 64))):
+               dict(out=at(2)), dict(out=at(10)), dict(ws=at(1)), dict(w=at(7)), dict(out=at(7, 64)),
+               dict(out=at(3)), dict(ws=at(5)), dict(idx=at(4)), dict(out=at(6, 16)),
+               dict(bias=at(11), out=at(11))):
         assert call(**kw) == BAD, kw
     need = eplib.ep_layer_w4_workspace_bytes(4, 128, 4)
     assert need > 2 * 2 * 16 * 128
@@ -65,7 +67,8 @@ def test_block_norm_arguments(eplib):
                dict(rows, K=0), dict(rows, K=33), dict(rows, rows=-1), dict(rows, rows=1 << 31),
                dict(rows, y=None), dict(rows, comb=ODD), dict(rows, comb=at(2)), dict(rows, comb=at(6)),
                dict(z=at(2)), dict(z=at(1, 64)), dict(h=at(1)), dict(h=at(2, 128)), dict(h=at(5)),
-               dict(kind=3, gate=at(5, 16))):
+               dict(kind=3, gate=at(5, 16)), dict(z=at(3)), dict(h=at(4)), dict(rows, h=at(7)),
+               dict(rows, w=at(8), z=at(8))):
         assert call(**kw) == BAD, kw
     assert call(T=0, x=None, y=None, z=None, h=None, post=None, pre=None) == 0
 
@@ -82,7 +85,8 @@ def test_block_norm_backward_arguments(eplib):
                dict(dx=ODD), dict(dy=ODD), dict(dgate=at(13)), dict(dpost=ODD), dict(dpre=ODD),
                dict(dz=None, dh=None, pre=None, dpre=None), dict(dx=at(1)), dict(dx=at(3, 16)),
                dict(dy=at(4)), dict(dy=at(2, 64)), dict(dy=at(7)), dict(ws=ODD),
-               dict(kind=3, gate=at(9), dgate=at(9))):
+               dict(kind=3, gate=at(9), dgate=at(9)), dict(dpost=at(5)), dict(dpre=at(10)), dict(ws=at(7)),
+               dict(dx=at(6))):
         assert call(**kw) == BAD, kw
     for bad in ((0, 64), (-1, 64), (4, 12), (4, 1 << 15)):
         assert eplib.ep_block_norm_backward_workspace_bytes(*bad) == 0
@@ -94,7 +98,8 @@ def test_swiglu_arguments(eplib):
     for kw in (dict(gu=None), dict(gu=ODD), dict(N=0), dict(N=12), dict(N=64), dict(N=136), dict(rows=-1),
                dict(rows=1 << 31), dict(T=-1), dict(K=0), dict(K=33), dict(T=1 << 30, K=8), dict(slot=None),
                dict(h=None), dict(h=ODD), dict(c=None), dict(s=None), dict(c=ODD), dict(s=ODD),
-               dict(h=at(1)), dict(c=at(1, 16)), dict(s=at(3)), dict(c=at(3)), dict(s=at(4, 32))):
+               dict(h=at(1)), dict(c=at(1, 16)), dict(s=at(3)), dict(c=at(3)), dict(s=at(4, 32)), dict(h=at(2)),
+               dict(w=at(6), c=at(6))):
         assert call(**kw) == BAD, kw
     assert call(T=0, gu=None, slot=None, h=None) == 0
 
@@ -103,6 +108,7 @@ def test_swiglu_arguments(eplib):
     for kw in (dict(dh=None), dict(dh=ODD), dict(gu=at(8)), dict(c=None), dict(s=None), dict(c=None, s=None),
                dict(c=ODD), dict(s=ODD), dict(N=64), dict(N=0), dict(rows=-1), dict(T=-1), dict(K=33),
                dict(slot=None), dict(d=None), dict(d=ODD), dict(d=at(1)), dict(d=at(2, 16)),
-               dict(d=at(3)), dict(c=None, s=None, gu=at(6)), dict(c=None, s=None, gu=ODD)):
+               dict(d=at(3)), dict(c=None, s=None, gu=at(6)), dict(c=None, s=None, gu=ODD), dict(d=at(4)),
+               dict(dw=at(4)), dict(dw=at(5)), dict(dw=at(6))):
         assert back(**kw) == BAD, kw
     assert back(T=0, dh=None, d=None, slot=None) == 0

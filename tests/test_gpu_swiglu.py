@@ -238,7 +238,8 @@ def test_no_tokens_and_arguments(ep):
            lambda: ep.ll_swiglu(gu.cpu(), L), lambda: ep.alloc_checkpoint8(4, 100, gu.device),
            lambda: ep.ll_swiglu_backward(dh, gu, L, out=gu), lambda: ep.ll_swiglu_backward(dh, short, L),
            lambda: ep.ll_swiglu_backward(dh, gu[:-1], L), lambda: ep.ll_swiglu_backward(gu, gu, L),
-           lambda: ep.ll_swiglu_backward(dh, kept, L, w.double())]
+           lambda: ep.ll_swiglu_backward(dh, kept, L, w.double()),
+           lambda: ep.ll_swiglu(gu[:-1], L), lambda: ep.ll_swiglu_backward(dh[:-1], gu[:-1], L)]
     for i, call in enumerate(bad):
         with pytest.raises(ep.EPError):
             call()
