@@ -46,7 +46,7 @@ __device__ void route_all(const LayerArgs& a, float* scratch, int64_t* idx, floa
 
 // The entries, each of at most `most` tokens, of the experts in the order of
 // their first slots.  A thread looks through all slots for those that name its slot's
-// expert; the code is short on purpose (below).
+// expert; the code is short on purpose, as route_all's is.
 __device__ void make_lists(const LayerArgs& a, const int* idx, int* sums, int most, Lists& l) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.route.K;
   static_assert(kMaxSlots <= kThreads, "a thread for every slot");

@@ -251,6 +251,20 @@ def test_backward_rows_of_zeros_and_no_tokens(ep):
     assert r.z.shape == r.h.shape == (0, 256)
 
 
+@pytest.mark.parametrize("H", [512, 7176])
+@pytest.mark.parametrize("zs,ys,use_dz", [(1e15, 1e15, True), (1e15, 1.0, False), (1e12, 1e12, False),
+                                          (1e-14, 1.0, True), (1.0, 1e-14, True)])
+def test_backward_of_large_and_small_rows(ep, H, zs, ys, use_dz):
+    """Rows whose 1 / rms cubed is not a 32-bit number have the same relative bounds."""
+    s = inputs(7, H, "token", F32, F32, seed=6)
+    z, y = s["x"] * zs, (s["y"].float() * ys).to(BF16)
+    dz = rand(s["gen"], 7, H) if use_dz else None
+    dh = rand(s["gen"], 7, H, dtype=BF16)
+    r = ep.block_norm_backward(dz, dh, z, y, gate=s["gate"], post_weight=s["post"],
+                               pre_weight=s["pre"], eps=1e-30)
+    check_backward(r, dz, dh, z, y, s["gate"], s["post"], s["pre"], 1.0, 1e-30)
+
+
 def test_formula_agrees_with_differences():
     """The 64-bit gradient against central differences (error h^2 / 6 of a third
     derivative, and 1e-16 / h of the values)."""
