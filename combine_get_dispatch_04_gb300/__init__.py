@@ -1129,7 +1129,7 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *,
         raise EPError("nothing to compute without y and without pre_weight")
     if y is not None:
         _need(y, "y", torch.bfloat16, x.shape)
-    r = _block_norm(x, y, x.shape[0], None, None, gate, post_weight, pre_weight, scale, eps, False,
+    r = _block_norm(x, y, 0, None, None, gate, post_weight, pre_weight, scale, eps, False,
                     None, out)
     _debug_check("block_norm", None, x.device)
     return r

@@ -112,3 +112,15 @@ def test_swiglu_arguments(eplib):
                dict(dw=at(4)), dict(dw=at(5)), dict(dw=at(6))):
         assert back(**kw) == BAD, kw
     assert back(T=0, dh=None, d=None, slot=None) == 0
+
+
+def test_streams_without_rows_are_refused(eplib):
+    import torch
+
+    import combine_get_dispatch_04_gb300 as ep
+    w = torch.ones(8)
+    for x in (torch.zeros(()), torch.zeros(8)):
+        for call in (lambda: ep.block_norm(x, pre_weight=w), lambda: ep.block_norm(x, x),
+                     lambda: ep.block_norm_backward(x, None, x)):
+            with pytest.raises(ep.EPError):
+                call()
