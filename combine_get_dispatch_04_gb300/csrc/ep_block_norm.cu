@@ -668,7 +668,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
           u = mul2(u, g[k]);
         }
         cpost[k] = fma2(u, y, cpost[k]);  // without the channel's gate, which the second kernel knows
-        u = fma2(u, q[k], mul2(y, -cy));
+        // without the norm after the block y is not part of its own gradient: 0 y would be, where
+        // y is not finite
+        u = a.post ? fma2(u, q[k], mul2(y, -cy)) : mul2(u, q[k]);
       }
       (&dy4.x)[k] = (int)pack2(u);
       if (kF32)
