@@ -486,8 +486,12 @@ template <bool kF32>
 constexpr int kGradPieces = kF32 ? 6 : 4;  // 16-byte pieces of a thread's vectors of a row
 
 // kStages: rows in shared memory, 3 (one row's second half with the next one's first) or 2.
-// kH: with dh (the norm before the next block), kY: with y (the norm after the block or a gate).
-template <bool kF32, bool kFullGate, int kStages, bool kH, bool kY>
+// kH: with dh (the norm before the next block), kY: with y (the norm after the block or a gate),
+// kPost: with the norm after the block.  Without that y is not part of its own gradient, not even
+// as 0 y, which is NaN where y is not finite.  (A branch instead of instances for that: 16384 tokens
+// of 7168, float32, 395 against 379 us.  In the sums a branch on the weight is the faster: with
+// instances 16384 tokens of 4096, float32, 204 against 188 us, of spills.)
+template <bool kF32, bool kFullGate, int kStages, bool kH, bool kY, bool kPost>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs a) {
   constexpr int kPieces = kGradPieces<kF32>, kS = kF32 ? 2 : 1;
   constexpr bool kOverlap = kStages == 3;
@@ -668,9 +672,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
           u = mul2(u, g[k]);
         }
         cpost[k] = fma2(u, y, cpost[k]);  // without the channel's gate, which the second kernel knows
-        // without the norm after the block y is not part of its own gradient: 0 y would be, where
-        // y is not finite
-        u = a.post ? fma2(u, q[k], mul2(y, -cy)) : mul2(u, q[k]);
+        u = kPost ? fma2(u, q[k], mul2(y, -cy)) : mul2(u, q[k]);
       }
       (&dy4.x)[k] = (int)pack2(u);
       if (kF32)
@@ -973,10 +975,10 @@ int backward_blocks(int64_t T, int threads, int sm_count) {
   return (int)(T < blocks ? T : blocks);
 }
 
-template <bool kF32, bool kFullGate, int kStages, bool kH, bool kY>
+template <bool kF32, bool kFullGate, int kStages, bool kH, bool kY, bool kPost>
 bool launch_backward_parts(const NormArgs& a, int blocks, int threads, cudaStream_t st) {
   constexpr int kThreadBytes = kStages * kGradPieces<kF32> * 16;
-  const auto kernel = norm_grad_row_kernel<kF32, kFullGate, kStages, kH, kY>;
+  const auto kernel = norm_grad_row_kernel<kF32, kFullGate, kStages, kH, kY, kPost>;
   static std::mutex mu;
   static bool done[64] = {};
   int dev = -1;
@@ -996,12 +998,15 @@ bool launch_backward_parts(const NormArgs& a, int blocks, int threads, cudaStrea
 // gradient of the block's output is a product.
 template <bool kF32, bool kFullGate, int kStages>
 bool launch_backward_stages(const NormArgs& a, int blocks, int threads, cudaStream_t st) {
-  if (!a.dh) return launch_backward_parts<kF32, kFullGate, kStages, false, true>(a, blocks, threads, st);
   if constexpr (!kFullGate) {
-    if (!a.post && a.gate_kind == kGateNone)
-      return launch_backward_parts<kF32, false, kStages, true, false>(a, blocks, threads, st);
+    if (a.dh && !a.post && a.gate_kind == kGateNone)
+      return launch_backward_parts<kF32, false, kStages, true, false, false>(a, blocks, threads, st);
   }
-  return launch_backward_parts<kF32, kFullGate, kStages, true, true>(a, blocks, threads, st);
+  if (a.post)
+    return a.dh ? launch_backward_parts<kF32, kFullGate, kStages, true, true, true>(a, blocks, threads, st)
+                : launch_backward_parts<kF32, kFullGate, kStages, false, true, true>(a, blocks, threads, st);
+  return a.dh ? launch_backward_parts<kF32, kFullGate, kStages, true, true, false>(a, blocks, threads, st)
+              : launch_backward_parts<kF32, kFullGate, kStages, false, true, false>(a, blocks, threads, st);
 }
 template <bool kF32, bool kFullGate>
 bool launch_backward_rows(const NormArgs& a, int blocks, int threads, cudaStream_t st) {
