@@ -39,7 +39,7 @@ __device__ void route_all(const LayerArgs& a, float* scratch, int64_t* idx, floa
   r.idx = idx;
   r.w = w;
   float m, z;
-  choose_in_shared<false, 1>(r, warp, lane, key, gscore, slot, m, z);
+  choose_in_shared<false, 1>(r, warp, lane, a.route_run, key, gscore, slot, m, z);
   __syncwarp();
   write_slots<32, false>(r, warp, true, lane, slot, score, m, z);
 }
@@ -209,6 +209,7 @@ extern "C" ep_status_t ep_layer_w4(const void* x, int hidden, int inter, int64_t
              topk_groups, score == EP_SCORE_SIGMOID, renormalize != 0, scale, topk_idx,
              topk_weights};
   if (a.route.keep == a.route.G) a.route.G = a.route.keep = 1;  // every group is kept
+  a.route_run = route_tile(num_experts, a.route.G).vpl;
   a.logits_bf16 = logits_bf16 != 0;
   a.x = static_cast<const uint8_t*>(x);
   a.T = (int)num_tokens;

@@ -79,6 +79,7 @@ struct Weights {
 
 struct LayerArgs {
   RouteArgs route;
+  int route_run;  // of choose_in_shared: the router's own
   bool logits_bf16;
   const uint8_t* x;
   int T, H, N;

@@ -205,7 +205,7 @@ __global__ void route_any_kernel(RouteArgs a) {
   int* slots = reinterpret_cast<int*>(gscore + kMaxGroups);
   float* score = reinterpret_cast<float*>(slots + EP_MAX_TOPK);
   float m, z;
-  choose_in_shared<kBF16, 4>(a, t, lane, key, gscore, slots, m, z);
+  choose_in_shared<kBF16, 4>(a, t, lane, 0, key, gscore, slots, m, z);
   write_slots<32, kBF16>(a, t, true, lane, slots, score, m, z);
 }
 
@@ -394,20 +394,6 @@ template <bool kBF16>
 void launch_route(const RouteArgs& a, int sm_count, cudaStream_t st) {
   const int size = a.E / a.G;
   const bool vec = a.E % 8 == 0 && aligned16(a.logits) && a.stride * (kBF16 ? 2 : 4) % 16 == 0;
-  // The first tile below that holds E and, with groups, splits them into a power
-  // of two of whole lanes.  Tiles of eight experts a lane, which are loaded in
-  // 16-byte vectors, come first, from few lanes a token to many: 32768 float32
-  // tokens of 16 / 64 / 128 experts, 8 chosen (of 16: 4), take 4.4 / 10.5 / 19.3 us,
-  // and 21 / 26 / 26 with 32 lanes each.  Then other widths of 32 lanes, for sizes
-  // and groups that eight does not divide and up to 512 experts (384: 74 us), then
-  // the keys in shared memory (600: 85 us).
-  const auto fits = [&](int lanes, int vpl) {
-    if (a.E > lanes * vpl) return false;
-    if (a.G == 1) return true;
-    if (size % vpl) return false;
-    const int n = size / vpl;
-    return (n & (n - 1)) == 0 && n <= lanes;
-  };
   if (kBF16 && !a.sigmoid && !a.bias && a.G == 1 && a.K <= kBest && a.E <= 8 * kChunks * 32) {
     // the fewest lanes that hold E, so that most of the joining is a lane's
     // own, unless there are too few tokens for every scheduler to have a warp
@@ -434,8 +420,9 @@ void launch_route(const RouteArgs& a, int sm_count, cudaStream_t st) {
     }
 #undef EP_ROUTE_SORT
   }
+  const RouteTile tile = route_tile(a.E, a.G);
 #define EP_ROUTE_CASE(L, V)                                                              \
-  if (fits(L, V)) {                                                                      \
+  if (tile.lanes == L && tile.vpl == V) {                                                \
     const int64_t per = kWarps * (32 / L);                                               \
     launch_pdl(route_kernel<L, V, kBF16>, (unsigned)((a.T + per - 1) / per), kWarps * 32, \
                0, st, a, a.G > 1 ? size / V : L, vec);                                   \

@@ -717,7 +717,8 @@ void ep_debug_set_experts_stall(int step);
  * ep_route, ep_ll_get_dispatch_layout, ep_ll_dispatch, ep_ll_experts_w4 (twice)
  * and ep_ll_combine compute one after the other.
  *
- *   e_k, w_k  the choice and the weights of ep_route for the logits' row
+ *   e_k, w_k  the choice of ep_route for the logits' row, the same experts in every case, and its
+ *             weights (sums of a token's weights may be added up in another order)
  *   h_k[n]  = w_k * silu(G_{e_k} x)[n] * (U_{e_k} x)[n]
  *   out     = bf16_rne( sum_k D_{e_k} h_k )
  *
