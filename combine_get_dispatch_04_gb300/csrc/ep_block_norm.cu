@@ -106,22 +106,42 @@ __device__ __forceinline__ void st_stream_32(void* p, const float (&f)[8]) {
                : "memory");
 }
 
+// The same of memory that this kernel may write later: not through the read-only path.
+__device__ __forceinline__ void ld_written_32(const void* p, int4 (&v)[2]) {
+  asm volatile(
+      "ld.global.L1::no_allocate.L2::256B.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y),
+        "=r"(v[1].z), "=r"(v[1].w)
+      : "l"(p));
+}
+__device__ __forceinline__ int4 ld_written_16(const int4* p) {
+  int4 v;
+  asm volatile("ld.global.L1::no_allocate.L2::256B.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // Eight values of the stream, read once.  Float32 ones are two 16-byte pieces, or one of 32 where
-// the buffer allows it: L2 sees every sector twice otherwise.
+// the buffer allows it: L2 sees every sector twice otherwise.  kWritten: the kernel may write
+// them in place, each thread its own after it has read them.
 template <bool kF32>
 struct Stream8 {
   int4 v[kF32 ? 2 : 1];
+  template <bool kWritten>
   __device__ __forceinline__ void load(const void* p, int64_t at) {
+    const int4* q = static_cast<const int4*>(p) + at * (kF32 ? 2 : 1);
     if constexpr (kF32) {
-      const int4* q = static_cast<const int4*>(p) + 2 * at;
       if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {  // the same for all threads
-        ld_stream_32(q, v);
+        if (kWritten)
+          ld_written_32(q, v);
+        else
+          ld_stream_32(q, v);
         return;
       }
     }
 #pragma unroll
-    for (int i = 0; i < (kF32 ? 2 : 1); ++i)
-      v[i] = ld_stream_v4(static_cast<const int4*>(p) + at * (kF32 ? 2 : 1) + i);
+    for (int i = 0; i < (kF32 ? 2 : 1); ++i) v[i] = kWritten ? ld_written_16(q + i) : ld_stream_v4(q + i);
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -261,7 +281,7 @@ __global__ void __launch_bounds__(kWarpRow ? kRowWarps * 32 : 512) norm_kernel(N
     xv[i].zero();
     yv[i] = make_int4(0, 0, 0, 0);
     if (v < a.nvec) {
-      xv[i].load(a.x, base + v);
+      xv[i].template load<true>(a.x, base + v);  // z may be x
       if (a.y) yv[i] = ld_stream_v4(reinterpret_cast<const int4*>(a.y) + base + v);
     }
   }
@@ -773,8 +793,8 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
       dzv[i].zero();
       yv[i] = dhv[i] = make_int4(0, 0, 0, 0);
       if (v < a.nvec) {
-        if (a.dh) zv[i].load(a.x, base + v);
-        if (a.dz) dzv[i].load(a.dz, base + v);
+        if (a.dh) zv[i].template load<false>(a.x, base + v);
+        if (a.dz) dzv[i].template load<false>(a.dz, base + v);
         if (need_y) yv[i] = ld_stream_v4(reinterpret_cast<const int4*>(a.y) + base + v);
         if (a.dh) dhv[i] = ld_stream_v4(reinterpret_cast<const int4*>(a.dh) + base + v);
       }
