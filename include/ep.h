@@ -834,6 +834,7 @@ ep_status_t ep_block_norm_backward(const void* dz, const void* dh, const void* z
  *   codes[row], scales[row] = g and u as E4M3 with one scale per 128 channels,
  *                 rounded as ep_dispatch rounds its rows (use_fp8); a block of 128
  *                 that holds an infinity or a NaN reads back as NaN throughout
+ * All arithmetic is float32, and every output is rounded once (exp(-|g|) below 2^-126 counts as 0).
  * With the weights here, the combine takes none (topk_weights NULL), and the
  * gradient of the weights comes from these rows instead of the experts' outputs.
  * In (device): gate_up [num_rows, 2N] bf16; topk_weights [T, K] float32
@@ -853,6 +854,7 @@ ep_status_t ep_ll_swiglu(const void* gate_up, int inter, int64_t num_rows,
  * itself (codes and scales NULL).  With s = 1 / (1 + exp(-g)):
  *   dgate_up[row] = [ w dh u s (1 + g (1 - s)) | w dh g s ]     (bf16, rounded once)
  *   dweights[t][k] = sum_n dh g s u     (float32; 0 for a slot without a row)
+ * All arithmetic is float32, as above.
  * In (device): dh [num_rows, N] bf16; the rest as ep_ll_swiglu.
  * Out (device): dgate_up [num_rows, 2N] bf16: rows that no slot names are not
  *   touched; dweights [T, K] float32 (nullable), every element written.
