@@ -769,7 +769,9 @@ ep_status_t ep_layer_w4(const void* x, int hidden, int inter, int64_t num_tokens
  * expert-major layout, which are combined first, as by ep_ll_combine but without
  * its rounding: y[t] = sum over slots k with ll_slot[t][k] >= 0 of w[t][k] * rows[ll_slot[t][k]].
  * h is made from z before its rounding.  All arithmetic is float32, and every
- * output is rounded once.  (Squares of magnitudes beyond 2^63 overflow.)
+ * output is rounded once.  A row's sum of squares, of y or of z, has to stay below 2^128: a row
+ * of one magnitude v reaches that at v = 2^64 / sqrt(H) (2^57 for H = 16384), and from there on
+ * its 1 / rms counts as 0.
  * In (device): x [T, H] bf16, or (stream_f32 != 0) float32; y [T, H] or
  *   [num_rows, H] bf16 (NULL without ll_slot: no block's output, h = x / rms(x) *
  *   pre_weight); ll_slot [T, K] int32 and topk_weights [T, K] float32 (nullable: 1
@@ -807,6 +809,8 @@ ep_status_t ep_block_norm(const void* x, int stream_f32, const void* y, int64_t 
  *   dy    = r_y dn post_weight - r_y^3 mean(y dn post_weight) y   (dn without a post_weight)
  *   dpre  = sum_t dh z r_z,  dpost = sum_t dn y r_y
  *   dgate = scale * n * dx, summed over what the gate is shared by
+ * Beside the sums of squares, a row's sums of the products z d, q dz, q d and q z with q = y *
+ * post_weight * gate have to stay below 2^128.
  * Either of dz and dh may be NULL (zero; dh is NULL if and only if pre_weight is);
  * z may be NULL without dh, y without post_weight and gate.
  * Out (device): dx [T, H] of the stream's type; dy [T, H] bf16, dpost_weight and
