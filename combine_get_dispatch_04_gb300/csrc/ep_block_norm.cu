@@ -1141,7 +1141,8 @@ extern "C" ep_status_t ep_block_norm(const void* x, int stream_f32, const void* 
   if (!block && (post_weight || gate_kind != kGateNone)) return EP_ERR_INVALID_ARG;
   if (ll_slot && num_rows > 0 && !y) return EP_ERR_INVALID_ARG;
   if (!gate != (gate_kind == kGateNone)) return EP_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(y) || !aligned16(z) || !aligned16(h) || !aligned16(combined))
+  if (!aligned16(x) || !aligned16(y) || !aligned16(z) || !aligned16(h) || !aligned16(combined) ||
+      !aligned4(ll_slot) || !aligned4(topk_weights) || !aligned4(err_word))
     return EP_ERR_INVALID_ARG;
   // a token's outputs are written while others still read: nothing may overlap,
   // but z may be x itself, which each token reads before it writes

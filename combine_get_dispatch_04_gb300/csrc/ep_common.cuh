@@ -19,6 +19,7 @@ namespace ep {
 inline cudaStream_t to_cuda(ep_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Whether two buffers of these sizes (in bytes; a null one: none) share a byte.
 inline bool overlap(const void* p, uint64_t pn, const void* q, uint64_t qn) {

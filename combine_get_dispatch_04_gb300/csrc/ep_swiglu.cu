@@ -273,7 +273,8 @@ extern "C" ep_status_t ep_ll_swiglu(const void* gate_up, int inter, int64_t num_
     return EP_ERR_INVALID_ARG;
   if (num_tokens == 0) return EP_OK;
   if (!ll_slot || (num_rows > 0 && (!gate_up || !h))) return EP_ERR_INVALID_ARG;
-  if (!aligned16(gate_up) || !aligned16(h) || !aligned16(codes) || !aligned16(scales))
+  if (!aligned16(gate_up) || !aligned16(h) || !aligned16(codes) || !aligned16(scales) ||
+      !aligned4(ll_slot) || !aligned4(topk_weights) || !aligned4(err_word))
     return EP_ERR_INVALID_ARG;
   // no output may overlap an input or another output
   const uint64_t n = (uint64_t)num_rows * inter, in = 4 * n, hn = 2 * n, cn = 2 * n, sn = n / 16;
@@ -321,7 +322,8 @@ extern "C" ep_status_t ep_ll_swiglu_backward(const void* dh, const void* gate_up
   if (!ll_slot || (num_rows > 0 && (!dh || !dgate_up || (!gate_up && !codes))))
     return EP_ERR_INVALID_ARG;
   if (!aligned16(gate_up) || !aligned16(dh) || !aligned16(codes) || !aligned16(scales) ||
-      !aligned16(dgate_up))
+      !aligned16(dgate_up) || !aligned4(ll_slot) || !aligned4(topk_weights) ||
+      !aligned4(dweights) || !aligned4(err_word))
     return EP_ERR_INVALID_ARG;
   const uint64_t n = (uint64_t)num_rows * inter, slots = (uint64_t)num_tokens * num_topk * 4;
   const struct {
