@@ -8,7 +8,8 @@ Training: the same block with bf16 weights, forward and backward.  What the
 activation's gradient needs is kept in 8 bits, half of what bf16 takes; the top-k
 weights are applied to the activation, so the combine takes none, and the gradient goes
 back through the norms, the combine, the experts and the router to the stream and to
-every weight.
+every weight.  For those of the experts' weights the activation is kept in bf16 and the
+experts' input rows are dispatched again; in both, rows that no token fills are zeros.
 
     python examples/moe_block.py [--tokens 4] [--train-tokens 512] [--hidden 2048] ...
 """
@@ -50,39 +51,47 @@ class MoEBlock:
                              scale=self.scale, out=x).h
 
     # --- training -------------------------------------------------------------------
+    def rows(self, x, L):
+        """The experts' rows of x [T, H], zeros where no token goes."""
+        out = ep.LLDispatched(x.new_zeros(L.num_rows, x.shape[1]), None,
+                              torch.empty(L.num_rows, dtype=torch.int32, device=x.device), False)
+        return ep.ll_dispatch(x, L, out=out).recv_x.view(self.experts, L.expert_capacity, -1)
+
     def forward(self, x):
         """x [T, H], the stream (bf16 or float32).  Returns z, h and what backward needs."""
         h = ep.block_norm(x, pre_weight=self.before).h
         logits = (h @ self.router.t()).float()
         idx, w = ep.route(logits, self.topk)
         L = ep.ll_get_dispatch_layout(idx, self.experts, 1)
-        rows = ep.ll_dispatch(h, L).recv_x
-        each = lambda v: v.view(self.experts, L.expert_capacity, -1)  # noqa: E731
-        gate_up = torch.bmm(each(rows), self.w13.transpose(1, 2)).flatten(0, 1)
+        gate_up = torch.bmm(self.rows(h, L), self.w13.transpose(1, 2)).flatten(0, 1)
         kept = ep.alloc_checkpoint8(L.num_rows, gate_up.shape[1], x.device)
-        a = ep.ll_swiglu(gate_up, L, w, checkpoint=kept)
-        y = torch.bmm(each(a), self.w2.transpose(1, 2)).flatten(0, 1)
+        a = ep.ll_swiglu(gate_up, L, w, checkpoint=kept,
+                         out=gate_up.new_zeros(L.num_rows, gate_up.shape[1] // 2))
+        a = a.view(self.experts, L.expert_capacity, -1)
+        y = torch.bmm(a, self.w2.transpose(1, 2)).flatten(0, 1)
         r = ep.ll_combine_norm(y, None, L, x, gate=self.gate, post_weight=self.post,
                                pre_weight=self.after, scale=self.scale, save=True)
-        return r.z, r.h, (x, h, logits, idx, w, L, kept, r.z, r.y)
+        return r.z, r.h, (x, h, logits, idx, w, L, kept, r.z, r.y, a)
 
     def backward(self, dz, dh, saved):
-        """Gradients of x and of the weights, from those of z and of the next block's h."""
-        x, h, logits, idx, w, L, kept, z, y = saved
-        each = lambda v: v.view(self.experts, L.expert_capacity, -1)  # noqa: E731
+        """Gradients of x, of the weights and of the experts' rows (gate_up, y), from those of z
+        and of the next block's h."""
+        x, h, logits, idx, w, L, kept, z, y, a = saved
         g = ep.block_norm_backward(dz, dh, z, y, gate=self.gate, post_weight=self.post,
                                    pre_weight=self.after, scale=self.scale)
         # of a combine without weights: every row gets its token's gradient
-        dy = ep.ll_dispatch(g.dy, L).recv_x
-        da = torch.bmm(each(dy), self.w2).flatten(0, 1)
+        dy = self.rows(g.dy, L)
+        da = torch.bmm(dy, self.w2).flatten(0, 1)
         d13, dw = ep.ll_swiglu_backward(da, kept, L, w)
-        drows = torch.bmm(each(d13), self.w13).flatten(0, 1)
+        d13 = d13.view(self.experts, L.expert_capacity, -1)
+        drows = torch.bmm(d13, self.w13).flatten(0, 1)
         dlogits = ep.route_backward(dw, logits, idx)
         dh = ep.ll_combine(drows, None, L) + dlogits.to(h.dtype) @ self.router
         first = ep.block_norm_backward(g.dx, dh, x, pre_weight=self.before)
         grads = dict(before=first.dpre_weight, after=g.dpre_weight, post=g.dpost_weight, gate=g.dgate,
-                     router=dlogits.t() @ h.float())
-        return first.dx, grads, (d13, dy)  # with the rows, those of w13 and w2
+                     router=dlogits.t() @ h.float(), w13=torch.bmm(d13.transpose(1, 2), self.rows(h, L)),
+                     w2=torch.bmm(dy.transpose(1, 2), a))
+        return first.dx, grads, (d13, dy)
 
 
 def main():
