@@ -310,7 +310,7 @@ __device__ __forceinline__ int4 lds128(uint32_t addr) {
 // row of the stream), of which several are on their way with asynchronous
 // copies, each thread's vectors into a place of its own.  The rows of
 // the tokens ahead come from lists that the first warp makes before they are read.
-// (4096 tokens of 7168 channels, eight rows each: 110 us with 3 or 4 ahead, 116 with 2, 113 with 5.)
+// (4096 tokens of 7168 channels, eight rows each: 109 us with 3 or 4 ahead, 116 with 2, 113 with 5.)
 constexpr int kRowsAhead = 3;
 constexpr int kLists = 8;
 
@@ -767,7 +767,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_grad_row_kernel(NormArgs 
   p[1] = make_float4(cpost[2].x, cpost[2].y, cpost[3].x, cpost[3].y);
 }
 
-// Longer rows: NV vectors a thread, loaded when their token's turn comes.
+// Longer rows: NV vectors a thread, loaded when their token's turn comes.  Bound by that wait and by
+// spills (the values of four vectors take more than the 128 registers, some 650 bytes): 8192 tokens of
+// 8192 channels 408 us (their bytes 120), float32 464 (180), of 16384 channels 681 (240).
 template <int NV, bool kF32>
 __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a) {
   pdl_wait_then_release();

@@ -25,14 +25,16 @@
 // in the next four bits the first normal numbers, which continue the same
 // scale), and one fused multiply-add makes (q - zero) / 64 of it, exactly.
 //
-// What bounds it: with many experts the stream of the codes and, nearly as long, the
-// instructions that turn them into operands, some 300 for a step; with one token also
-// what comes before and between (routing and lists 4.5 us, a launch and the way to the first
-// product 5 us).  Measured on 256 experts of 7168 -> 2 x 2048 -> 7168, 8 chosen: 16
-// tokens 353 us (the bytes take 346 if all chosen experts differ), 4 tokens 142
-// (104), 1 token 53 (27); 5 tokens on 64 experts of 4096 -> 2 x 1024, groups of 64 and zero
-// points, 56 us (26).  More stages (4: 55 us for one token) or more warps (20:
-// 58 us, registers) did not help.
+// What bounds it: with many experts the latencies of a step (some 300 instructions a lane) at
+// four warps a scheduler: 61 to 64% of the issue slots, no pipe above 62%, 4.7 TB/s in the first
+// launch and 3.7 in the second; with one token also what comes before and between (routing and
+// lists 4.5 us, a launch and the way to the first product 5 us).  Measured on 256 experts
+// of 7168 -> 2 x 2048 -> 7168, 8 chosen by a router with a bias that all tokens share: 16
+// tokens 354 us (they choose 70 experts, whose bytes take 237), 8 tokens 232 (46, 156), 4
+// tokens 142 (27, 93), 1 token 53 (27 us); 5 tokens on 64 experts of 4096 -> 2 x 1024, groups of 64 and zero
+// points, 56 us (26).  A further entry of an expert reads its codes again (8 experts of
+// 4096 -> 2 x 4096, 2 chosen, 16 tokens: 70 us for 31).  More stages (4: 55 us for one
+// token) or more warps (20: 58 us, registers) did not help.
 #pragma once
 
 #include <cuda_bf16.h>
