@@ -8,7 +8,7 @@
 // The rows are found through the slots, so the weight of a row is the slot's,
 // and rows that no slot names are neither read nor written.
 //
-// Bound by DRAM, with the instructions close behind (some 29 a channel of the gradient).
+// Bound by DRAM, with the instructions close behind (some 30 a channel of the gradient).
 // Measured: 32768 rows of 2 x 4096 channels with checkpoint, 168 us (its bytes take 162);
 // gradient of 262144 rows of 2 x 2048 from codes, 741 us (646), of 131072 from bf16, 420 (401).
 #include <cuda_bf16.h>
